@@ -22,6 +22,8 @@ __all__ = [
     "moe_plan_query", "moe_mlp_workspace_bytes", "moe_mlp_swiglu", "moe_mlp_swiglu_timed",
     "moe_mlp_set_spin_limit", "moe_mlp_gave_up", "moe_mlp_plan_query", "MOE_MLP_COUNTER_BYTES",
     "MOE_X_PER_ROUTE", "MOE_SWIGLU", "MAX_TOPK", "KERNEL_NAMES",
+    "KV_BF16", "KV_FP8", "KvCache", "KvBatch", "make_kv_cache", "make_batch", "kv_append",
+    "kv_attention", "kv_attention_workspace_bytes",
 ]
 
 BF16 = 0
@@ -41,6 +43,8 @@ KERNEL_NAMES = {1: "skinny_rows", 2: "skinny_rows (lean)", 3: "skinny_rows_flat"
                 4: "skinny_tiles", 5: "skinny_tiles (8-wave)", 6: "skinny_tiles (K-split)",
                 7: "skinny_moe_mlp1"}
 STATIC_SCRATCH_BYTES = 64 << 20
+KV_BF16 = 0
+KV_FP8 = 1
 MOE_MLP_COUNTER_BYTES = 256   # moe_mlp_swiglu's workspace: counter and flag, then gate_up outputs
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -75,6 +79,21 @@ class Experts(ctypes.Structure):
     """struct skinny_experts"""
     _fields_ = [("dtype", ctypes.c_int), ("E", ctypes.c_int), ("N", ctypes.c_int),
                 ("K", ctypes.c_int), ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    """struct skinny_kv_cache"""
+    _fields_ = [("dtype", ctypes.c_int), ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("reserved", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class KvBatch(ctypes.Structure):
+    """struct skinny_kv_batch"""
+    _fields_ = [("seqs", ctypes.c_int), ("tokens", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("reserved", ctypes.c_int), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
 class Plan(ctypes.Structure):
@@ -151,6 +170,13 @@ def _bind(path: str):
     L.skinny_moe_mlp_plan_query.argtypes = [ep, ep, i, i, ctypes.POINTER(Plan)]
     L.skinny_moe_mlp_set_spin_limit.restype = None
     L.skinny_moe_mlp_set_spin_limit.argtypes = [ctypes.c_longlong]
+    cp, bp = ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch)
+    L.skinny_kv_append.restype = i
+    L.skinny_kv_append.argtypes = [cp, bp, vp, i, vp, i, i, vp, vp]
+    L.skinny_kv_attention_workspace_bytes.restype = sz
+    L.skinny_kv_attention_workspace_bytes.argtypes = [cp, bp, i]
+    L.skinny_kv_attention.restype = i
+    L.skinny_kv_attention.argtypes = [cp, bp, vp, i, ctypes.c_float, vp, vp, sz, vp]
     L.skinny_status_string.restype = ctypes.c_char_p
     L.skinny_status_string.argtypes = [i]
     L.skinny_abi_version.restype = i
@@ -574,3 +600,79 @@ def moe_plan_query(experts: Experts, T: int, topk: int, x_per_route: bool = Fals
                                        _moe_flags(x_per_route, swiglu), ctypes.byref(plan)),
            "skinny_moe_plan_query")
     return plan
+
+
+def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
+    """A skinny_kv_cache from GPU tensors k and v [pages][kv_heads][page_tokens]
+    [head_dim]: bf16, or e4m3 codes (uint8 / float8_e4m3fn) with k_scale and
+    v_scale [pages][kv_heads] float32."""
+    if isinstance(k, int) or k.dim() != 4:
+        raise ValueError("k must be a 4-D tensor [pages][kv_heads][page_tokens][head_dim]")
+    shape = tuple(int(n) for n in k.shape)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale come together")
+    fp8 = k_scale is not None
+    for t, what in ((k, "k"), (v, "v")):
+        _need(t, shape, _FP8 if fp8 else _BF16, what)
+    if fp8:
+        _need(k_scale, shape[:2], _F32, "k_scale")
+        _need(v_scale, shape[:2], _F32, "v_scale")
+    return KvCache(KV_FP8 if fp8 else KV_BF16, *shape, 0, _ptr(k), _ptr(v), _ptr(k_scale),
+                   _ptr(v_scale))
+
+
+def make_batch(q_start, kv_len, page_table, tokens: int) -> KvBatch:
+    """A skinny_kv_batch from int32 GPU tensors q_start [seqs + 1], kv_len [seqs]
+    and page_table [seqs][max_pages], for steps of `tokens` rows.  The tensors
+    may change between calls (their values are read on the device)."""
+    if isinstance(page_table, int):
+        raise TypeError("pass tensors, or call the raw C entry points through lib()")
+    seqs, width = _shape2(page_table)
+    _need(q_start, (seqs + 1,), _I32, "q_start")
+    _need(kv_len, (seqs,), _I32, "kv_len")
+    _need(page_table, (seqs, width), _I32, "page_table")
+    return KvBatch(seqs, int(tokens), width, 0, _ptr(q_start), _ptr(kv_len), _ptr(page_table))
+
+
+def _heads(cache: KvCache, batch: KvBatch, t, what: str, extra: int = 0) -> int:
+    """Query heads of a [tokens][(q_heads + extra) * head_dim] tensor."""
+    rows, width = _shape2(t)
+    heads = width // cache.head_dim - extra
+    _need(t, (batch.tokens, (heads + extra) * cache.head_dim), _BF16, what)
+    return heads
+
+
+def kv_append(cache: KvCache, batch: KvBatch, qkv, inv_freq, q_out, interleaved: bool = False,
+              stream=None):
+    """Write a step's keys and values into the paged cache and its rotated
+    queries into q_out [tokens][q_heads * head_dim].  qkv [tokens][(q_heads +
+    2 kv_heads) * head_dim] is the QKV linear's y; inv_freq [rotary_dim / 2]
+    float32, or None for no rotation."""
+    heads = _heads(cache, batch, qkv, "qkv", 2 * cache.kv_heads)
+    _need(q_out, (batch.tokens, heads * cache.head_dim), _BF16, "q_out")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * int(inv_freq.shape[0])
+        _need(inv_freq, (rot // 2,), _F32, "inv_freq")
+    _check(lib().skinny_kv_append(cache, batch, _ptr(qkv), heads, _ptr(inv_freq), rot,
+                                  int(interleaved), _ptr(q_out), _stream(stream)),
+           "skinny_kv_append")
+    return q_out
+
+
+def kv_attention_workspace_bytes(cache: KvCache, batch: KvBatch, q_heads: int) -> int:
+    return lib().skinny_kv_attention_workspace_bytes(cache, batch, q_heads)
+
+
+def kv_attention(cache: KvCache, batch: KvBatch, q, out, workspace, scale: float | None = None,
+                 stream=None):
+    """out = softmax(scale q k^T) v over each sequence's cache, causal within
+    the step's rows; q and out bf16 [tokens][q_heads * head_dim], scale
+    1 / sqrt(head_dim) unless given."""
+    heads = _heads(cache, batch, q, "q")
+    _need(out, (batch.tokens, heads * cache.head_dim), _BF16, "out")
+    wp, wb = _ws(workspace)
+    _check(lib().skinny_kv_attention(cache, batch, _ptr(q), heads,
+                                     cache.head_dim ** -0.5 if scale is None else scale, _ptr(out),
+                                     wp, wb, _stream(stream)), "skinny_kv_attention")
+    return out

@@ -1,0 +1,1195 @@
+// kv_cache.hip - gfx950 kernels and C ABI for the paged key/value cache of a
+// decode or verify step: skinny_kv_append (position rotation, then the cache
+// write in bf16 or in e4m3 with one scale per page and head) and
+// skinny_kv_attention (each token's attention over its sequence's cache).
+//
+// Both stand between two of the step's linears: the QKV linear's y is
+// kv_append's input, kv_attention's output is the O linear's x.  A decode
+// step's attention reads every cached byte once per step, so like the linears
+// it is bound by HBM bandwidth; grouped query heads share each byte ("Developing
+// a custom Qwen2.5 72B inference engine from scratch - what is the real
+// bottleneck?", section 6.3).
+//
+// Device arrays that describe the batch are never trusted: row ranges are
+// clamped to [0, T], lengths to the page table, and a page number outside the
+// pool is a page that no key of it is seen in and no row is written to.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "host_util.h"
+#include "skinny_gemm.h"
+
+namespace {
+
+using skinny_host::DeviceInfo;
+using skinny_host::Range;
+using skinny_host::aligned;
+using skinny_host::device_info;
+using skinny_host::overlap;
+using skinny_host::range_of;
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBF16 = SKINNY_KV_BF16;
+constexpr int kFP8 = SKINNY_KV_FP8;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxPosition = 1 << 30;
+constexpr float kE4m3Max = 448.0f;
+constexpr int kMinScaleExp = -64;
+
+// The batch and the cache, as both operators' kernels take them.
+struct KvArgs {
+  unsigned char* k;        // [pages][kv_heads][P][D]
+  unsigned char* v;
+  float* k_scale;          // [pages][kv_heads] (FP8)
+  float* v_scale;
+  const int* q_start;      // [S + 1]
+  const int* kv_len;       // [S]
+  const int* table;        // [S][max_pages]
+  int S;
+  int T;
+  int max_pages;
+  int pages;
+  int kv_heads;
+  int group;               // query heads per KV head
+  int log2p;               // log2 of the page's tokens
+};
+
+// One sequence: rows q0 .. q0 + n of the batch; row i at position base + i,
+// of which the first `cap` positions have a place in the page table.
+struct Seq {
+  int q0, n, base, cap;
+};
+
+__device__ __forceinline__ Seq load_seq(const KvArgs& a, int s) {
+  Seq q;
+  q.q0 = min(max(a.q_start[s], 0), a.T);
+  q.n = min(max(a.q_start[s + 1], q.q0), a.T) - q.q0;
+  const int len = min(max(a.kv_len[s], 0), kMaxPosition);
+  q.base = len - q.n;
+  q.cap = min(len, a.max_pages << a.log2p);
+  return q;
+}
+
+// Sum of two counts that stops at the largest int, so that row ranges which
+// overlap (q_start not ascending) cannot wrap a count around.
+constexpr int kMaxCount = 0x7fffffff;
+__device__ __forceinline__ int add_count(int a, int b) {
+  return (int)min((unsigned)a + (unsigned)b, (unsigned)kMaxCount);
+}
+
+// Inclusive sum over the wave's lanes of counts.
+__device__ __forceinline__ int wave_scan(int v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(v, off);
+    if ((int)(threadIdx.x & 63) >= off) v = add_count(v, o);
+  }
+  return v;
+}
+
+// In a list of counts (one per sequence, `incl` their running sums over the
+// wave's lanes, `before` the sum ahead of lane 0), the lane whose share holds
+// `index`, or -1; `at` becomes the index within that share.
+__device__ __forceinline__ int scan_find(int incl, int before, int index, int& at) {
+  const unsigned long long b = __ballot(incl > index);
+  if (!b) return -1;
+  const int lane = __builtin_ctzll(b);
+  at = index - (lane ? __shfl(incl, max(lane - 1, 0)) : before);
+  return lane;
+}
+
+// ---------------------------------------------------------------------------
+// Appending.
+
+struct AppendArgs {
+  KvArgs kv;
+  const __bf16* qkv;       // [T][(q_heads + 2 kv_heads) D]
+  __bf16* q_out;           // [T][q_heads D]
+  const float* inv_freq;   // [rot / 2], or NULL
+  int q_heads;
+  int head_dim;
+  int rot;                 // rotated values of a head, a multiple of 4
+  int interleaved;         // pairs (2i, 2i + 1) rather than (i, i + rot / 2)
+  int kv_blocks;           // leading workgroups, one per (touched page, head, k or v)
+};
+
+constexpr int kQHeadsPerBlock = 16;
+
+// cos and sin of pos * f.  The angle of a far position needs more than fp32
+// (an error of 2^-24 of 10^6 rad is 0.06 rad), so it is taken in fp64 and
+// reduced to half turns by 1 / pi in two doubles.
+__device__ __forceinline__ void rotation(int pos, float f, double& c, double& s) {
+  constexpr double kInvPiHi = 0x1.45f306dc9c883p-2, kInvPiLo = -0x1.6b01ec5417056p-56;
+  const double x = (double)pos * (double)f;
+  const double p = x * kInvPiHi;
+  const double e = fma(x, kInvPiHi, -p) + x * kInvPiLo;
+  sincospi((p - 2.0 * rint(0.5 * p)) + e, &s, &c);
+}
+
+// fp64 -> fp32 rounded to odd: an inexact value gets an odd last bit, so a
+// later rounding to bf16 or e4m3 is that of the fp64 value itself (one
+// rounding, not two).
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = (float)x;
+  const double back = (double)f;
+  unsigned u = __builtin_bit_cast(unsigned, f);
+  if (back != x && x == x && (u & 0x7f800000u) != 0x7f800000u) {
+    // The nearest fp32 is one of the two neighbours; take the odd one.
+    if (!(u & 1)) u = (back < x) == (f > 0.0f || (f == 0.0f && x > 0.0)) ? u + 1 : u - 1;
+    if (f == 0.0f) u = 1u | (x < 0.0 ? 0x80000000u : 0u);
+  }
+  return __builtin_bit_cast(float, u);
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+  bf16x2 r;
+  r[0] = (__bf16)a;
+  r[1] = (__bf16)b;
+  return __builtin_bit_cast(unsigned, r);
+}
+
+__device__ __forceinline__ float bf16_lo(unsigned u) { return __builtin_bit_cast(float, u << 16); }
+__device__ __forceinline__ float bf16_hi(unsigned u) {
+  return __builtin_bit_cast(float, u & 0xffff0000u);
+}
+
+// Two fp32 -> two e4m3 bytes, to nearest even; beyond 448 (infinities too)
+// the largest number, NaN stays NaN.
+__device__ __forceinline__ unsigned pack_e4m3(float a, float b) {
+  const float ca = fminf(fmaxf(a, -kE4m3Max), kE4m3Max);
+  const float cb = fminf(fmaxf(b, -kE4m3Max), kE4m3Max);
+  unsigned r = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(ca, cb, 0, false) & 0xffffu;
+  if (a != a) r = (r & 0xff00u) | 0x7fu;
+  if (b != b) r = (r & 0x00ffu) | 0x7f00u;
+  return r;
+}
+
+// A unit of four values of a head: two neighbours at pa and two at pb that
+// rotate together (half-split: partners lie rot / 2 apart), or, unrotated or
+// interleaved, four in a row.
+struct Unit {
+  int pa, pb;
+  bool turned;
+};
+
+__device__ __forceinline__ Unit unit_of(int j, int rot, int interleaved) {
+  Unit u;
+  u.turned = 4 * j < rot;
+  const bool split = u.turned && !interleaved;
+  u.pa = split ? 2 * j : 4 * j;
+  u.pb = split ? rot / 2 + 2 * j : 4 * j + 2;
+  return u;
+}
+
+// Rotates a unit's values by the frequencies (c0, s0), (c1, s1) in fp64.
+__device__ __forceinline__ f32x4 turn(unsigned a, unsigned b, int interleaved, double c0, double s0,
+                                      double c1, double s1) {
+  const double a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
+  f32x4 r;
+  if (interleaved) {
+    r[0] = to_odd(a0 * c0 - a1 * s0);
+    r[1] = to_odd(a0 * s0 + a1 * c0);
+    r[2] = to_odd(b0 * c1 - b1 * s1);
+    r[3] = to_odd(b0 * s1 + b1 * c1);
+  } else {
+    r[0] = to_odd(a0 * c0 - b0 * s0);
+    r[1] = to_odd(a1 * c1 - b1 * s1);
+    r[2] = to_odd(a0 * s0 + b0 * c0);
+    r[3] = to_odd(a1 * s1 + b1 * c1);
+  }
+  return r;
+}
+
+// Sequence of batch row t, or -1 for a row behind the last one.
+__device__ __forceinline__ int find_row(const KvArgs& a, int t) {
+  const int lane = threadIdx.x & 63;
+  for (int s0 = 0; s0 < a.S; s0 += 64) {
+    const int s = s0 + lane;
+    const bool hit = s < a.S && a.q_start[s] <= t && t < a.q_start[s + 1];
+    const unsigned long long b = __ballot(hit);
+    if (b) return s0 + __builtin_ctzll(b);
+  }
+  return -1;
+}
+
+// First page and number of pages that a sequence's new rows fall into.
+__device__ __forceinline__ int touched(const Seq& q, int log2p, int& first) {
+  const int lo = max(q.base, 0), hi = min(q.base + q.n, q.cap);
+  first = lo >> log2p;
+  return lo < hi ? ((hi - 1) >> log2p) - first + 1 : 0;
+}
+
+// One workgroup per (page that receives rows, KV head, k or v), which alone
+// reads and writes that page's block and scale, then one per token and
+// kQHeadsPerBlock query heads.  The rotated rows wait in LDS (as fp32 rounded
+// to odd) between the maximum and the rounding.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs a) {
+  extern __shared__ f32x4 rows[];                    // [new rows][D / 4]
+  __shared__ float smax[kWaves];
+  const KvArgs& kv = a.kv;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int D = a.head_dim;
+  const int upr = D / 4;                             // units per row
+  const size_t row_elems = (size_t)(a.q_heads + 2 * kv.kv_heads) * D;
+
+  if ((int)blockIdx.x >= a.kv_blocks) {              // query heads
+    const int chunks = (a.q_heads + kQHeadsPerBlock - 1) / kQHeadsPerBlock;
+    const int b = blockIdx.x - a.kv_blocks;
+    const int t = b / chunks;
+    const int h0 = b % chunks * kQHeadsPerBlock;
+    const int h1 = min(h0 + kQHeadsPerBlock, a.q_heads);
+    const int s = find_row(kv, t);
+    if (s < 0) return;
+    const Seq q = load_seq(kv, s);
+    const int pos = q.base + (t - q.q0);
+    double* cs = reinterpret_cast<double*>(rows);    // [rot / 2] (cos, sin)
+    for (int i = tid; i < a.rot / 2; i += kThreads) rotation(pos, a.inv_freq[i], cs[2 * i], cs[2 * i + 1]);
+    __syncthreads();
+    const unsigned* src = reinterpret_cast<const unsigned*>(a.qkv + t * row_elems);
+    unsigned* dst = reinterpret_cast<unsigned*>(a.q_out + (size_t)t * a.q_heads * D);
+    for (int i = h0 * upr + tid; i < h1 * upr; i += kThreads) {
+      const int h = i / upr, j = i % upr;
+      const Unit u = unit_of(j, a.rot, a.interleaved);
+      unsigned x = src[(h * D + u.pa) / 2], y = src[(h * D + u.pb) / 2];
+      if (u.turned) {
+        const f32x4 r = turn(x, y, a.interleaved, cs[4 * j], cs[4 * j + 1], cs[4 * j + 2],
+                             cs[4 * j + 3]);
+        x = pack_bf16(r[0], r[1]);
+        y = pack_bf16(r[2], r[3]);
+      }
+      dst[(h * D + u.pa) / 2] = x;
+      dst[(h * D + u.pb) / 2] = y;
+    }
+    return;
+  }
+
+  const bool is_v = blockIdx.x & 1;
+  const int h = (blockIdx.x >> 1) % kv.kv_heads;
+  const int unit = (blockIdx.x >> 1) / kv.kv_heads;
+  // The unit-th page touched, sequences in order.
+  int s = -1, page_no = 0, before = 0;
+  for (int s0 = 0; s0 < kv.S && s < 0; s0 += 64) {
+    int first = 0, c = 0;
+    if (s0 + lane < kv.S) c = touched(load_seq(kv, s0 + lane), kv.log2p, first);
+    const int incl = add_count(wave_scan(c), before);
+    int idx;
+    const int at = scan_find(incl, before, unit, idx);
+    if (at >= 0) {
+      s = s0 + at;
+      page_no = __shfl(first, at) + idx;
+    }
+    before = __shfl(incl, 63);
+  }
+  if (s < 0) return;
+  const Seq q = load_seq(kv, s);
+  const int P = 1 << kv.log2p;
+  const int lo = max(max(q.base, 0), page_no << kv.log2p);
+  const int hi = min(min(q.base + q.n, q.cap), (page_no + 1) << kv.log2p);
+  const int count = hi - lo;                         // new rows, 1 .. P
+  const int older = lo & (P - 1);                    // rows of this sequence before them
+  const int page = kv.table[(size_t)s * kv.max_pages + page_no];
+  if (page < 0 || page >= kv.pages) return;
+  constexpr int kEsize = DT == kBF16 ? 2 : 1;
+  unsigned char* block = (is_v ? kv.v : kv.k) + ((size_t)page * kv.kv_heads + h) * P * D * kEsize;
+  const int rot = is_v ? 0 : a.rot;
+  const unsigned* src = reinterpret_cast<const unsigned*>(
+      a.qkv + (size_t)(q.q0 + (lo - q.base)) * row_elems +
+      (size_t)(a.q_heads + (is_v ? kv.kv_heads : 0) + h) * D);
+
+  float top = 0.0f;
+  for (int i = tid; i < count * upr; i += kThreads) {
+    const int r = i / upr, j = i % upr;
+    const Unit u = unit_of(j, rot, a.interleaved);
+    const unsigned x = src[(r * row_elems + u.pa) / 2], y = src[(r * row_elems + u.pb) / 2];
+    f32x4 w{bf16_lo(x), bf16_hi(x), bf16_lo(y), bf16_hi(y)};
+    if (u.turned) {
+      double c0, s0, c1, s1;
+      rotation(lo + r, a.inv_freq[2 * j], c0, s0);
+      rotation(lo + r, a.inv_freq[2 * j + 1], c1, s1);
+      w = turn(x, y, a.interleaved, c0, s0, c1, s1);
+    }
+    if constexpr (DT == kBF16) {
+      unsigned* dst = reinterpret_cast<unsigned*>(block) + (size_t)(older + r) * D / 2;
+      dst[u.pa / 2] = pack_bf16(w[0], w[1]);
+      dst[u.pb / 2] = pack_bf16(w[2], w[3]);
+    } else {
+      rows[i] = w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float m = fabsf(w[e]);
+        if (m < __builtin_inff()) top = fmaxf(top, m);
+      }
+    }
+  }
+  if constexpr (DT == kFP8) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if (lane == 0) smax[tid >> 6] = top;
+    float* scale = (is_v ? kv.v_scale : kv.k_scale) + (size_t)page * kv.kv_heads + h;
+    const float had = older ? *scale : 0.0f;
+    __syncthreads();
+    top = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+    // The smallest power of two that brings the largest value to 448 = 1.75 * 2^8 or below.
+    const unsigned bits = __builtin_bit_cast(unsigned, top);
+    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+    e = max(e, kMinScaleExp);
+    const float need = __builtin_bit_cast(float, (unsigned)(e + 127) << 23);
+    const float now = had >= need ? had : need;
+    const double inv = 1.0 / (double)now;
+    if (older && now != had) {
+      // The older codes move to the larger scale: exact for a power of two,
+      // but for codes that become subnormal.
+      const float ratio = (float)((double)had * inv);
+      unsigned* old = reinterpret_cast<unsigned*>(block);
+      for (int i = tid; i < older * upr; i += kThreads) {
+        const unsigned c = old[i];
+        const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
+        const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+        old[i] = pack_e4m3(x[0] * ratio, x[1] * ratio) |
+                 pack_e4m3(y[0] * ratio, y[1] * ratio) << 16;
+      }
+    }
+    for (int i = tid; i < count * upr; i += kThreads) {
+      const int r = i / upr, j = i % upr;
+      const Unit u = unit_of(j, rot, a.interleaved);
+      const f32x4 w = rows[i];
+      unsigned short* dst = reinterpret_cast<unsigned short*>(block + (size_t)(older + r) * D);
+      dst[u.pa / 2] = (unsigned short)pack_e4m3((float)(w[0] * inv), (float)(w[1] * inv));
+      dst[u.pb / 2] = (unsigned short)pack_e4m3((float)(w[2] * inv), (float)(w[3] * inv));
+    }
+    if (tid == 0) *scale = now;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention.
+//
+// out = softmax(scale q k^T + mask) v over a sequence's cache, one pass with
+// the running maximum m and sum l of exp2 (scores carry log2 e): a larger
+// maximum scales the sums by 2^(m - m').
+//
+// A work item is (sequence, KV head, row group): up to ROWS = 16 RT rows, row
+// r = i * group + g being token i under query head g of the KV head, so each
+// cached byte serves every head that shares it.  A wave takes 32 keys at a
+// time and keeps everything in registers:
+//   S^T = K Q^T    v_mfma_f32_16x16x32_bf16, A = 16 keys, B = 16 rows.  Lane
+//                  (c = lane % 16, g = lane / 16) ends with row c's scores of
+//                  keys 4g .. 4g + 3, so a row's statistics need two lane
+//                  exchanges (lanes +16, +32) and nothing else;
+//   O^T += V^T P^T the products' k index may run over the keys in any order
+//                  that A and B share: lane (c, g) takes as its eight keys the
+//                  ones whose scores it holds (4g + 0..3 of both 16-key
+//                  halves), so P goes from the scores straight into the B
+//                  operand.  For A the lane loads D / 16 neighbouring values of
+//                  those eight keys and turns the 8 x D / 16 block around with
+//                  byte permutes: output tile j holds values c D/16 + j.
+// Keys and values therefore go from HBM to registers with no LDS and no
+// barrier in the loop; e4m3 codes become bf16 exactly, and a page's scale is
+// folded into the scores (k) and the probabilities (v).
+//
+// The blocks of kBlockKeys keys of all items, in order, are cut into equal
+// shares, one per workgroup (every workgroup computes the cut from the batch's
+// device arrays); each wave takes a quarter of a segment's keys.  A segment
+// that is not a whole item leaves its m, l and O in the workspace, and a
+// second launch joins an item's segments in order: no atomics, so a result
+// depends on the lengths and the grid only.
+
+constexpr int kBlockKeys = 128;
+constexpr int kMaxGroups = 1024;         // workgroups of the grid at most
+constexpr float kNegInf = -__builtin_inff();
+
+struct AttnArgs {
+  KvArgs kv;
+  const __bf16* q;         // [T][q_heads D]
+  __bf16* out;             // [T][q_heads D]
+  float* part;             // [2 grid] segments: [ROWS][D] sums, [ROWS] m, [ROWS] l
+  float scale;             // softmax scale * log2 e
+  int groups;              // workgroups of the main launch
+};
+
+__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <bool HIGH>
+__device__ __forceinline__ unsigned e4m3x2_to_bf16(unsigned v) {
+  return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, HIGH));
+}
+
+// Blocks of one (row group, KV head) of a sequence, and its row groups.
+// An item without keys has one block, for its rows' zeros.
+__device__ __forceinline__ int seq_blocks(const Seq& q) {
+  return max(1, (q.cap + kBlockKeys - 1) / kBlockKeys);
+}
+__device__ __forceinline__ int seq_row_groups(const Seq& q, int group, int rows) {
+  return (q.n * group + rows - 1) / rows;
+}
+__device__ __forceinline__ int seq_work(const KvArgs& a, const Seq& q, int rows) {
+  const long long w = (long long)seq_row_groups(q, a.group, rows) * a.kv_heads * seq_blocks(q);
+  return (int)(w < kMaxCount ? w : kMaxCount);
+}
+
+// Where a block number falls.
+struct Place {
+  int s;          // sequence
+  int item;       // h * row groups + row group
+  int blk;        // block within the item
+  int nb;         // blocks of the item
+  int rgs;        // row groups of the sequence
+  Seq q;
+};
+
+__device__ __forceinline__ int total_work(const KvArgs& a, int rows) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int s0 = 0; s0 < a.S; s0 += 64) {
+    const int w = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), rows) : 0;
+    total = add_count(total, __shfl(wave_scan(w), 63));
+  }
+  return total;
+}
+
+__device__ __forceinline__ Place place_of(const KvArgs& a, int rows, int pos) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  Place p{};
+  for (int s0 = 0; s0 < a.S; s0 += 64) {
+    const int w = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), rows) : 0;
+    const int incl = add_count(wave_scan(w), before);
+    int idx;
+    const int at = scan_find(incl, before, pos, idx);
+    if (at >= 0) {
+      p.s = s0 + at;
+      p.q = load_seq(a, p.s);
+      p.nb = seq_blocks(p.q);
+      p.rgs = seq_row_groups(p.q, a.group, rows);
+      p.item = idx / p.nb;
+      p.blk = idx % p.nb;
+      return p;
+    }
+    before = __shfl(incl, 63);
+  }
+  return p;
+}
+
+__device__ __forceinline__ int share_begin(int total, int b, int groups) {
+  return (int)((long long)total * b / groups);
+}
+
+// Floats of one segment in the workspace.
+template <int D>
+__host__ __device__ constexpr int part_floats(int rows) {
+  return rows * (D + 2);
+}
+
+// A lane's value and that of the lane 32 (or 16) away, in either order.
+struct Pair {
+  float a, b;
+};
+__device__ __forceinline__ Pair across32(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned lo = s[0], hi = s[1];
+  return Pair{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ Pair across16(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned lo = s[0], hi = s[1];
+  return Pair{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+
+// Largest value, and sum, over the four lanes of a row (lane, +16, +32, +48).
+__device__ __forceinline__ float row_max(float x) {
+  const Pair p = across32(x);
+  const Pair q = across16(fmaxf(p.a, p.b));
+  return fmaxf(q.a, q.b);
+}
+__device__ __forceinline__ float row_sum(float x) {
+  const Pair p = across32(x);
+  const Pair q = across16(p.a + p.b);
+  return q.a + q.b;
+}
+
+// Bytes (FP8) or halves (bf16) of x that are no finite number, as full masks.
+template <int DT>
+__device__ __forceinline__ unsigned not_finite(unsigned x) {
+  if constexpr (DT == kFP8) {
+    const unsigned f = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // 0x7f: NaN
+    return f | (f - (f >> 7));
+  } else {
+    const unsigned f = ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
+    return f | (f - (f >> 15));
+  }
+}
+
+template <int DT, int D>
+struct Shape {
+  static constexpr int kRowBytes = D * (DT == kBF16 ? 2 : 1);
+  static constexpr int kLoads = kRowBytes / 64;      // 16-byte K loads per lane and 16 keys
+  static constexpr int kSteps = D / 32;              // products over D per 16 keys
+  static constexpr int kTiles = D / 16;              // output tiles
+  static constexpr int kWords = kRowBytes / 64;      // dwords of a lane's part of a V row
+};
+
+// Value j of a lane's part of two keys' V rows, side by side: in the dword's
+// low (j even) or high half's bytes for e4m3 codes, in its halves for bf16.
+template <int DT, int D>
+__device__ __forceinline__ unsigned v_pair(const unsigned (&raw)[8][Shape<DT, D>::kWords], int p,
+                                           int j) {
+  if constexpr (DT == kFP8)
+    return __builtin_amdgcn_perm(raw[2 * p + 1][j / 4], raw[2 * p][j / 4],
+                                 j % 4 < 2 ? 0x05010400u : 0x07030602u);
+  else
+    return __builtin_amdgcn_perm(raw[2 * p + 1][j / 2], raw[2 * p][j / 2],
+                                 j % 2 ? 0x07060302u : 0x05040100u);
+}
+template <int DT>
+__device__ __forceinline__ unsigned v_bf16(unsigned m, int j) {
+  if constexpr (DT == kFP8) return j % 2 ? e4m3x2_to_bf16<true>(m) : e4m3x2_to_bf16<false>(m);
+  return m;
+}
+
+// A operand of output tile j: V^T of the lane's eight keys.
+template <int DT, int D>
+__device__ __forceinline__ u32x4 v_tile(const unsigned (&raw)[8][Shape<DT, D>::kWords], int j) {
+  u32x4 r;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) r[p] = v_bf16<DT>(v_pair<DT, D>(raw, p, j), j);
+  return r;
+}
+
+// The same with 1 in the place of +inf and NaN (sign 0), or of -inf and NaN
+// (sign 1), and 0 elsewhere; e4m3 has NaN only.
+template <int DT, int D>
+__device__ __forceinline__ u32x4 v_marks(const unsigned (&raw)[8][Shape<DT, D>::kWords], int j,
+                                         int sign) {
+  u32x4 r;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const unsigned x = v_pair<DT, D>(raw, p, j);
+    unsigned bad = not_finite<DT>(x);
+    if constexpr (DT == kFP8) {
+      bad &= 0x38383838u;
+    } else {
+      const unsigned nan = ((x & 0x7fu) ? 0xffffu : 0u) | ((x & 0x7f0000u) ? 0xffff0000u : 0u);
+      const unsigned s = x & 0x80008000u;
+      const unsigned neg = s | (s - (s >> 15));
+      bad &= (nan | (sign ? neg : ~neg)) & 0x3f803f80u;
+    }
+    r[p] = v_bf16<DT>(bad, j);
+  }
+  return r;
+}
+
+template <int DT, int D, int RT>
+__global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs a) {
+  using Sh = Shape<DT, D>;
+  constexpr int ROWS = 16 * RT;
+  constexpr int kStride = D + 4;                     // LDS row of the waves' sums, padded
+  __shared__ float sums[kWaves][16][kStride];
+  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  const KvArgs& kv = a.kv;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int P = 1 << kv.log2p;
+  const int q_heads = kv.kv_heads * kv.group;
+
+  const int total = total_work(kv, ROWS);
+  int pos = share_begin(total, blockIdx.x, a.groups);
+  const int end = share_begin(total, blockIdx.x + 1, a.groups);
+
+  while (pos < end) {
+    const Place pl = place_of(kv, ROWS, pos);
+    const int h = pl.item / pl.rgs, rg = pl.item % pl.rgs;
+    const int blocks = min(pl.nb - pl.blk, end - pos);
+    const Seq q = pl.q;
+    const int row_count = min(q.n * kv.group - rg * ROWS, ROWS);
+    const int tok_lo = rg * ROWS / kv.group;
+    const int tok_hi = (rg * ROWS + row_count - 1) / kv.group;
+    // Keys seen by the group's first and last row.
+    const int lim_lo = min(max(q.base + tok_lo + 1, 0), q.cap);
+    const int lim_hi = min(max(q.base + tok_hi + 1, 0), q.cap);
+
+    // Rows: row rt * 16 + c of the group in this lane's column.
+    u32x4 qf[RT][Sh::kSteps];
+    int lim[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = rg * ROWS + rt * 16 + c;
+      const int tok = r / kv.group, head = r % kv.group;
+      const bool live = rt * 16 + c < row_count;
+      lim[rt] = live ? min(max(q.base + tok + 1, 0), q.cap) : lim_hi;
+      const __bf16* src = a.q + ((size_t)(q.q0 + tok) * q_heads + h * kv.group + head) * D;
+#pragma unroll
+      for (int st = 0; st < Sh::kSteps; ++st) {
+        // The 8 values of the product's k index that this lane's K load holds.
+        const int d = DT == kBF16 ? 32 * st + 8 * g : 64 * (st / 2) + 16 * g + 8 * (st % 2);
+        qf[rt][st] = live ? *reinterpret_cast<const u32x4*>(src + d) : u32x4{0, 0, 0, 0};
+      }
+    }
+
+    f32x4 o[RT][Sh::kTiles];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      m[rt] = kNegInf;
+      l[rt] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] = f32x4{0, 0, 0, 0};
+    }
+
+    // This wave's keys: tiles of 32, a quarter of the segment's blocks.
+    const int key0 = (pl.blk * 4 + wave * blocks) * 32;
+    const int tiles = min(max((lim_hi - key0 + 31) / 32, 0), blocks);
+    const int* table = kv.table + (size_t)pl.s * kv.max_pages;
+    const int last_page = max(q.cap - 1, 0) >> kv.log2p;
+    int window = -1;                                 // first page whose number the lanes hold
+    int w_page = -1;
+    float w_ks = 0.0f, w_vs = 0.0f;
+    const size_t page_bytes = (size_t)kv.kv_heads * P * Sh::kRowBytes;
+
+    for (int t = 0; t < tiles; ++t) {
+      const int key = key0 + 32 * t;
+      const int pg = key >> kv.log2p;
+      if (window < 0 || ((key + 16) >> kv.log2p) >= window + 64) {
+        window = pg;
+        w_page = table[min(window + lane, last_page)];
+        const bool good = w_page >= 0 && w_page < kv.pages;
+        w_page = good ? w_page : -1;
+        if constexpr (DT == kFP8) {
+          const size_t at = (size_t)max(w_page, 0) * kv.kv_heads + h;
+          w_ks = good ? kv.k_scale[at] : 0.0f;
+          w_vs = good ? kv.v_scale[at] : 0.0f;
+        }
+      }
+      u32x4 kf[2][Sh::kLoads];
+      unsigned vf[8][Sh::kWords];
+      float ks[2], vs[2];
+      bool good = true;
+      bool there[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = ((key + 16 * u) >> kv.log2p) - window;
+        const int page = __builtin_amdgcn_readlane(w_page, at);
+        there[u] = page >= 0;
+        good = good && there[u];
+        ks[u] = vs[u] = 1.0f;
+        if constexpr (DT == kFP8) {
+          ks[u] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w_ks), at));
+          vs[u] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w_vs), at));
+        }
+        const size_t off = (size_t)max(page, 0) * page_bytes +
+                           (size_t)(h * P + ((key + 16 * u) & (P - 1))) * Sh::kRowBytes;
+        const unsigned char* kp = kv.k + off + c * Sh::kRowBytes + g * 16;
+#pragma unroll
+        for (int i = 0; i < Sh::kLoads; ++i)
+          kf[u][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
+        const unsigned char* vp = kv.v + off + 4 * g * Sh::kRowBytes + c * (4 * Sh::kWords);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int w = 0; w < Sh::kWords; ++w)
+            vf[4 * u + r][w] = *reinterpret_cast<const unsigned*>(vp + r * Sh::kRowBytes + 4 * w);
+      }
+      const bool masked = !good || key + 32 > lim_lo;   // some row does not see some key
+
+      u32x4 pf[RT];
+      f32x4 sc[RT][2];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          f32x4 s{0, 0, 0, 0};
+#pragma unroll
+          for (int st = 0; st < Sh::kSteps; ++st) {
+            u32x4 kk;
+            if constexpr (DT == kBF16) {
+              kk = kf[u][st];
+            } else {
+              const u32x4 raw = kf[u][st / 2];
+              const unsigned x = raw[2 * (st % 2)], y = raw[2 * (st % 2) + 1];
+              kk = u32x4{e4m3x2_to_bf16<false>(x), e4m3x2_to_bf16<true>(x),
+                         e4m3x2_to_bf16<false>(y), e4m3x2_to_bf16<true>(y)};
+            }
+            s = mfma_bf16(kk, qf[rt][st], s);
+          }
+          const float f = a.scale * ks[u];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sc[rt][u][r] = s[r] * f;
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (!there[u] || key + 16 * u + 4 * g + r >= lim[rt]) sc[rt][u][r] = kNegInf;
+          }
+        }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float top = m[rt];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][u][r]);
+        top = row_max(top);
+        if (__any(top > m[rt])) {
+          const float f = top > m[rt] ? __builtin_amdgcn_exp2f(m[rt] - top) : 1.0f;
+          l[rt] *= f;
+#pragma unroll
+          for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] *= f;
+          m[rt] = top;
+        }
+        const float ref = m[rt] == kNegInf ? 0.0f : m[rt];
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(sc[rt][i / 4][i % 4] - ref);
+          l[rt] += p[i];
+          if constexpr (DT == kFP8) p[i] *= vs[i / 4];
+        }
+        if (masked) {
+          // A key that the row does not see takes no part, whatever its page's scale holds.
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!there[i / 4] || key + 16 * (i / 4) + 4 * g + i % 4 >= lim[rt]) p[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf[rt][i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+      }
+      if (masked) {
+        // 0 * inf and 0 * NaN are NaN: values that are no finite numbers leave
+        // the product, and come back for the rows that do see their keys.
+        unsigned any = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int w = 0; w < Sh::kWords; ++w) any |= not_finite<DT>(vf[i][w]);
+        if (__any(any != 0)) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            u32x4 seen{0, 0, 0, 0};                  // 1 where the row sees the key
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (there[x / 4] && key + 16 * (x / 4) + 4 * g + x % 4 < lim[rt])
+                seen[x / 2] |= 0x3f80u << (16 * (x % 2));
+#pragma unroll
+            for (int sign = 0; sign < (DT == kBF16 ? 2 : 1); ++sign)
+#pragma unroll
+              for (int j = 0; j < Sh::kTiles; ++j) {
+                const f32x4 hits = mfma_bf16(v_marks<DT, D>(vf, j, sign), seen, f32x4{0, 0, 0, 0});
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (hits[r] > 0.0f)
+                    o[rt][j][r] += DT == kFP8 ? __builtin_nanf("") : (sign ? kNegInf : -kNegInf);
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int w = 0; w < Sh::kWords; ++w) vf[i][w] &= ~not_finite<DT>(vf[i][w]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < Sh::kTiles; ++j) {
+        const u32x4 vt = v_tile<DT, D>(vf, j);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_bf16(vt, pf[rt], o[rt][j]);
+      }
+    }
+
+    // The four waves' sums, 16 rows at a time.
+    const bool whole = blocks == pl.nb;
+    float* part = a.part + (size_t)(2 * blockIdx.x + (pl.blk == 0 ? 1 : 0)) * part_floats<D>(ROWS);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const float lw = row_sum(l[rt]);
+      if (g == 0) {
+        sm[wave][c] = m[rt];
+        sl[wave][c] = lw;
+      }
+      // Lane (c, g), tile j, register r holds value (4g + r) D/16 + j of row c.
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < Sh::kTiles; ++j)
+          sums[wave][c][(4 * g + r) * Sh::kTiles + j] = o[rt][j][r];
+      __syncthreads();
+      for (int i = tid; i < 16 * (D / 8); i += kThreads) {
+        const int rr = i / (D / 8), d = i % (D / 8) * 8;
+        const int row = rt * 16 + rr;
+        if (row < row_count) {
+          float top = kNegInf;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][rr]);
+          float sum = 0.0f;
+          float x[8] = {};
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            // Without a maximum l is 0 (no key seen) or NaN (a score was).
+            const float f = sm[w][rr] == kNegInf ? sl[w][rr]
+                                                 : __builtin_amdgcn_exp2f(sm[w][rr] - top);
+            sum += f * sl[w][rr];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += f * sums[w][rr][d + e];
+          }
+          if (whole) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int r = rg * ROWS + row;
+            u32x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv);
+            *reinterpret_cast<u32x4*>(a.out +
+                ((size_t)(q.q0 + r / kv.group) * q_heads + h * kv.group + r % kv.group) * D + d) = y;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+              *reinterpret_cast<f32x4*>(part + row * D + d + e) =
+                  f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+            if (d == 0) {
+              part[ROWS * D + row] = top;
+              part[ROWS * D + ROWS + row] = sum;
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    pos += blocks;
+  }
+}
+
+// Joins the segments of the item that workgroup blockIdx.x's share begins
+// inside of, if that is the item's first such share.
+template <int D>
+__global__ __launch_bounds__(kThreads) void skinny_kv_attention_join(const AttnArgs a, int rows) {
+  const KvArgs& kv = a.kv;
+  const int b = blockIdx.x + 1;                      // share 0 begins no item's middle
+  const int total = total_work(kv, rows);
+  const int pos = share_begin(total, b, a.groups);
+  if (pos >= total || pos == share_begin(total, b - 1, a.groups)) return;
+  const Place pl = place_of(kv, rows, pos);
+  if (pl.blk == 0) return;                           // the share begins an item
+  const int first = pos - pl.blk;                    // the item's first block
+  if (share_begin(total, b - 1, a.groups) > first) return;   // an earlier share's
+  const int last = first + pl.nb;
+  const int h = pl.item / pl.rgs, rg = pl.item % pl.rgs;
+  const int row_count = min(pl.q.n * kv.group - rg * rows, rows);
+  const int q_heads = kv.kv_heads * kv.group;
+  const size_t stride = part_floats<D>(rows);
+  const float* head = a.part + (size_t)(2 * (b - 1) + 1) * stride;   // the item's first segment
+  const float* rest = a.part + (size_t)(2 * b) * stride;             // then one per share
+  int n = 0;                                         // shares from b on that reach into the item
+  while (b + n < a.groups && share_begin(total, b + n, a.groups) < last) ++n;
+
+  constexpr int kPer = D / 4;
+  for (int i = blockIdx.y * kThreads + threadIdx.x; i < row_count * kPer;
+       i += gridDim.y * kThreads) {
+    const int row = i / kPer, d = i % kPer * 4;
+    float top = head[rows * D + row];
+    for (int k = 0; k < n; ++k)
+      if (share_begin(total, b + k, a.groups) < share_begin(total, b + k + 1, a.groups))
+        top = fmaxf(top, rest[2 * k * stride + rows * D + row]);
+    float sum = 0.0f;
+    f32x4 x{0, 0, 0, 0};
+    for (int k = -1; k < n; ++k) {
+      if (k >= 0 && share_begin(total, b + k, a.groups) == share_begin(total, b + k + 1, a.groups))
+        continue;                                    // an empty share wrote nothing
+      const float* s = k < 0 ? head : rest + 2 * k * stride;
+      const float mk = s[rows * D + row], lk = s[rows * D + rows + row];
+      const float f = mk == kNegInf ? lk : __builtin_amdgcn_exp2f(mk - top);
+      sum += f * lk;
+      x += f * *reinterpret_cast<const f32x4*>(s + row * D + d);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int r = rg * rows + row;
+    *reinterpret_cast<u32x2*>(a.out +
+        ((size_t)(pl.q.q0 + r / kv.group) * q_heads + h * kv.group + r % kv.group) * D + d) =
+        u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+size_t pool_elems(const skinny_kv_cache& c) {
+  return (size_t)c.pages * c.kv_heads * c.page_tokens * c.head_dim;
+}
+
+skinny_status check_cache(const skinny_kv_cache* c) {
+  if (!c || c->reserved != 0) return SKINNY_ERR_INVALID_ARG;
+  if (c->dtype != SKINNY_KV_BF16 && c->dtype != SKINNY_KV_FP8) return SKINNY_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->kv_heads < 1 || c->page_tokens < 1 || c->head_dim < 1)
+    return SKINNY_ERR_INVALID_ARG;
+  if (!c->k || !c->v) return SKINNY_ERR_INVALID_ARG;
+  const bool fp8 = c->dtype == SKINNY_KV_FP8;
+  if (fp8 != (c->k_scale != nullptr) || fp8 != (c->v_scale != nullptr))
+    return SKINNY_ERR_INVALID_ARG;
+  if (c->page_tokens < SKINNY_KV_MIN_PAGE || c->page_tokens > SKINNY_KV_MAX_PAGE ||
+      (c->page_tokens & (c->page_tokens - 1)))
+    return SKINNY_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return SKINNY_ERR_UNSUPPORTED;
+  if (c->kv_heads > SKINNY_KV_MAX_HEADS) return SKINNY_ERR_UNSUPPORTED;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return SKINNY_ERR_UNSUPPORTED;
+  if (fp8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return SKINNY_ERR_UNSUPPORTED;
+  return SKINNY_OK;
+}
+
+skinny_status check_batch(const skinny_kv_cache& c, const skinny_kv_batch* b) {
+  if (!b || b->reserved != 0) return SKINNY_ERR_INVALID_ARG;
+  if (b->seqs < 1 || b->tokens < 1 || b->max_pages < 1) return SKINNY_ERR_INVALID_ARG;
+  if (!b->q_start || !b->kv_len || !b->page_table) return SKINNY_ERR_INVALID_ARG;
+  if (b->seqs > SKINNY_KV_MAX_SEQS || b->tokens > SKINNY_KV_MAX_TOKENS)
+    return SKINNY_ERR_UNSUPPORTED;
+  if ((long long)b->max_pages * c.page_tokens > kMaxPosition) return SKINNY_ERR_UNSUPPORTED;
+  if (!aligned(b->q_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->page_table, 4))
+    return SKINNY_ERR_UNSUPPORTED;
+  return SKINNY_OK;
+}
+
+// A written buffer against everything else of the call.
+constexpr int kSharedRanges = 7;
+void shared_ranges(const skinny_kv_cache& c, const skinny_kv_batch& b, Range (&r)[kSharedRanges]) {
+  const size_t bytes = pool_elems(c) * (c.dtype == SKINNY_KV_BF16 ? 2 : 1);
+  const size_t sb = c.k_scale ? (size_t)c.pages * c.kv_heads * 4 : 0;
+  r[0] = range_of(c.k, bytes);
+  r[1] = range_of(c.v, bytes);
+  r[2] = range_of(c.k_scale, sb);
+  r[3] = range_of(c.v_scale, sb);
+  r[4] = range_of(b.q_start, (size_t)(b.seqs + 1) * 4);
+  r[5] = range_of(b.kv_len, (size_t)b.seqs * 4);
+  r[6] = range_of(b.page_table, (size_t)b.seqs * b.max_pages * 4);
+}
+
+bool meets(Range w, const Range* r, int n) {
+  for (int i = 0; i < n; ++i)
+    if (r[i].lo != r[i].hi && overlap(w, r[i])) return true;
+  return false;
+}
+
+int log2_of(int p) {
+  int l = 0;
+  while ((1 << l) < p) ++l;
+  return l;
+}
+
+KvArgs kv_args(const skinny_kv_cache& c, const skinny_kv_batch& b, int group) {
+  KvArgs a;
+  a.k = (unsigned char*)c.k;
+  a.v = (unsigned char*)c.v;
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
+  a.q_start = b.q_start;
+  a.kv_len = b.kv_len;
+  a.table = b.page_table;
+  a.S = b.seqs;
+  a.T = b.tokens;
+  a.max_pages = b.max_pages;
+  a.pages = c.pages;
+  a.kv_heads = c.kv_heads;
+  a.group = group;
+  a.log2p = log2_of(c.page_tokens);
+  return a;
+}
+
+skinny_status check_heads(const skinny_kv_cache& c, int q_heads) {
+  if (q_heads < 1 || q_heads % c.kv_heads != 0) return SKINNY_ERR_INVALID_ARG;
+  if (q_heads > SKINNY_KV_MAX_HEADS) return SKINNY_ERR_UNSUPPORTED;
+  return SKINNY_OK;
+}
+
+// Row tiles per item: the rows of an average sequence under one KV head.
+int row_tiles(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
+  const int most = c.head_dim == 256 ? 2 : 4;
+  const long long tokens = (b.tokens + b.seqs - 1) / b.seqs;
+  const long long t = (tokens * (q_heads / c.kv_heads) + 15) / 16;
+  return t < most ? (int)t : most;
+}
+
+// Blocks of all items at most: every sequence at the page table's length.
+long long max_work(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads, int rt) {
+  const long long rows = 16 * rt;
+  const long long rgs = (long long)b.tokens * (q_heads / c.kv_heads) / rows + b.seqs;
+  const long long keys = (long long)b.max_pages * c.page_tokens;
+  return rgs * c.kv_heads * ((keys + kBlockKeys - 1) / kBlockKeys);
+}
+
+size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
+  const int rt = row_tiles(c, b, q_heads);
+  const long long w = max_work(c, b, q_heads, rt);
+  const long long groups = w < kMaxGroups ? w : kMaxGroups;
+  return (size_t)(2 * groups) * (16 * rt) * (c.head_dim + 2) * sizeof(float);
+}
+
+constexpr int kGroupsPerCU = 2;
+
+template <int DT, int D, int RT>
+skinny_status launch_attention(const AttnArgs& a, bool split, hipStream_t stream) {
+  hipLaunchKernelGGL((skinny_kv_attention_k<DT, D, RT>), dim3(a.groups), dim3(kThreads), 0, stream, a);
+  if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
+  if (!split) return SKINNY_OK;
+  const int parts = (16 * RT * (D / 4) + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((skinny_kv_attention_join<D>), dim3(a.groups - 1, parts), dim3(kThreads), 0,
+                     stream, a, 16 * RT);
+  return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
+}
+
+template <int DT, int D>
+skinny_status launch_rows(const AttnArgs& a, int rt, bool split, hipStream_t stream) {
+  if (rt == 1) return launch_attention<DT, D, 1>(a, split, stream);
+  if (rt == 2) return launch_attention<DT, D, 2>(a, split, stream);
+  if constexpr (D < 256) {
+    if (rt == 3) return launch_attention<DT, D, 3>(a, split, stream);
+    if (rt == 4) return launch_attention<DT, D, 4>(a, split, stream);
+  }
+  return SKINNY_ERR_UNSUPPORTED;
+}
+
+template <int DT>
+skinny_status launch_dim(const AttnArgs& a, int d, int rt, bool split, hipStream_t stream) {
+  if (d == 64) return launch_rows<DT, 64>(a, rt, split, stream);
+  if (d == 128) return launch_rows<DT, 128>(a, rt, split, stream);
+  return launch_rows<DT, 256>(a, rt, split, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_batch* batch,
+                               const void* qkv, int q_heads, const float* inv_freq,
+                               int rotary_dim, int interleaved, void* q_out, void* stream) {
+  skinny_status st = check_cache(cache);
+  if (st == SKINNY_OK) st = check_batch(*cache, batch);
+  if (st == SKINNY_OK) st = check_heads(*cache, q_heads);
+  if (st != SKINNY_OK) return st;
+  const skinny_kv_cache& c = *cache;
+  const skinny_kv_batch& b = *batch;
+  if (!qkv || !q_out) return SKINNY_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > c.head_dim || (rotary_dim > 0) != (inv_freq != nullptr) ||
+      (interleaved != 0 && interleaved != 1))
+    return SKINNY_ERR_INVALID_ARG;
+  if (rotary_dim % 4 != 0) return SKINNY_ERR_UNSUPPORTED;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || (inv_freq && !aligned(inv_freq, 4)))
+    return SKINNY_ERR_UNSUPPORTED;
+  const size_t width = (size_t)(q_heads + 2 * c.kv_heads) * c.head_dim;
+  const Range xr = range_of(qkv, b.tokens * width * 2);
+  const Range fr = range_of(inv_freq, (size_t)rotary_dim / 2 * 4);
+  const Range qr = range_of(q_out, (size_t)b.tokens * q_heads * c.head_dim * 2);
+  Range sh[kSharedRanges + 2];
+  Range base[kSharedRanges];
+  shared_ranges(c, b, base);
+  for (int i = 0; i < kSharedRanges; ++i) sh[i] = base[i];
+  sh[kSharedRanges] = xr;
+  sh[kSharedRanges + 1] = fr;
+  if (meets(qr, sh, kSharedRanges + 2)) return SKINNY_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)                       // the pools and scales are written too
+    if (sh[i].lo != sh[i].hi && meets(sh[i], sh + i + 1, kSharedRanges + 1 - i))
+      return SKINNY_ERR_INVALID_ARG;
+  // n rows of a sequence fall into at most n pages, and at most (n - 2) / P + 2.
+  const long long seqs = b.seqs < b.tokens ? b.seqs : b.tokens;
+  long long units = b.tokens / c.page_tokens + 2 * seqs;
+  if (units > b.tokens) units = b.tokens;
+  const long long kvb = units * c.kv_heads * 2;
+  const long long qb = (long long)b.tokens * ((q_heads + kQHeadsPerBlock - 1) / kQHeadsPerBlock);
+  if ((kvb + qb) * kThreads > 0xffffffffLL) return SKINNY_ERR_UNSUPPORTED;   // threads of a launch
+  DeviceInfo d;
+  st = device_info(&d);
+  if (st != SKINNY_OK) return st;
+  if (!d.gfx950) return SKINNY_ERR_UNSUPPORTED;
+
+  AppendArgs a;
+  a.kv = kv_args(c, b, q_heads / c.kv_heads);
+  a.qkv = (const __bf16*)qkv;
+  a.q_out = (__bf16*)q_out;
+  a.inv_freq = inv_freq;
+  a.q_heads = q_heads;
+  a.head_dim = c.head_dim;
+  a.rot = rotary_dim;
+  a.interleaved = interleaved;
+  a.kv_blocks = (int)kvb;
+  const int most = b.tokens < c.page_tokens ? b.tokens : c.page_tokens;
+  const size_t rows = c.dtype == SKINNY_KV_FP8 ? (size_t)most * c.head_dim * 4 : 0;
+  const size_t turns = (size_t)rotary_dim * 8;      // cos and sin in fp64
+  const size_t lds = rows > turns ? rows : turns;
+  const void* fn = c.dtype == SKINNY_KV_FP8 ? (const void*)skinny_kv_append_k<kFP8>
+                                            : (const void*)skinny_kv_append_k<kBF16>;
+  if (lds > 64 * 1024 &&
+      hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+    return SKINNY_ERR_HIP;
+  if (c.dtype == SKINNY_KV_FP8)
+    hipLaunchKernelGGL(skinny_kv_append_k<kFP8>, dim3((unsigned)(kvb + qb)), dim3(kThreads), lds,
+                       (hipStream_t)stream, a);
+  else
+    hipLaunchKernelGGL(skinny_kv_append_k<kBF16>, dim3((unsigned)(kvb + qb)), dim3(kThreads), lds,
+                       (hipStream_t)stream, a);
+  return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
+}
+
+size_t skinny_kv_attention_workspace_bytes(const skinny_kv_cache* cache,
+                                           const skinny_kv_batch* batch, int q_heads) {
+  if (check_cache(cache) != SKINNY_OK || check_batch(*cache, batch) != SKINNY_OK ||
+      check_heads(*cache, q_heads) != SKINNY_OK)
+    return 0;
+  const size_t b = attention_workspace(*cache, *batch, q_heads);
+  return b > SKINNY_MIN_WORKSPACE_BYTES ? b : SKINNY_MIN_WORKSPACE_BYTES;
+}
+
+skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_batch* batch,
+                                  const void* q, int q_heads, float scale, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  skinny_status st = check_cache(cache);
+  if (st == SKINNY_OK) st = check_batch(*cache, batch);
+  if (st == SKINNY_OK) st = check_heads(*cache, q_heads);
+  if (st != SKINNY_OK) return st;
+  const skinny_kv_cache& c = *cache;
+  const skinny_kv_batch& b = *batch;
+  if (!q || !out || !(scale - scale == 0.0f)) return SKINNY_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16)) return SKINNY_ERR_UNSUPPORTED;
+  const int rt = row_tiles(c, b, q_heads);
+  const long long work = max_work(c, b, q_heads, rt);
+  if (work > 0x7fffffffLL) return SKINNY_ERR_UNSUPPORTED;
+  if (!workspace ||
+      workspace_bytes < skinny_kv_attention_workspace_bytes(cache, batch, q_heads))
+    return SKINNY_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return SKINNY_ERR_UNSUPPORTED;
+  const size_t row_bytes = (size_t)b.tokens * q_heads * c.head_dim * 2;
+  const Range qr = range_of(q, row_bytes), yr = range_of(out, row_bytes);
+  const Range wr = range_of(workspace, workspace_bytes);
+  Range sh[kSharedRanges];
+  shared_ranges(c, b, sh);
+  if (overlap(yr, qr) || overlap(yr, wr) || overlap(wr, qr) || meets(yr, sh, kSharedRanges) ||
+      meets(wr, sh, kSharedRanges))
+    return SKINNY_ERR_INVALID_ARG;
+  DeviceInfo d;
+  st = device_info(&d);
+  if (st != SKINNY_OK) return st;
+  if (!d.gfx950) return SKINNY_ERR_UNSUPPORTED;
+
+  AttnArgs a;
+  a.kv = kv_args(c, b, q_heads / c.kv_heads);
+  a.q = (const __bf16*)q;
+  a.out = (__bf16*)out;
+  a.part = (float*)workspace;
+  a.scale = scale * 1.44269504088896340736f;         // log2 e: the kernel's softmax is in exp2
+  long long groups = (long long)d.cus * kGroupsPerCU;
+  if (groups > kMaxGroups) groups = kMaxGroups;
+  if (groups > work) groups = work;
+  a.groups = (int)groups;
+  if (c.dtype == SKINNY_KV_FP8)
+    return launch_dim<kFP8>(a, c.head_dim, rt, groups > 1, (hipStream_t)stream);
+  return launch_dim<kBF16>(a, c.head_dim, rt, groups > 1, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -433,6 +433,116 @@ void skinny_moe_mlp_set_spin_limit(long long polls);
 skinny_status skinny_moe_mlp_plan_query(const skinny_experts* gate_up, const skinny_experts* down,
                                         int T, int topk, skinny_plan* out);
 
+/* ------------------------------------------------------------------------
+ * The step's operators between the QKV linear and the O linear: the paged
+ * key/value cache and the attention over it (grouped query heads, flash
+ * decoding: "Developing a custom Qwen2.5 72B inference engine from scratch -
+ * what is the real bottleneck?", section 6.3).
+ *
+ * A pool of `pages` pages of `page_tokens` tokens holds the keys and values of
+ * all sequences, one layer's at a time; all pointers are device pointers:
+ *   k, v              [pages][kv_heads][page_tokens][head_dim], bf16 or e4m3
+ *   k_scale, v_scale  [pages][kv_heads] fp32 (FP8 only, else NULL): an e4m3
+ *                     code of that page and head stands for code * scale
+ * page_tokens is a power of two from SKINNY_KV_MIN_PAGE to SKINNY_KV_MAX_PAGE,
+ * head_dim 64, 128 or 256, kv_heads at most SKINNY_KV_MAX_HEADS; k and v are
+ * 16-byte aligned.  reserved must be 0. */
+enum skinny_kv_dtype { SKINNY_KV_BF16 = 0, SKINNY_KV_FP8 = 1 };
+#define SKINNY_KV_MIN_PAGE 16
+#define SKINNY_KV_MAX_PAGE 128
+#define SKINNY_KV_MAX_HEADS 1024
+#define SKINNY_KV_MAX_SEQS 65536
+#define SKINNY_KV_MAX_TOKENS 1048576
+typedef struct skinny_kv_cache {
+  int dtype;            /* SKINNY_KV_BF16 or SKINNY_KV_FP8 */
+  int pages;
+  int kv_heads;
+  int page_tokens;
+  int head_dim;
+  int reserved;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} skinny_kv_cache;
+
+/* The sequences of a step, ragged (device arrays, read by the kernels):
+ *   q_start     [seqs + 1] int32, ascending: sequence s owns rows q_start[s] ..
+ *               q_start[s + 1] - 1 of the step's `tokens` rows (none if equal);
+ *               rows from q_start[seqs] on belong to no sequence
+ *   kv_len      [seqs] int32: the sequence's tokens with this step's included,
+ *               so row i of its n rows stands at position kv_len - n + i
+ *   page_table  [seqs][max_pages] int32: page j holds positions j * page_tokens
+ *               .. (j + 1) * page_tokens - 1
+ * One token per sequence is plain decode, several are a verify step or a
+ * prompt.  The values are not trusted: row ranges are cut to 0 .. tokens,
+ * lengths to the page table, and a page outside the pool is one that is
+ * neither written nor seen.  Entries of page_table past a sequence's length
+ * are not used.  reserved must be 0. */
+typedef struct skinny_kv_batch {
+  int seqs;             /* 1 .. SKINNY_KV_MAX_SEQS   */
+  int tokens;           /* 1 .. SKINNY_KV_MAX_TOKENS */
+  int max_pages;        /* >= 1, max_pages * page_tokens <= 2^30 */
+  int reserved;
+  const int* q_start;
+  const int* kv_len;
+  const int* page_table;
+} skinny_kv_batch;
+
+/* Appends a step's keys and values to the cache, rotating queries and keys by
+ * their positions on the way.
+ *   qkv       [tokens][(q_heads + 2 kv_heads) head_dim] bf16, the QKV linear's
+ *             y: query heads, then key heads, then value heads; 16-byte aligned
+ *   inv_freq  [rotary_dim / 2] fp32, or NULL with rotary_dim 0 (no rotation)
+ *   q_out     [tokens][q_heads head_dim] bf16, written, 16-byte aligned
+ * Of each query and key head the first rotary_dim values (a multiple of 4) are
+ * rotated in pairs (a, b) = (x[i], x[i + rotary_dim / 2]), or (x[2i], x[2i + 1])
+ * with interleaved = 1, by the angle t = position * inv_freq[i]:
+ * a' = a cos t - b sin t, b' = a sin t + b cos t, angles and products in fp64.
+ * Queries, and a bf16 cache's keys and values, are rounded once, to bf16.
+ *   An FP8 cache keeps one scale per page, head and k or v.  Rows that begin a
+ * page set it to the smallest power of two s, 2^-64 at least, with |x| <= 448 s
+ * for all of this step's rows in the page; rows that continue a page set it to
+ * the larger of that and the scale the page has, and where it grows the
+ * sequence's earlier codes in the page are rounded again to the new scale
+ * (exact but for codes that become subnormal).  Codes are x / scale to nearest
+ * even; infinities become the largest code and take no part in the scale, NaN
+ * stays NaN.
+ *   Written are q_out's rows that belong to a sequence and the cache's slots of
+ * their positions (and, as above, earlier codes in the same page), nothing
+ * else: positions below 0 or past the page table have no slot.  A page that
+ * receives rows must belong to one sequence only (shared full pages are fine:
+ * they receive none); if two sequences write one page, its contents are
+ * undefined.  A second call with the same inputs changes nothing.
+ * q_heads is a multiple of kv_heads.  No buffer that is written may overlap
+ * another operand.  No workspace; one launch. */
+skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_batch* batch,
+                               const void* qkv, int q_heads, const float* inv_freq,
+                               int rotary_dim, int interleaved, void* q_out, void* stream);
+
+/* Each row's attention over its sequence's cache, up to and including the
+ * row's own position (kv_append has put it there):
+ *   out[row][head] = sum_j p_j v_j,  p = softmax_j(scale * q[row][head] . k_j)
+ * over the positions j <= kv_len - n + i of row i, query head `head` reading KV
+ * head head / (q_heads / kv_heads).
+ *   q, out  [tokens][q_heads head_dim] bf16, 16-byte aligned; out is written
+ *   scale   finite, usually 1 / sqrt(head_dim)
+ * Scores, the softmax's statistics and sums are fp32; the probabilities are
+ * rounded to bf16 for the product with v.  Keys and values of positions that a
+ * row does not see do not reach it, whatever they hold.  A row that sees no
+ * position gets zeros; rows that belong to no sequence are left as they were.
+ * Results are reproducible bitwise for the same lengths, shapes and device.
+ *   workspace  >= skinny_kv_attention_workspace_bytes(cache, batch, q_heads)
+ *              bytes (0 for invalid arguments; pure host arithmetic on the
+ *              shapes), 16-byte aligned; contents undefined afterwards
+ * out must not overlap q, the cache, the batch's arrays or the workspace, nor
+ * the workspace any of them. */
+size_t skinny_kv_attention_workspace_bytes(const skinny_kv_cache* cache,
+                                           const skinny_kv_batch* batch, int q_heads);
+skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_batch* batch,
+                                  const void* q, int q_heads, float scale, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code; never NULL. */
 const char* skinny_status_string(int status);
 
