@@ -23,7 +23,8 @@ __all__ = [
     "moe_mlp_set_spin_limit", "moe_mlp_gave_up", "moe_mlp_plan_query", "MOE_MLP_COUNTER_BYTES",
     "MOE_X_PER_ROUTE", "MOE_SWIGLU", "MAX_TOPK", "KERNEL_NAMES",
     "KV_BF16", "KV_FP8", "KvCache", "KvBatch", "make_kv_cache", "make_batch", "kv_append",
-    "kv_attention", "kv_attention_workspace_bytes",
+    "kv_attention", "kv_attention_workspace_bytes", "LOGITS_BF16", "LOGITS_F32", "Verify",
+    "verify_draft", "verify_workspace_bytes",
 ]
 
 BF16 = 0
@@ -43,6 +44,8 @@ KERNEL_NAMES = {1: "skinny_rows", 2: "skinny_rows (lean)", 3: "skinny_rows_flat"
                 4: "skinny_tiles", 5: "skinny_tiles (8-wave)", 6: "skinny_tiles (K-split)",
                 7: "skinny_moe_mlp1"}
 STATIC_SCRATCH_BYTES = 64 << 20
+LOGITS_BF16 = 0
+LOGITS_F32 = 1
 KV_BF16 = 0
 KV_FP8 = 1
 MOE_MLP_COUNTER_BYTES = 256   # moe_mlp_swiglu's workspace: counter and flag, then gate_up outputs
@@ -94,6 +97,16 @@ class KvBatch(ctypes.Structure):
     _fields_ = [("seqs", ctypes.c_int), ("tokens", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("reserved", ctypes.c_int), ("q_start", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class Verify(ctypes.Structure):
+    """struct skinny_verify"""
+    _fields_ = [("dtype", ctypes.c_int), ("vocab", ctypes.c_int), ("rows", ctypes.c_int),
+                ("seqs", ctypes.c_int), ("q_start", ctypes.c_void_p), ("logits", ctypes.c_void_p),
+                ("draft_logits", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p), ("accept_u", ctypes.c_void_p),
+                ("sample_u", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p),
+                ("accepted", ctypes.c_void_p)]
 
 
 class Plan(ctypes.Structure):
@@ -177,6 +190,10 @@ def _bind(path: str):
     L.skinny_kv_attention_workspace_bytes.argtypes = [cp, bp, i]
     L.skinny_kv_attention.restype = i
     L.skinny_kv_attention.argtypes = [cp, bp, vp, i, ctypes.c_float, vp, vp, sz, vp]
+    L.skinny_verify_workspace_bytes.restype = sz
+    L.skinny_verify_workspace_bytes.argtypes = [i, i, i]
+    L.skinny_verify_draft.restype = i
+    L.skinny_verify_draft.argtypes = [ctypes.POINTER(Verify), vp, sz, vp]
     L.skinny_status_string.restype = ctypes.c_char_p
     L.skinny_status_string.argtypes = [i]
     L.skinny_abi_version.restype = i
@@ -676,3 +693,35 @@ def kv_attention(cache: KvCache, batch: KvBatch, q, out, workspace, scale: float
                                      cache.head_dim ** -0.5 if scale is None else scale, _ptr(out),
                                      wp, wb, _stream(stream)), "skinny_kv_attention")
     return out
+
+
+def verify_workspace_bytes(rows: int, seqs: int, vocab: int) -> int:
+    return lib().skinny_verify_workspace_bytes(rows, seqs, vocab)
+
+
+def verify_draft(q_start, logits, tokens, accept_u, sample_u, out_tokens, accepted, workspace,
+                 draft_logits=None, temperature=None, stream=None):
+    """Which drafted tokens the target keeps and the token that follows them.
+    logits (and draft_logits) [rows][vocab] bf16 or float32, tokens int32 [rows]
+    (the step's input tokens), q_start int32 [seqs + 1], accept_u float32 [rows],
+    sample_u and temperature float32 [seqs]; out_tokens int32 [rows] gets each
+    sequence's kept drafts, its next token, then -1, and accepted int32 [seqs]
+    the number kept."""
+    rows, vocab = _shape2(logits)
+    seqs = int(sample_u.shape[0])
+    name = _dtype_name(logits)
+    _need(logits, (rows, vocab), _BF16 | _F32, "logits")
+    _need(draft_logits, (rows, vocab), {name}, "draft_logits")
+    _need(q_start, (seqs + 1,), _I32, "q_start")
+    _need(tokens, (rows,), _I32, "tokens")
+    _need(accept_u, (rows,), _F32, "accept_u")
+    _need(sample_u, (seqs,), _F32, "sample_u")
+    _need(temperature, (seqs,), _F32, "temperature")
+    _need(out_tokens, (rows,), _I32, "out_tokens")
+    _need(accepted, (seqs,), _I32, "accepted")
+    v = Verify(LOGITS_BF16 if name == "bfloat16" else LOGITS_F32, vocab, rows, seqs, _ptr(q_start),
+               _ptr(logits), _ptr(draft_logits), _ptr(tokens), _ptr(temperature), _ptr(accept_u),
+               _ptr(sample_u), _ptr(out_tokens), _ptr(accepted))
+    wp, wb = _ws(workspace)
+    _check(lib().skinny_verify_draft(v, wp, wb, _stream(stream)), "skinny_verify_draft")
+    return out_tokens

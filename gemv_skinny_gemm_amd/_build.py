@@ -25,7 +25,8 @@ COMMON = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-shared",
           "-Wall", "-Wno-unused-command-line-argument", f"-I{INCLUDE}"]
 
 LIBS = {
-    "libskinny_gemm.so": [os.path.join(CSRC, f) for f in ("skinny_gemm.hip", "kv_cache.hip")],
+    "libskinny_gemm.so": [os.path.join(CSRC, f) for f in ("skinny_gemm.hip", "kv_cache.hip",
+                                                              "verify_draft.hip")],
     os.path.join("synth", "libskinny_synth.so"): [os.path.join(PKG, "synth", "synth_gpu.hip")],
     os.path.join("probe", "libskinny_probe.so"): [os.path.join(PKG, "probe", "stream_read.hip")],
 }

@@ -543,6 +543,62 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
                                   const void* q, int q_heads, float scale, void* out,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* The end of a verify step: which drafted tokens the target keeps, and the one
+ * that follows them, from the target's logits and given random numbers, so that
+ * the tokens are distributed as the target's own ("9% faster GLM-5.3-Flash
+ * prefill with GPU-to-GPU IPC (and why TileLang didn't help)", section
+ * "TileLang: twice as fast, and no faster": a verify step of drafted tokens).
+ *   Sequence s has rows q_start[s] .. q_start[s + 1] - 1 (device int32, as in
+ * skinny_kv_batch, values not trusted); tokens[row] is the token that the step
+ * read at that row: a sequence's first one is its last sure token, the others
+ * are drafted.  logits[row] are the target's for the place after it, and
+ * draft_logits[row] those that the token at row + 1 was drawn from (a sequence's
+ * last row is not read).  With p = softmax(logits[row] / t), q =
+ * softmax(draft_logits[row] / t), t = temperature[s] and d = tokens[row + 1]:
+ *   row by row, d is kept while accept_u[row] * q(d) < p(d);
+ *   at the first row that keeps none, the next token is drawn from max(0, p - q)
+ *   (from p if that is zero everywhere), and at a sequence's last row, all
+ *   drafts kept, from p: the smallest v whose running sum, v included, is above
+ *   sample_u[s] times the total.
+ * draft_logits NULL: the drafts are given, not drawn (q = 1 at d).  temperature
+ * NULL: 1 for all.  t <= 0 (or NaN): greedy, p is 1 at the lowest index of the
+ * largest logit, and draft_logits are not asked.  A NaN logit counts as -inf; a row
+ * without any logit above -inf keeps nothing and gives token 0.  A drafted token
+ * outside 0 .. vocab - 1 is not kept.
+ *   out_tokens [rows] int32: at a sequence's rows its kept drafts, the next
+ *     token, then -1; rows of no sequence are left as they were
+ *   accepted [seqs] int32: drafts kept, so accepted + 1 tokens are new (0, and
+ *     none, for a sequence without rows)
+ * Probabilities and sums are fp64: the tokens are those of exact arithmetic
+ * unless a random number lies within about 1e-13 of a boundary.
+ *   accept_u [rows], sample_u [seqs] fp32, uniform on [0, 1)
+ *   logits, draft_logits [rows][vocab] bf16 or fp32, aligned to their type (read
+ *     16 bytes at a time when 16-byte aligned and rows are multiples of 16 bytes)
+ *   workspace >= skinny_verify_workspace_bytes(rows, seqs, vocab) bytes (0 for
+ *     invalid arguments), 16-byte aligned, contents undefined before and after
+ * out_tokens, accepted and the workspace must not overlap anything else. */
+enum skinny_logits_dtype { SKINNY_LOGITS_BF16 = 0, SKINNY_LOGITS_F32 = 1 };
+#define SKINNY_VERIFY_MAX_ROWS 65535
+#define SKINNY_VERIFY_MAX_VOCAB 16777216
+typedef struct skinny_verify {
+  int dtype;            /* enum skinny_logits_dtype              */
+  int vocab;            /* 1 .. SKINNY_VERIFY_MAX_VOCAB          */
+  int rows;             /* 1 .. SKINNY_VERIFY_MAX_ROWS           */
+  int seqs;             /* 1 .. SKINNY_VERIFY_MAX_ROWS           */
+  const int* q_start;
+  const void* logits;
+  const void* draft_logits;
+  const int* tokens;
+  const float* temperature;
+  const float* accept_u;
+  const float* sample_u;
+  int* out_tokens;
+  int* accepted;
+} skinny_verify;
+size_t skinny_verify_workspace_bytes(int rows, int seqs, int vocab);
+skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Static text for a status code; never NULL. */
 const char* skinny_status_string(int status);
 
