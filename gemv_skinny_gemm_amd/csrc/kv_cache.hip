@@ -62,6 +62,14 @@ struct KvArgs {
   int log2p;               // log2 of the page's tokens
 };
 
+// A value that all lanes hold, or one lane's, as a scalar: addresses and
+// branches that depend on it stay out of the vector registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int lane_of(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
 // One sequence: rows q0 .. q0 + n of the batch; row i at position base + i,
 // of which the first `cap` positions have a place in the page table.
 struct Seq {
@@ -76,6 +84,9 @@ __device__ __forceinline__ Seq load_seq(const KvArgs& a, int s) {
   q.base = len - q.n;
   q.cap = min(len, a.max_pages << a.log2p);
   return q;
+}
+__device__ __forceinline__ Seq uniform(const Seq& q) {
+  return Seq{uniform(q.q0), uniform(q.n), uniform(q.base), uniform(q.cap)};
 }
 
 // Sum of two counts that stops at the largest int, so that row ranges which
@@ -102,7 +113,7 @@ __device__ __forceinline__ int scan_find(int incl, int before, int index, int& a
   const unsigned long long b = __ballot(incl > index);
   if (!b) return -1;
   const int lane = __builtin_ctzll(b);
-  at = index - (lane ? __shfl(incl, max(lane - 1, 0)) : before);
+  at = index - (lane ? lane_of(incl, max(lane - 1, 0)) : before);
   return lane;
 }
 
@@ -250,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
     const int h1 = min(h0 + kQHeadsPerBlock, a.q_heads);
     const int s = find_row(kv, t);
     if (s < 0) return;
-    const Seq q = load_seq(kv, s);
+    const Seq q = uniform(load_seq(kv, s));
     const int pos = q.base + (t - q.q0);
     double* cs = reinterpret_cast<double*>(rows);    // [rot / 2] (cos, sin)
     for (int i = tid; i < a.rot / 2; i += kThreads) rotation(pos, a.inv_freq[i], cs[2 * i], cs[2 * i + 1]);
@@ -286,12 +297,12 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
     const int at = scan_find(incl, before, unit, idx);
     if (at >= 0) {
       s = s0 + at;
-      page_no = __shfl(first, at) + idx;
+      page_no = lane_of(first, at) + idx;
     }
-    before = __shfl(incl, 63);
+    before = lane_of(incl, 63);
   }
   if (s < 0) return;
-  const Seq q = load_seq(kv, s);
+  const Seq q = uniform(load_seq(kv, s));
   const int P = 1 << kv.log2p;
   const int lo = max(max(q.base, 0), page_no << kv.log2p);
   const int hi = min(min(q.base + q.n, q.cap), (page_no + 1) << kv.log2p);
@@ -455,7 +466,7 @@ __device__ __forceinline__ int total_work(const KvArgs& a, int rows) {
   int total = 0;
   for (int s0 = 0; s0 < a.S; s0 += 64) {
     const int w = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), rows) : 0;
-    total = add_count(total, __shfl(wave_scan(w), 63));
+    total = add_count(total, lane_of(wave_scan(w), 63));
   }
   return total;
 }
@@ -471,21 +482,30 @@ __device__ __forceinline__ Place place_of(const KvArgs& a, int rows, int pos) {
     const int at = scan_find(incl, before, pos, idx);
     if (at >= 0) {
       p.s = s0 + at;
-      p.q = load_seq(a, p.s);
+      p.q = uniform(load_seq(a, p.s));
       p.nb = seq_blocks(p.q);
       p.rgs = seq_row_groups(p.q, a.group, rows);
       p.item = idx / p.nb;
       p.blk = idx % p.nb;
       return p;
     }
-    before = __shfl(incl, 63);
+    before = lane_of(incl, 63);
   }
   return p;
 }
 
-__device__ __forceinline__ int share_begin(int total, int b, int groups) {
-  return (int)((long long)total * b / groups);
-}
+// The cut of `total` blocks into equal shares, the first `rest` of them one
+// block longer.
+struct Shares {
+  int base, rest;
+  __device__ __forceinline__ Shares(int total, int groups)
+      : base(total / groups), rest(total % groups) {}
+  __device__ __forceinline__ int begin(int b) const { return b * base + min(b, rest); }
+  __device__ __forceinline__ int of(int pos) const {      // the share of a block
+    const int longer = rest * (base + 1);
+    return pos < longer ? pos / (base + 1) : rest + (pos - longer) / base;
+  }
+};
 
 // Floats of one segment in the workspace.
 template <int D>
@@ -531,6 +551,28 @@ __device__ __forceinline__ unsigned not_finite(unsigned x) {
   } else {
     const unsigned f = ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
     return f | (f - (f >> 15));
+  }
+}
+
+// Loads of the cache: every byte is read once per call (per row group).
+__device__ __forceinline__ u32x4 load16(const unsigned char* p) {
+  return *reinterpret_cast<const u32x4*>(p);
+}
+template <int W>
+__device__ __forceinline__ void load_words(const unsigned char* p, unsigned (&out)[W]) {
+  if constexpr (W == 1) {
+    out[0] = *reinterpret_cast<const unsigned*>(p);
+  } else if constexpr (W == 2) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    out[0] = x[0];
+    out[1] = x[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const u32x4 x = load16(p + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[i + e] = x[e];
+    }
   }
 }
 
@@ -609,8 +651,9 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
   const int q_heads = kv.kv_heads * kv.group;
 
   const int total = total_work(kv, ROWS);
-  int pos = share_begin(total, blockIdx.x, a.groups);
-  const int end = share_begin(total, blockIdx.x + 1, a.groups);
+  const Shares shares(total, a.groups);
+  int pos = shares.begin(blockIdx.x);
+  const int end = shares.begin(blockIdx.x + 1);
 
   while (pos < end) {
     const Place pl = place_of(kv, ROWS, pos);
@@ -662,11 +705,10 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
     float w_ks = 0.0f, w_vs = 0.0f;
     const size_t page_bytes = (size_t)kv.kv_heads * P * Sh::kRowBytes;
 
-    for (int t = 0; t < tiles; ++t) {
-      const int key = key0 + 32 * t;
-      const int pg = key >> kv.log2p;
-      if (window < 0 || ((key + 16) >> kv.log2p) >= window + 64) {
-        window = pg;
+    // Page number and scales of the page that holds `key`, from the lanes.
+    const auto look = [&](int key) {
+      if (window < 0 || (key >> kv.log2p) < window || ((key + 16) >> kv.log2p) >= window + 64) {
+        window = key >> kv.log2p;
         w_page = table[min(window + lane, last_page)];
         const bool good = w_page >= 0 && w_page < kv.pages;
         w_page = good ? w_page : -1;
@@ -676,35 +718,61 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
           w_vs = good ? kv.v_scale[at] : 0.0f;
         }
       }
-      u32x4 kf[2][Sh::kLoads];
-      unsigned vf[8][Sh::kWords];
-      float ks[2], vs[2];
-      bool good = true;
-      bool there[2];
+    };
+    // A tile's two halves of 16 keys: where they lie, and their scales.
+    struct Half {
+      size_t off;
+      float ks, vs;
+      bool there;
+    };
+    const auto half_of = [&](int key) {
+      Half x;
+      const int at = (key >> kv.log2p) - window;
+      const int page = lane_of(w_page, at);
+      x.there = page >= 0;
+      x.ks = x.vs = 1.0f;
+      if constexpr (DT == kFP8) {
+        x.ks = lane_of(w_ks, at);
+        x.vs = lane_of(w_vs, at);
+      }
+      x.off = (size_t)max(page, 0) * page_bytes + (size_t)(h * P + (key & (P - 1))) * Sh::kRowBytes;
+      return x;
+    };
+    u32x4 kf[2][Sh::kLoads];
+    unsigned vf[8][Sh::kWords];
+    const auto load_k = [&](const Half (&at)[2]) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int at = ((key + 16 * u) >> kv.log2p) - window;
-        const int page = __builtin_amdgcn_readlane(w_page, at);
-        there[u] = page >= 0;
-        good = good && there[u];
-        ks[u] = vs[u] = 1.0f;
-        if constexpr (DT == kFP8) {
-          ks[u] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w_ks), at));
-          vs[u] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w_vs), at));
-        }
-        const size_t off = (size_t)max(page, 0) * page_bytes +
-                           (size_t)(h * P + ((key + 16 * u) & (P - 1))) * Sh::kRowBytes;
-        const unsigned char* kp = kv.k + off + c * Sh::kRowBytes + g * 16;
+        const unsigned char* kp = kv.k + at[u].off + c * Sh::kRowBytes + g * 16;
 #pragma unroll
-        for (int i = 0; i < Sh::kLoads; ++i)
-          kf[u][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
-        const unsigned char* vp = kv.v + off + 4 * g * Sh::kRowBytes + c * (4 * Sh::kWords);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int w = 0; w < Sh::kWords; ++w)
-            vf[4 * u + r][w] = *reinterpret_cast<const unsigned*>(vp + r * Sh::kRowBytes + 4 * w);
+        for (int i = 0; i < Sh::kLoads; ++i) kf[u][i] = load16(kp + 64 * i);
       }
+    };
+    const auto load_v = [&](const Half (&at)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const unsigned char* vp = kv.v + at[u].off + 4 * g * Sh::kRowBytes + c * (4 * Sh::kWords);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) load_words<Sh::kWords>(vp + r * Sh::kRowBytes, vf[4 * u + r]);
+      }
+    };
+
+    // The next tile's keys load behind this tile's scores, its values behind
+    // this tile's output; the last tile loads itself once more.
+    Half now[2];
+    if (tiles > 0) {
+      look(key0);
+      now[0] = half_of(key0);
+      now[1] = half_of(key0 + 16);
+      load_k(now);
+      load_v(now);
+    }
+    bool dirty = false;                              // a masked tile had such values
+    for (int t = 0; t < tiles; ++t) {
+      const int key = key0 + 32 * t;
+      const float ks[2] = {now[0].ks, now[1].ks}, vs[2] = {now[0].vs, now[1].vs};
+      const bool there[2] = {now[0].there, now[1].there};
+      const bool good = there[0] && there[1];
       const bool masked = !good || key + 32 > lim_lo;   // some row does not see some key
 
       u32x4 pf[RT];
@@ -736,6 +804,11 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
               if (!there[u] || key + 16 * u + 4 * g + r >= lim[rt]) sc[rt][u][r] = kNegInf;
           }
         }
+      const int next = key0 + 32 * min(t + 1, tiles - 1);
+      look(next);
+      now[0] = half_of(next);
+      now[1] = half_of(next + 16);
+      load_k(now);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float top = m[rt];
@@ -770,31 +843,14 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
       }
       if (masked) {
         // 0 * inf and 0 * NaN are NaN: values that are no finite numbers leave
-        // the product, and come back for the rows that do see their keys.
+        // the product, and come back below for the rows that do see their keys.
         unsigned any = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int w = 0; w < Sh::kWords; ++w) any |= not_finite<DT>(vf[i][w]);
         if (__any(any != 0)) {
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            u32x4 seen{0, 0, 0, 0};                  // 1 where the row sees the key
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (there[x / 4] && key + 16 * (x / 4) + 4 * g + x % 4 < lim[rt])
-                seen[x / 2] |= 0x3f80u << (16 * (x % 2));
-#pragma unroll
-            for (int sign = 0; sign < (DT == kBF16 ? 2 : 1); ++sign)
-#pragma unroll
-              for (int j = 0; j < Sh::kTiles; ++j) {
-                const f32x4 hits = mfma_bf16(v_marks<DT, D>(vf, j, sign), seen, f32x4{0, 0, 0, 0});
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (hits[r] > 0.0f)
-                    o[rt][j][r] += DT == kFP8 ? __builtin_nanf("") : (sign ? kNegInf : -kNegInf);
-              }
-          }
+          dirty = true;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -806,6 +862,34 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
         const u32x4 vt = v_tile<DT, D>(vf, j);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_bf16(vt, pf[rt], o[rt][j]);
+      }
+      load_v(now);
+    }
+
+    for (int t = dirty ? 0 : tiles; t < tiles; ++t) {
+      const int key = key0 + 32 * t;
+      look(key);
+      now[0] = half_of(key);
+      now[1] = half_of(key + 16);
+      if (now[0].there && now[1].there && key + 32 <= lim_lo) continue;
+      load_v(now);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        u32x4 seen{0, 0, 0, 0};                      // 1 where the row sees the key
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (now[x / 4].there && key + 16 * (x / 4) + 4 * g + x % 4 < lim[rt])
+            seen[x / 2] |= 0x3f80u << (16 * (x % 2));
+#pragma unroll
+        for (int sign = 0; sign < (DT == kBF16 ? 2 : 1); ++sign)
+#pragma unroll
+          for (int j = 0; j < Sh::kTiles; ++j) {
+            const f32x4 hits = mfma_bf16(v_marks<DT, D>(vf, j, sign), seen, f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (hits[r] > 0.0f)
+                o[rt][j][r] += DT == kFP8 ? __builtin_nanf("") : (sign ? kNegInf : -kNegInf);
+          }
       }
     }
 
@@ -870,52 +954,86 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
   }
 }
 
-// Joins the segments of the item that workgroup blockIdx.x's share begins
-// inside of, if that is the item's first such share.
+// Joins the segments of item blockIdx.x, row blockIdx.y: kGroups groups of D / 4
+// lanes take every kGroups-th segment, in order, and are added in order.
+constexpr int kJoinThreads = 512;
 template <int D>
-__global__ __launch_bounds__(kThreads) void skinny_kv_attention_join(const AttnArgs a, int rows) {
+__global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const AttnArgs a, int rows) {
+  constexpr int kLanes = D / 4;                      // lanes of a row, 4 values each
+  constexpr int kGroups = kJoinThreads / kLanes;
+  __shared__ f32x4 sx[kGroups][kLanes];
+  __shared__ float sl[kGroups], sm[kGroups];
   const KvArgs& kv = a.kv;
-  const int b = blockIdx.x + 1;                      // share 0 begins no item's middle
-  const int total = total_work(kv, rows);
-  const int pos = share_begin(total, b, a.groups);
-  if (pos >= total || pos == share_begin(total, b - 1, a.groups)) return;
-  const Place pl = place_of(kv, rows, pos);
-  if (pl.blk == 0) return;                           // the share begins an item
-  const int first = pos - pl.blk;                    // the item's first block
-  if (share_begin(total, b - 1, a.groups) > first) return;   // an earlier share's
-  const int last = first + pl.nb;
-  const int h = pl.item / pl.rgs, rg = pl.item % pl.rgs;
-  const int row_count = min(pl.q.n * kv.group - rg * rows, rows);
-  const int q_heads = kv.kv_heads * kv.group;
+  const int lane = threadIdx.x & 63;
+  // The item's sequence, its first block, and the number of all blocks.
+  int items = 0, total = 0, at_item = -1, first = 0;
+  Seq q{};
+  for (int s0 = 0; s0 < kv.S; s0 += 64) {
+    Seq mine{};
+    int n = 0, w = 0;
+    if (s0 + lane < kv.S) {
+      mine = load_seq(kv, s0 + lane);
+      n = seq_row_groups(mine, kv.group, rows) * kv.kv_heads;
+      w = seq_work(kv, mine, rows);
+    }
+    const int ni = add_count(wave_scan(n), items), wi = add_count(wave_scan(w), total);
+    int idx;
+    const int at = at_item < 0 ? scan_find(ni, items, blockIdx.x, idx) : -1;
+    if (at >= 0) {
+      at_item = idx;
+      q = uniform(load_seq(kv, s0 + at));
+      first = (at ? lane_of(wi, max(at - 1, 0)) : total) + idx * seq_blocks(q);
+    }
+    items = lane_of(ni, 63);
+    total = lane_of(wi, 63);
+  }
+  if (at_item < 0) return;
+  const int nb = seq_blocks(q);
+  const Shares shares(total, a.groups);
+  const int b0 = shares.of(first), b1 = shares.of(first + nb - 1);
+  if (b0 == b1) return;                              // one share holds the whole item
+  const int rgs = seq_row_groups(q, kv.group, rows);
+  const int h = at_item / rgs, rg = at_item % rgs;
+  const int row = blockIdx.y;
+  if (rg * rows + row >= q.n * kv.group) return;
   const size_t stride = part_floats<D>(rows);
-  const float* head = a.part + (size_t)(2 * (b - 1) + 1) * stride;   // the item's first segment
-  const float* rest = a.part + (size_t)(2 * b) * stride;             // then one per share
-  int n = 0;                                         // shares from b on that reach into the item
-  while (b + n < a.groups && share_begin(total, b + n, a.groups) < last) ++n;
-
-  constexpr int kPer = D / 4;
-  for (int i = blockIdx.y * kThreads + threadIdx.x; i < row_count * kPer;
-       i += gridDim.y * kThreads) {
-    const int row = i / kPer, d = i % kPer * 4;
-    float top = head[rows * D + row];
-    for (int k = 0; k < n; ++k)
-      if (share_begin(total, b + k, a.groups) < share_begin(total, b + k + 1, a.groups))
-        top = fmaxf(top, rest[2 * k * stride + rows * D + row]);
-    float sum = 0.0f;
-    f32x4 x{0, 0, 0, 0};
-    for (int k = -1; k < n; ++k) {
-      if (k >= 0 && share_begin(total, b + k, a.groups) == share_begin(total, b + k + 1, a.groups))
-        continue;                                    // an empty share wrote nothing
-      const float* s = k < 0 ? head : rest + 2 * k * stride;
-      const float mk = s[rows * D + row], lk = s[rows * D + rows + row];
-      const float f = mk == kNegInf ? lk : __builtin_amdgcn_exp2f(mk - top);
-      sum += f * lk;
-      x += f * *reinterpret_cast<const f32x4*>(s + row * D + d);
+  // Segment k is share b0 + k's: the item's first one stands second in its share's pair.
+  const int n = b1 - b0 + 1;
+  const float* part = a.part + (size_t)(2 * b0) * stride;
+  const int d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+  float top = kNegInf;
+  for (int k = threadIdx.x; k < n; k += kJoinThreads)
+    top = fmaxf(top, part[(2 * k + (k == 0)) * stride + rows * D + row]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+  if (lane == 0) sm[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, sm[w]);
+  float sum = 0.0f;
+  f32x4 x{0, 0, 0, 0};
+#pragma unroll 4
+  for (int k = grp; k < n; k += kGroups) {
+    const float* s = part + (2 * k + (k == 0)) * stride;
+    const float mk = s[rows * D + row], lk = s[rows * D + rows + row];
+    const f32x4 y = *reinterpret_cast<const f32x4*>(s + row * D + 4 * d);
+    const float f = mk == kNegInf ? lk : __builtin_amdgcn_exp2f(mk - top);
+    sum += f * lk;
+    x += f * y;
+  }
+  sx[grp][d] = x;
+  if (d == 0) sl[grp] = sum;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+      x += sx[i][d];
+      sum += sl[i];
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int r = rg * rows + row;
-    *reinterpret_cast<u32x2*>(a.out +
-        ((size_t)(pl.q.q0 + r / kv.group) * q_heads + h * kv.group + r % kv.group) * D + d) =
+    *reinterpret_cast<u32x2*>(a.out + ((size_t)(q.q0 + r / kv.group) * kv.kv_heads * kv.group +
+                                       h * kv.group + r % kv.group) * D + 4 * d) =
         u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
   }
 }
@@ -1009,20 +1127,33 @@ skinny_status check_heads(const skinny_kv_cache& c, int q_heads) {
   return SKINNY_OK;
 }
 
-// Row tiles per item: the rows of an average sequence under one KV head.
+// Row tiles per item: the rows of an average sequence under one KV head, as
+// many as a wave's registers hold beside a tile of keys and values.
+constexpr int most_row_tiles(int dtype, int head_dim) {
+  return head_dim < 256 ? 4 : dtype == SKINNY_KV_FP8 ? 2 : 1;
+}
 int row_tiles(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
-  const int most = c.head_dim == 256 ? 2 : 4;
+  const int most = most_row_tiles(c.dtype, c.head_dim);
   const long long tokens = (b.tokens + b.seqs - 1) / b.seqs;
   const long long t = (tokens * (q_heads / c.kv_heads) + 15) / 16;
   return t < most ? (int)t : most;
 }
 
+// Row groups of all sequences at most.
+long long max_row_groups(const skinny_kv_batch& b, int group, int rt) {
+  const long long rows = (long long)b.tokens * group;
+  const long long r = rows / (16 * rt) + (b.seqs < b.tokens ? b.seqs : b.tokens);
+  return r < rows ? r : rows;
+}
+
+long long max_items(const skinny_kv_batch& b, const skinny_kv_cache& c, int q_heads, int rt) {
+  return max_row_groups(b, q_heads / c.kv_heads, rt) * c.kv_heads;
+}
+
 // Blocks of all items at most: every sequence at the page table's length.
 long long max_work(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads, int rt) {
-  const long long rows = 16 * rt;
-  const long long rgs = (long long)b.tokens * (q_heads / c.kv_heads) / rows + b.seqs;
   const long long keys = (long long)b.max_pages * c.page_tokens;
-  return rgs * c.kv_heads * ((keys + kBlockKeys - 1) / kBlockKeys);
+  return max_items(b, c, q_heads, rt) * ((keys + kBlockKeys - 1) / kBlockKeys);
 }
 
 size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
@@ -1035,32 +1166,33 @@ size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, i
 constexpr int kGroupsPerCU = 2;
 
 template <int DT, int D, int RT>
-skinny_status launch_attention(const AttnArgs& a, bool split, hipStream_t stream) {
+skinny_status launch_attention(const AttnArgs& a, int items, int rows, hipStream_t stream) {
   hipLaunchKernelGGL((skinny_kv_attention_k<DT, D, RT>), dim3(a.groups), dim3(kThreads), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
-  if (!split) return SKINNY_OK;
-  const int parts = (16 * RT * (D / 4) + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL((skinny_kv_attention_join<D>), dim3(a.groups - 1, parts), dim3(kThreads), 0,
-                     stream, a, 16 * RT);
+  if (a.groups == 1) return SKINNY_OK;               // nothing is split
+  hipLaunchKernelGGL((skinny_kv_attention_join<D>), dim3(items, rows), dim3(kJoinThreads), 0, stream,
+                     a, 16 * RT);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 
 template <int DT, int D>
-skinny_status launch_rows(const AttnArgs& a, int rt, bool split, hipStream_t stream) {
-  if (rt == 1) return launch_attention<DT, D, 1>(a, split, stream);
-  if (rt == 2) return launch_attention<DT, D, 2>(a, split, stream);
-  if constexpr (D < 256) {
-    if (rt == 3) return launch_attention<DT, D, 3>(a, split, stream);
-    if (rt == 4) return launch_attention<DT, D, 4>(a, split, stream);
+skinny_status launch_rows(const AttnArgs& a, int rt, int items, int rows, hipStream_t stream) {
+  constexpr int kMost = most_row_tiles(DT, D);
+  if (rt == 1) return launch_attention<DT, D, 1>(a, items, rows, stream);
+  if constexpr (kMost >= 2)
+    if (rt == 2) return launch_attention<DT, D, 2>(a, items, rows, stream);
+  if constexpr (kMost >= 4) {
+    if (rt == 3) return launch_attention<DT, D, 3>(a, items, rows, stream);
+    if (rt == 4) return launch_attention<DT, D, 4>(a, items, rows, stream);
   }
   return SKINNY_ERR_UNSUPPORTED;
 }
 
 template <int DT>
-skinny_status launch_dim(const AttnArgs& a, int d, int rt, bool split, hipStream_t stream) {
-  if (d == 64) return launch_rows<DT, 64>(a, rt, split, stream);
-  if (d == 128) return launch_rows<DT, 128>(a, rt, split, stream);
-  return launch_rows<DT, 256>(a, rt, split, stream);
+skinny_status launch_dim(const AttnArgs& a, int d, int rt, int items, int rows, hipStream_t stream) {
+  if (d == 64) return launch_rows<DT, 64>(a, rt, items, rows, stream);
+  if (d == 128) return launch_rows<DT, 128>(a, rt, items, rows, stream);
+  return launch_rows<DT, 256>(a, rt, items, rows, stream);
 }
 
 }  // namespace
@@ -1159,7 +1291,8 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   if (!aligned(q, 16) || !aligned(out, 16)) return SKINNY_ERR_UNSUPPORTED;
   const int rt = row_tiles(c, b, q_heads);
   const long long work = max_work(c, b, q_heads, rt);
-  if (work > 0x7fffffffLL) return SKINNY_ERR_UNSUPPORTED;
+  if (work > 0x7fffffffLL || max_items(b, c, q_heads, rt) * kJoinThreads > 0xffffffffLL)
+    return SKINNY_ERR_UNSUPPORTED;
   if (!workspace ||
       workspace_bytes < skinny_kv_attention_workspace_bytes(cache, batch, q_heads))
     return SKINNY_ERR_WORKSPACE;
@@ -1187,9 +1320,12 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   if (groups > kMaxGroups) groups = kMaxGroups;
   if (groups > work) groups = work;
   a.groups = (int)groups;
+  const long long items = max_items(b, c, q_heads, rt);
+  const long long most = (long long)b.tokens * (q_heads / c.kv_heads);
+  const int rows = most < 16 * rt ? (int)most : 16 * rt;
   if (c.dtype == SKINNY_KV_FP8)
-    return launch_dim<kFP8>(a, c.head_dim, rt, groups > 1, (hipStream_t)stream);
-  return launch_dim<kBF16>(a, c.head_dim, rt, groups > 1, (hipStream_t)stream);
+    return launch_dim<kFP8>(a, c.head_dim, rt, (int)items, rows, (hipStream_t)stream);
+  return launch_dim<kBF16>(a, c.head_dim, rt, (int)items, rows, (hipStream_t)stream);
 }
 
 }  // extern "C"
