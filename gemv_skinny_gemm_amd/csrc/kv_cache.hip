@@ -389,9 +389,11 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
 // the running maximum m and sum l of exp2 (scores carry log2 e): a larger
 // maximum scales the sums by 2^(m - m').
 //
-// A work item is (sequence, KV head, row group): up to ROWS = 16 RT rows, row
-// r = i * group + g being token i under query head g of the KV head, so each
-// cached byte serves every head that shares it.  A wave takes 32 keys at a
+// A work item is (sequence, KV head, row group): up to ROWS rows, row r =
+// i * group + g being token i under query head g of the KV head, so each cached
+// byte serves every head that shares it.  A workgroup's waves are RW by KW: RW
+// waves take 16 RT rows each of the same keys (the second to read a key finds
+// it in the caches), KW waves take different keys.  A wave takes 32 keys at a
 // time and keeps everything in registers:
 //   S^T = K Q^T    v_mfma_f32_16x16x32_bf16, A = 16 keys, B = 16 rows.  Lane
 //                  (c = lane % 16, g = lane / 16) ends with row c's scores of
@@ -408,16 +410,23 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
 // barrier in the loop; e4m3 codes become bf16 exactly, and a page's scale is
 // folded into the scores (k) and the probabilities (v).
 //
-// The blocks of kBlockKeys keys of all items, in order, are cut into equal
-// shares, one per workgroup (every workgroup computes the cut from the batch's
-// device arrays); each wave takes a quarter of a segment's keys.  A segment
-// that is not a whole item leaves its m, l and O in the workspace, and a
-// second launch joins an item's segments in order: no atomics, so a result
-// depends on the lengths and the grid only.
+// The blocks of 32 KW keys of all items, in order, are cut into equal shares,
+// one per workgroup (every workgroup computes the cut from the batch's device
+// arrays); each wave takes an equal run of a segment's keys.  A segment that is
+// not a whole item leaves its m, l and O in the workspace, and a second launch
+// joins an item's segments in order: no atomics, so a result depends on the
+// lengths and the grid only.  (Joining in the first launch, by the last segment
+// to arrive, was measured at 1.5 to 3 times the whole call: the fences between
+// workgroups of different XCDs write back and invalidate the L2 caches that the
+// other waves stream through.)
 
-constexpr int kBlockKeys = 128;
-constexpr int kMaxGroups = 1024;         // workgroups of the grid at most
+constexpr int kMaxGroups = 512;          // workgroups of the grid at most
 constexpr float kNegInf = -__builtin_inff();
+// m need not be the maximum itself, only near it: sums are scaled again when a
+// score passes it by more than this (probabilities then reach 2^8, far from
+// fp32's and bf16's ends).  A wave's first tiles would otherwise do so nearly
+// every time, one of its 16 rows finding a new maximum.
+constexpr float kSlack = 8.0f;
 
 struct AttnArgs {
   KvArgs kv;
@@ -425,7 +434,7 @@ struct AttnArgs {
   __bf16* out;             // [T][q_heads D]
   float* part;             // [2 grid] segments: [ROWS][D] sums, [ROWS] m, [ROWS] l
   float scale;             // softmax scale * log2 e
-  int groups;              // workgroups of the main launch
+  int groups;              // workgroups
 };
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
@@ -440,14 +449,18 @@ __device__ __forceinline__ unsigned e4m3x2_to_bf16(unsigned v) {
 
 // Blocks of one (row group, KV head) of a sequence, and its row groups.
 // An item without keys has one block, for its rows' zeros.
-__device__ __forceinline__ int seq_blocks(const Seq& q) {
-  return max(1, (q.cap + kBlockKeys - 1) / kBlockKeys);
+struct Cut {
+  int rows;       // of a row group
+  int keys;       // of a block
+};
+__device__ __forceinline__ int seq_blocks(const Seq& q, Cut cut) {
+  return max(1, (q.cap + cut.keys - 1) / cut.keys);
 }
-__device__ __forceinline__ int seq_row_groups(const Seq& q, int group, int rows) {
-  return (q.n * group + rows - 1) / rows;
+__device__ __forceinline__ int seq_row_groups(const Seq& q, int group, Cut cut) {
+  return (q.n * group + cut.rows - 1) / cut.rows;
 }
-__device__ __forceinline__ int seq_work(const KvArgs& a, const Seq& q, int rows) {
-  const long long w = (long long)seq_row_groups(q, a.group, rows) * a.kv_heads * seq_blocks(q);
+__device__ __forceinline__ int seq_work(const KvArgs& a, const Seq& q, Cut cut) {
+  const long long w = (long long)seq_row_groups(q, a.group, cut) * a.kv_heads * seq_blocks(q, cut);
   return (int)(w < kMaxCount ? w : kMaxCount);
 }
 
@@ -461,36 +474,55 @@ struct Place {
   Seq q;
 };
 
-__device__ __forceinline__ int total_work(const KvArgs& a, int rows) {
+// The sequences' work, in running sums over the wave's lanes, 64 at a time;
+// the first 64 sequences' stay in the lanes.
+struct Work {
+  Seq q;          // of sequence `lane`
+  int incl;       // blocks up to and with it
+  int total;      // blocks of all sequences
+};
+
+__device__ __forceinline__ Work all_work(const KvArgs& a, Cut cut) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
-  for (int s0 = 0; s0 < a.S; s0 += 64) {
-    const int w = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), rows) : 0;
-    total = add_count(total, lane_of(wave_scan(w), 63));
+  Work w{};
+  int own = 0;
+  if (lane < a.S) {
+    w.q = load_seq(a, lane);
+    own = seq_work(a, w.q, cut);
   }
-  return total;
+  w.incl = wave_scan(own);
+  w.total = lane_of(w.incl, 63);
+  for (int s0 = 64; s0 < a.S; s0 += 64) {
+    const int more = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), cut) : 0;
+    w.total = add_count(w.total, lane_of(wave_scan(more), 63));
+  }
+  return w;
 }
 
-__device__ __forceinline__ Place place_of(const KvArgs& a, int rows, int pos) {
+__device__ __forceinline__ Place place_of(const KvArgs& a, Cut cut, const Work& work, int pos) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
   Place p{};
-  for (int s0 = 0; s0 < a.S; s0 += 64) {
-    const int w = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), rows) : 0;
-    const int incl = add_count(wave_scan(w), before);
-    int idx;
-    const int at = scan_find(incl, before, pos, idx);
-    if (at >= 0) {
+  int idx = 0;
+  int at = scan_find(work.incl, 0, pos, idx);
+  if (at >= 0) {
+    p.s = at;
+    p.q = Seq{lane_of(work.q.q0, at), lane_of(work.q.n, at), lane_of(work.q.base, at),
+              lane_of(work.q.cap, at)};
+  } else {
+    int before = lane_of(work.incl, 63);
+    for (int s0 = 64; s0 < a.S && at < 0; s0 += 64) {
+      const int more = s0 + lane < a.S ? seq_work(a, load_seq(a, s0 + lane), cut) : 0;
+      const int incl = add_count(wave_scan(more), before);
+      at = scan_find(incl, before, pos, idx);
       p.s = s0 + at;
-      p.q = uniform(load_seq(a, p.s));
-      p.nb = seq_blocks(p.q);
-      p.rgs = seq_row_groups(p.q, a.group, rows);
-      p.item = idx / p.nb;
-      p.blk = idx % p.nb;
-      return p;
+      before = lane_of(incl, 63);
     }
-    before = lane_of(incl, 63);
+    p.q = uniform(load_seq(a, p.s));
   }
+  p.nb = seq_blocks(p.q, cut);
+  p.rgs = seq_row_groups(p.q, a.group, cut);
+  p.item = idx / p.nb;
+  p.blk = idx - p.item * p.nb;
   return p;
 }
 
@@ -635,46 +667,52 @@ __device__ __forceinline__ u32x4 v_marks(const unsigned (&raw)[8][Shape<DT, D>::
   return r;
 }
 
-template <int DT, int D, int RT>
-__global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs a) {
+template <int DT, int D, int RT, int RW, int NW>
+__global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs a) {
   using Sh = Shape<DT, D>;
-  constexpr int ROWS = 16 * RT;
+  constexpr int KW = NW / RW;
+  constexpr int kWaveRows = 16 * RT;
+  constexpr int ROWS = kWaveRows * RW;
+  constexpr int kAll = 64 * NW;                      // threads
   constexpr int kStride = D + 4;                     // LDS row of the waves' sums, padded
-  __shared__ float sums[kWaves][16][kStride];
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  constexpr Cut cut{ROWS, 32 * KW};
+  __shared__ __attribute__((aligned(16))) float sums[NW][16][kStride];
+  __shared__ float sm[NW][16], sl[NW][16];
   const KvArgs& kv = a.kv;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = uniform(tid >> 6);
+  const int rw = wave % RW, kw = wave / RW;
   const int c = lane & 15, g = lane >> 4;
   const int P = 1 << kv.log2p;
   const int q_heads = kv.kv_heads * kv.group;
 
-  const int total = total_work(kv, ROWS);
-  const Shares shares(total, a.groups);
+  const Work work = all_work(kv, cut);
+  const Shares shares(work.total, a.groups);
   int pos = shares.begin(blockIdx.x);
   const int end = shares.begin(blockIdx.x + 1);
 
   while (pos < end) {
-    const Place pl = place_of(kv, ROWS, pos);
+    const Place pl = place_of(kv, cut, work, pos);
     const int h = pl.item / pl.rgs, rg = pl.item % pl.rgs;
     const int blocks = min(pl.nb - pl.blk, end - pos);
     const Seq q = pl.q;
     const int row_count = min(q.n * kv.group - rg * ROWS, ROWS);
-    const int tok_lo = rg * ROWS / kv.group;
-    const int tok_hi = (rg * ROWS + row_count - 1) / kv.group;
-    // Keys seen by the group's first and last row.
-    const int lim_lo = min(max(q.base + tok_lo + 1, 0), q.cap);
-    const int lim_hi = min(max(q.base + tok_hi + 1, 0), q.cap);
+    // This wave's rows, and the keys seen by the first and the last of them.
+    const int row0 = rg * ROWS + rw * kWaveRows;
+    const int wave_rows = min(row_count - rw * kWaveRows, kWaveRows);
+    const int lim_lo = min(max(q.base + row0 / kv.group + 1, 0), q.cap);
+    const int lim_hi = wave_rows <= 0 ? 0
+        : min(max(q.base + (row0 + wave_rows - 1) / kv.group + 1, 0), q.cap);
 
-    // Rows: row rt * 16 + c of the group in this lane's column.
+    // Row rt * 16 + c of the wave's rows in this lane's column.
     u32x4 qf[RT][Sh::kSteps];
     int lim[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int r = rg * ROWS + rt * 16 + c;
+      const int r = row0 + rt * 16 + c;
       const int tok = r / kv.group, head = r % kv.group;
-      const bool live = rt * 16 + c < row_count;
+      const bool live = rt * 16 + c < wave_rows;
       lim[rt] = live ? min(max(q.base + tok + 1, 0), q.cap) : lim_hi;
       const __bf16* src = a.q + ((size_t)(q.q0 + tok) * q_heads + h * kv.group + head) * D;
 #pragma unroll
@@ -695,8 +733,8 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
       for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] = f32x4{0, 0, 0, 0};
     }
 
-    // This wave's keys: tiles of 32, a quarter of the segment's blocks.
-    const int key0 = (pl.blk * 4 + wave * blocks) * 32;
+    // This wave's keys: as many tiles of 32 as the segment has blocks.
+    const int key0 = (pl.blk * KW + kw * blocks) * 32;
     const int tiles = min(max((lim_hi - key0 + 31) / 32, 0), blocks);
     const int* table = kv.table + (size_t)pl.s * kv.max_pages;
     const int last_page = max(q.cap - 1, 0) >> kv.log2p;
@@ -817,12 +855,12 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
 #pragma unroll
           for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][u][r]);
         top = row_max(top);
-        if (__any(top > m[rt])) {
+        if (__any(top > m[rt] + kSlack)) {
           const float f = top > m[rt] ? __builtin_amdgcn_exp2f(m[rt] - top) : 1.0f;
           l[rt] *= f;
 #pragma unroll
           for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] *= f;
-          m[rt] = top;
+          m[rt] = fmaxf(m[rt], top);
         }
         const float ref = m[rt] == kNegInf ? 0.0f : m[rt];
         float p[8];
@@ -893,7 +931,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
       }
     }
 
-    // The four waves' sums, 16 rows at a time.
+    // The waves' sums, 16 rows of each row wave at a time.
     const bool whole = blocks == pl.nb;
     float* part = a.part + (size_t)(2 * blockIdx.x + (pl.blk == 0 ? 1 : 0)) * part_floats<D>(ROWS);
 #pragma unroll
@@ -910,23 +948,23 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
         for (int j = 0; j < Sh::kTiles; ++j)
           sums[wave][c][(4 * g + r) * Sh::kTiles + j] = o[rt][j][r];
       __syncthreads();
-      for (int i = tid; i < 16 * (D / 8); i += kThreads) {
-        const int rr = i / (D / 8), d = i % (D / 8) * 8;
-        const int row = rt * 16 + rr;
+      for (int i = tid; i < 16 * RW * (D / 8); i += kAll) {
+        const int d = i % (D / 8) * 8, rr = i / (D / 8) % 16, w0 = i / (D / 8) / 16;
+        const int row = w0 * kWaveRows + rt * 16 + rr;
         if (row < row_count) {
           float top = kNegInf;
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][rr]);
+          for (int w = 0; w < KW; ++w) top = fmaxf(top, sm[w * RW + w0][rr]);
           float sum = 0.0f;
           float x[8] = {};
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
+          for (int w = 0; w < KW; ++w) {
+            const float mw = sm[w * RW + w0][rr], lw2 = sl[w * RW + w0][rr];
             // Without a maximum l is 0 (no key seen) or NaN (a score was).
-            const float f = sm[w][rr] == kNegInf ? sl[w][rr]
-                                                 : __builtin_amdgcn_exp2f(sm[w][rr] - top);
-            sum += f * sl[w][rr];
+            const float f = mw == kNegInf ? lw2 : __builtin_amdgcn_exp2f(mw - top);
+            sum += f * lw2;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += f * sums[w][rr][d + e];
+            for (int e = 0; e < 8; ++e) x[e] += f * sums[w * RW + w0][rr][d + e];
           }
           if (whole) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -954,17 +992,23 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_attention_k(const AttnArgs
   }
 }
 
-// Joins the segments of item blockIdx.x, row blockIdx.y: kGroups groups of D / 4
-// lanes take every kGroups-th segment, in order, and are added in order.
+// Joins the segments of item blockIdx.x, kJoinRows<D> of its rows from blockIdx.y
+// on: per row D / 4 lanes (4 values each) in kJoinSets sets that take every
+// kJoinSets-th segment, kJoinAhead of them in flight, with the running maximum
+// and sum of a softmax; the sets' results are then added in order.
 constexpr int kJoinThreads = 512;
+constexpr int kJoinSets = 4;
+constexpr int kJoinAhead = 8;
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const AttnArgs a, int rows) {
-  constexpr int kLanes = D / 4;                      // lanes of a row, 4 values each
-  constexpr int kGroups = kJoinThreads / kLanes;
-  __shared__ f32x4 sx[kGroups][kLanes];
-  __shared__ float sl[kGroups], sm[kGroups];
+constexpr int kJoinRows = kJoinThreads / (kJoinSets * (D / 4));
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const AttnArgs a, Cut cut) {
+  constexpr int kLanes = D / 4;
+  __shared__ f32x4 sx[kJoinSets][kJoinRows<D>][kLanes];
+  __shared__ float st[kJoinSets][kJoinRows<D>], sl[kJoinSets][kJoinRows<D>];
   const KvArgs& kv = a.kv;
   const int lane = threadIdx.x & 63;
+  const int rows = cut.rows;
   // The item's sequence, its first block, and the number of all blocks.
   int items = 0, total = 0, at_item = -1, first = 0;
   Seq q{};
@@ -973,69 +1017,89 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
     int n = 0, w = 0;
     if (s0 + lane < kv.S) {
       mine = load_seq(kv, s0 + lane);
-      n = seq_row_groups(mine, kv.group, rows) * kv.kv_heads;
-      w = seq_work(kv, mine, rows);
+      n = seq_row_groups(mine, kv.group, cut) * kv.kv_heads;
+      w = seq_work(kv, mine, cut);
     }
     const int ni = add_count(wave_scan(n), items), wi = add_count(wave_scan(w), total);
     int idx;
     const int at = at_item < 0 ? scan_find(ni, items, blockIdx.x, idx) : -1;
     if (at >= 0) {
       at_item = idx;
-      q = uniform(load_seq(kv, s0 + at));
-      first = (at ? lane_of(wi, max(at - 1, 0)) : total) + idx * seq_blocks(q);
+      q = Seq{lane_of(mine.q0, at), lane_of(mine.n, at), lane_of(mine.base, at),
+              lane_of(mine.cap, at)};
+      first = (at ? lane_of(wi, max(at - 1, 0)) : total) + idx * seq_blocks(q, cut);
     }
     items = lane_of(ni, 63);
     total = lane_of(wi, 63);
   }
   if (at_item < 0) return;
-  const int nb = seq_blocks(q);
+  const int nb = seq_blocks(q, cut);
   const Shares shares(total, a.groups);
-  const int b0 = shares.of(first), b1 = shares.of(first + nb - 1);
-  if (b0 == b1) return;                              // one share holds the whole item
-  const int rgs = seq_row_groups(q, kv.group, rows);
+  const int b0 = shares.of(first), n = shares.of(first + nb - 1) - b0 + 1;
+  if (n == 1) return;                                // one share holds the whole item
+  const int rgs = seq_row_groups(q, kv.group, cut);
   const int h = at_item / rgs, rg = at_item % rgs;
-  const int row = blockIdx.y;
-  if (rg * rows + row >= q.n * kv.group) return;
+  const int row_count = min(q.n * kv.group - rg * rows, rows);
+  const int d = threadIdx.x % kLanes, set = threadIdx.x / kLanes % kJoinSets;
+  const int slot = threadIdx.x / (kLanes * kJoinSets);
+  const int row = blockIdx.y * kJoinRows<D> + slot;
+  if (blockIdx.y * kJoinRows<D> >= row_count) return;
+  const int from = min(row, row_count - 1);
+  // Segment k is share b0 + k's; the item's first one stands second in its share's pair.
   const size_t stride = part_floats<D>(rows);
-  // Segment k is share b0 + k's: the item's first one stands second in its share's pair.
-  const int n = b1 - b0 + 1;
   const float* part = a.part + (size_t)(2 * b0) * stride;
-  const int d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  float top = kNegInf;
-  for (int k = threadIdx.x; k < n; k += kJoinThreads)
-    top = fmaxf(top, part[(2 * k + (k == 0)) * stride + rows * D + row]);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-  if (lane == 0) sm[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, sm[w]);
-  float sum = 0.0f;
+  float top = kNegInf, sum = 0.0f;
   f32x4 x{0, 0, 0, 0};
-#pragma unroll 4
-  for (int k = grp; k < n; k += kGroups) {
-    const float* s = part + (2 * k + (k == 0)) * stride;
-    const float mk = s[rows * D + row], lk = s[rows * D + rows + row];
-    const f32x4 y = *reinterpret_cast<const f32x4*>(s + row * D + 4 * d);
-    const float f = mk == kNegInf ? lk : __builtin_amdgcn_exp2f(mk - top);
-    sum += f * lk;
-    x += f * y;
-  }
-  sx[grp][d] = x;
-  if (d == 0) sl[grp] = sum;
-  __syncthreads();
-  if (grp == 0) {
+  for (int k0 = set; k0 < n; k0 += kJoinSets * kJoinAhead) {
+    float mk[kJoinAhead], lk[kJoinAhead];
+    f32x4 y[kJoinAhead];
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
-      x += sx[i][d];
-      sum += sl[i];
+    for (int e = 0; e < kJoinAhead; ++e) {
+      const int k = min(k0 + e * kJoinSets, n - 1);
+      const float* s = part + (size_t)(2 * k + (k == 0 ? 1 : 0)) * stride;
+      mk[e] = s[rows * D + from];
+      lk[e] = s[rows * D + rows + from];
+      y[e] = *reinterpret_cast<const f32x4*>(s + from * D + 4 * d);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int r = rg * rows + row;
-    *reinterpret_cast<u32x2*>(a.out + ((size_t)(q.q0 + r / kv.group) * kv.kv_heads * kv.group +
-                                       h * kv.group + r % kv.group) * D + 4 * d) =
-        u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
+    float next = top;
+#pragma unroll
+    for (int e = 0; e < kJoinAhead; ++e) next = fmaxf(next, mk[e]);
+    const float f0 = top == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(top - next);
+    sum *= f0;
+    x *= f0;
+    top = next;
+#pragma unroll
+    for (int e = 0; e < kJoinAhead; ++e)
+      if (k0 + e * kJoinSets < n) {
+        // Without a maximum l is 0 (no key seen) or NaN (a score was).
+        const float f = mk[e] == kNegInf ? lk[e] : __builtin_amdgcn_exp2f(mk[e] - top);
+        sum += f * lk[e];
+        x += f * y[e];
+      }
   }
+  sx[set][slot][d] = x;
+  if (d == 0) {
+    st[set][slot] = top;
+    sl[set][slot] = sum;
+  }
+  __syncthreads();
+  if (set != 0 || row >= row_count) return;
+#pragma unroll
+  for (int k = 1; k < kJoinSets; ++k) top = fmaxf(top, st[k][slot]);
+  sum = 0.0f;
+  x = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < kJoinSets; ++k) {
+    const float tk = st[k][slot], lk = sl[k][slot];
+    const float f = tk == kNegInf ? lk : __builtin_amdgcn_exp2f(tk - top);
+    sum += tk == kNegInf ? lk : f * lk;
+    x += f * sx[k][slot][d];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int r = rg * rows + row;
+  *reinterpret_cast<u32x2*>(a.out + ((size_t)(q.q0 + r / kv.group) * kv.kv_heads * kv.group +
+                                     h * kv.group + r % kv.group) * D + 4 * d) =
+      u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
 }
 
 // ---------------------------------------------------------------------------
@@ -1127,72 +1191,85 @@ skinny_status check_heads(const skinny_kv_cache& c, int q_heads) {
   return SKINNY_OK;
 }
 
-// Row tiles per item: the rows of an average sequence under one KV head, as
-// many as a wave's registers hold beside a tile of keys and values.
+// How a launch cuts an item's rows: RT tiles of 16 rows per wave, RW row waves
+// of the workgroup's NW.  RT is what fits beside a tile of keys and values in
+// the registers of two waves per SIMD (one at head_dim 256, whose workgroups
+// have four waves); RW grows with the rows of an average sequence under one KV
+// head.
+struct RowCut {
+  int rt, rw;
+};
 constexpr int most_row_tiles(int dtype, int head_dim) {
-  return head_dim < 256 ? 4 : dtype == SKINNY_KV_FP8 ? 2 : 1;
+  return head_dim == 64 || (head_dim == 128 && dtype == SKINNY_KV_FP8) ? 2 : 1;
 }
-int row_tiles(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
-  const int most = most_row_tiles(c.dtype, c.head_dim);
+constexpr int waves_of(int head_dim) { return head_dim == 256 ? 4 : 8; }
+RowCut row_cut(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
   const long long tokens = (b.tokens + b.seqs - 1) / b.seqs;
-  const long long t = (tokens * (q_heads / c.kv_heads) + 15) / 16;
-  return t < most ? (int)t : most;
+  const long long rows = tokens * (q_heads / c.kv_heads);
+  RowCut r{1, 1};
+  if (rows <= 16) return r;
+  r.rt = most_row_tiles(c.dtype, c.head_dim);
+  const int most = 8 / r.rt < waves_of(c.head_dim) ? 8 / r.rt : waves_of(c.head_dim);
+  while (r.rw < most && 16 * r.rt * r.rw < rows) r.rw *= 2;
+  return r;
 }
 
-// Row groups of all sequences at most.
-long long max_row_groups(const skinny_kv_batch& b, int group, int rt) {
-  const long long rows = (long long)b.tokens * group;
-  const long long r = rows / (16 * rt) + (b.seqs < b.tokens ? b.seqs : b.tokens);
-  return r < rows ? r : rows;
-}
-
-long long max_items(const skinny_kv_batch& b, const skinny_kv_cache& c, int q_heads, int rt) {
-  return max_row_groups(b, q_heads / c.kv_heads, rt) * c.kv_heads;
+// Items (row groups under each KV head) of all sequences at most.
+long long max_items(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads, RowCut r) {
+  const long long rows = (long long)b.tokens * (q_heads / c.kv_heads);
+  const long long g = rows / (16 * r.rt * r.rw) + (b.seqs < b.tokens ? b.seqs : b.tokens);
+  return (g < rows ? g : rows) * c.kv_heads;
 }
 
 // Blocks of all items at most: every sequence at the page table's length.
-long long max_work(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads, int rt) {
+long long max_work(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads, RowCut r) {
   const long long keys = (long long)b.max_pages * c.page_tokens;
-  return max_items(b, c, q_heads, rt) * ((keys + kBlockKeys - 1) / kBlockKeys);
+  const long long block = 32 * (waves_of(c.head_dim) / r.rw);
+  return max_items(c, b, q_heads, r) * ((keys + block - 1) / block);
 }
 
 size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
-  const int rt = row_tiles(c, b, q_heads);
-  const long long w = max_work(c, b, q_heads, rt);
+  const RowCut r = row_cut(c, b, q_heads);
+  const long long w = max_work(c, b, q_heads, r);
   const long long groups = w < kMaxGroups ? w : kMaxGroups;
-  return (size_t)(2 * groups) * (16 * rt) * (c.head_dim + 2) * sizeof(float);
+  return (size_t)(2 * groups) * (16 * r.rt * r.rw) * (c.head_dim + 2) * sizeof(float);
 }
 
-constexpr int kGroupsPerCU = 2;
+constexpr int kGroupsPerCU = 1;
 
-template <int DT, int D, int RT>
+template <int DT, int D, int RT, int RW>
 skinny_status launch_attention(const AttnArgs& a, int items, int rows, hipStream_t stream) {
-  hipLaunchKernelGGL((skinny_kv_attention_k<DT, D, RT>), dim3(a.groups), dim3(kThreads), 0, stream, a);
+  constexpr int NW = waves_of(D);
+  constexpr int ROWS = 16 * RT * RW;
+  hipLaunchKernelGGL((skinny_kv_attention_k<DT, D, RT, RW, NW>), dim3(a.groups), dim3(64 * NW), 0,
+                     stream, a);
   if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
   if (a.groups == 1) return SKINNY_OK;               // nothing is split
-  hipLaunchKernelGGL((skinny_kv_attention_join<D>), dim3(items, rows), dim3(kJoinThreads), 0, stream,
-                     a, 16 * RT);
+  if (rows > ROWS) rows = ROWS;
+  hipLaunchKernelGGL((skinny_kv_attention_join<D>),
+                     dim3(items, (rows + kJoinRows<D> - 1) / kJoinRows<D>), dim3(kJoinThreads), 0,
+                     stream, a, Cut{ROWS, 32 * (NW / RW)});
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 
 template <int DT, int D>
-skinny_status launch_rows(const AttnArgs& a, int rt, int items, int rows, hipStream_t stream) {
-  constexpr int kMost = most_row_tiles(DT, D);
-  if (rt == 1) return launch_attention<DT, D, 1>(a, items, rows, stream);
-  if constexpr (kMost >= 2)
-    if (rt == 2) return launch_attention<DT, D, 2>(a, items, rows, stream);
-  if constexpr (kMost >= 4) {
-    if (rt == 3) return launch_attention<DT, D, 3>(a, items, rows, stream);
-    if (rt == 4) return launch_attention<DT, D, 4>(a, items, rows, stream);
-  }
+skinny_status launch_rows(const AttnArgs& a, RowCut r, int items, int rows,
+                          hipStream_t stream) {
+  constexpr int RT = most_row_tiles(DT, D);
+  if (r.rt == 1 && r.rw == 1) return launch_attention<DT, D, 1, 1>(a, items, rows, stream);
+  if (r.rw == 2) return launch_attention<DT, D, RT, 2>(a, items, rows, stream);
+  if (r.rw == 4) return launch_attention<DT, D, RT, 4>(a, items, rows, stream);
+  if constexpr (RT == 2) return launch_attention<DT, D, 2, 1>(a, items, rows, stream);
+  if constexpr (RT == 1 && waves_of(D) == 8) return launch_attention<DT, D, 1, 8>(a, items, rows, stream);
   return SKINNY_ERR_UNSUPPORTED;
 }
 
 template <int DT>
-skinny_status launch_dim(const AttnArgs& a, int d, int rt, int items, int rows, hipStream_t stream) {
-  if (d == 64) return launch_rows<DT, 64>(a, rt, items, rows, stream);
-  if (d == 128) return launch_rows<DT, 128>(a, rt, items, rows, stream);
-  return launch_rows<DT, 256>(a, rt, items, rows, stream);
+skinny_status launch_dim(const AttnArgs& a, int d, RowCut r, int items, int rows,
+                          hipStream_t stream) {
+  if (d == 64) return launch_rows<DT, 64>(a, r, items, rows, stream);
+  if (d == 128) return launch_rows<DT, 128>(a, r, items, rows, stream);
+  return launch_rows<DT, 256>(a, r, items, rows, stream);
 }
 
 }  // namespace
@@ -1289,10 +1366,10 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   const skinny_kv_batch& b = *batch;
   if (!q || !out || !(scale - scale == 0.0f)) return SKINNY_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return SKINNY_ERR_UNSUPPORTED;
-  const int rt = row_tiles(c, b, q_heads);
-  const long long work = max_work(c, b, q_heads, rt);
-  if (work > 0x7fffffffLL || max_items(b, c, q_heads, rt) * kJoinThreads > 0xffffffffLL)
-    return SKINNY_ERR_UNSUPPORTED;
+  const RowCut r = row_cut(c, b, q_heads);
+  const long long work = max_work(c, b, q_heads, r);
+  const long long items = max_items(c, b, q_heads, r);
+  if (work >= kMaxCount || items * kJoinThreads > 0xffffffffLL) return SKINNY_ERR_UNSUPPORTED;
   if (!workspace ||
       workspace_bytes < skinny_kv_attention_workspace_bytes(cache, batch, q_heads))
     return SKINNY_ERR_WORKSPACE;
@@ -1320,12 +1397,11 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   if (groups > kMaxGroups) groups = kMaxGroups;
   if (groups > work) groups = work;
   a.groups = (int)groups;
-  const long long items = max_items(b, c, q_heads, rt);
-  const long long most = (long long)b.tokens * (q_heads / c.kv_heads);
-  const int rows = most < 16 * rt ? (int)most : 16 * rt;
+  const long long rows = (long long)b.tokens * (q_heads / c.kv_heads);
+  const int most = rows < 128 ? (int)rows : 128;     // rows of an item at most
   if (c.dtype == SKINNY_KV_FP8)
-    return launch_dim<kFP8>(a, c.head_dim, rt, (int)items, rows, (hipStream_t)stream);
-  return launch_dim<kBF16>(a, c.head_dim, rt, (int)items, rows, (hipStream_t)stream);
+    return launch_dim<kFP8>(a, c.head_dim, r, (int)items, most, (hipStream_t)stream);
+  return launch_dim<kBF16>(a, c.head_dim, r, (int)items, most, (hipStream_t)stream);
 }
 
 }  // extern "C"
