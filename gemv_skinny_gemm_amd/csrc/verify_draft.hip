@@ -20,10 +20,15 @@
 //     logit of kSlice, the first place of it, and the sum of exp((l - max) / t);
 //   skinny_verify_pick    workgroup (slice, sequence): from the rows' slices,
 //     the normalisers and with them the first row that stops (each workgroup
-//     the same, in the same order), then its slice's sum of the weights to
-//     sample from, max(0, p - q).  The sequence's last workgroup to arrive
-//     (a counter that the first launch cleared) finds the slice, then the
-//     entry, where the running sum passes u times the total.
+//     the same, in the same order), then its waves' sums of the weights to
+//     sample from, max(0, p - q), over kSub entries each.  The sequence's last
+//     workgroup to arrive (a counter that the first launch cleared) finds the
+//     entries of kSub, then the entry, where the running sum passes u times the
+//     total; sums are added in index order, so it does not matter who came last.
+// The sums pass between workgroups as relaxed device-scope words that the first
+// launch set to a mark: a word read before it arrived is read again.  Fences in
+// their place cost about 8 us a call here (they write back and invalidate an
+// XCD's whole L2).
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -45,11 +50,16 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 constexpr int kSlice = 4096;                       // logits per workgroup
-constexpr int kPer = kSlice / kThreads;            // per thread
+constexpr int kSub = kSlice / kWaves;              // per wave
+constexpr int kPer = kSub / 64;                    // per lane
 constexpr int kRowLanes = 16;                      // lanes that read one row's slices
 constexpr int kRowsAtOnce = kThreads / kRowLanes;
+constexpr int kFind = kSub / kThreads;             // entries of a thread in the last search
 constexpr float kNegInf = -__builtin_inff();
+constexpr unsigned long long kNotYet = ~0ull;      // a NaN that no sum is
+constexpr int kMaxPolls = 1 << 16;
 
 struct Stat {
   double sum;            // sum over the slice of exp((l - max) / t)
@@ -68,7 +78,7 @@ struct VerifyArgs {
   int* out_tokens;       // [T]
   int* accepted;         // [S]
   Stat* stats;           // [2][T][slices]
-  double* weight;        // [S][slices]
+  unsigned long long* weight;   // [S][slices][kWaves] fp64
   int* arrived;          // [S]
   int T, S, V, slices;
 };
@@ -88,36 +98,87 @@ __device__ __forceinline__ float temperature_of(const VerifyArgs& a, int s) {
   return a.temperature ? a.temperature[s] : 1.0f;
 }
 
-// exp(x) for x <= 0 in fp64: x = n ln 2 + r, |r| <= ln 2 / 2, and the Taylor
-// series of exp(r) to r^12 (the next term is below 2^-52).  Below -700, and
-// for NaN, 0.
-__device__ __forceinline__ double exp_below(double x) {
-  constexpr double kLog2e = 1.4426950408889634074, kLn2Hi = 0x1.62e42fefa39efp-1,
-                   kLn2Lo = 0x1.abc9e3b39803fp-56;
-  const double n = rint(x * kLog2e);
-  const double r = fma(-n, kLn2Lo, fma(-n, kLn2Hi, x));
-  double p = 1.0 / 479001600.0;
-  p = fma(p, r, 1.0 / 39916800.0);
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
-  const double y = __builtin_ldexp(p, (int)fmax(n, -1100.0));
-  return x >= -700.0 ? y : 0.0;
+// 2^y for -1000 <= y <= 0 in fp64: y = n + f, |f| <= 1/2, n from the low bits of
+// y + 1.5 * 2^52, and the Taylor series of exp(f ln 2) to the 11th power (the
+// next term is below 2^-47 of it); n is added to the exponent's bits.  Below
+// that, and for NaN, 0.
+struct Taylor {
+  double c[12];
+  constexpr Taylor() : c{} {
+    c[0] = 1.0;
+    for (int k = 1; k < 12; ++k) c[k] = c[k - 1] * 0.69314718055994530942 / k;
+  }
+};
+__device__ __forceinline__ double exp2_below(double y) {
+  constexpr Taylor t;
+  constexpr double kShift = 6755399441055744.0;    // 1.5 * 2^52
+  const double s = y + kShift;
+  const double f = y - (s - kShift);
+  double p = t.c[11];
+#pragma unroll
+  for (int k = 10; k >= 0; --k) p = fma(p, f, t.c[k]);
+  const unsigned long long n = __builtin_bit_cast(unsigned long long, s) << 52;
+  const double r = __builtin_bit_cast(double, __builtin_bit_cast(unsigned long long, p) + n);
+  return y >= -1000.0 ? r : 0.0;
 }
 
-// exp((l - max) / t) with inv = 1 / t: 1 at the maximum (an infinite one too),
-// 0 for NaN and -inf.
-__device__ __forceinline__ double weight_of(float l, float top, double inv) {
-  if (l == top) return top > kNegInf ? 1.0 : 0.0;
-  return exp_below(((double)l - (double)top) * inv);
+// exp((l - top) / t) with c = log2 e / t: 1 at the maximum (an infinite one
+// too), 0 for NaN and -inf.
+__device__ __forceinline__ double weight_of(float l, float top, double c) {
+  const double w = exp2_below(((double)l - (double)top) * c);
+  return l == top ? (top > kNegInf ? 1.0 : 0.0) : w;
+}
+
+// Lane exchanges on the vector ALUs: rotation within 16 lanes, and with the
+// lanes 16 and 32 away.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, true);
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(int, x)));
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp(double x) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+  const unsigned lo = (unsigned)dpp<CTRL, ROWS>((int)(unsigned)u);
+  const unsigned hi = (unsigned)dpp<CTRL, ROWS>((int)(unsigned)(u >> 32));
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+constexpr int kRor = 0x120, kShr = 0x110, kBcast15 = 0x142, kBcast31 = 0x143;
+
+template <typename T, typename F>
+__device__ __forceinline__ T reduce16(T x, F f) {
+  x = f(x, dpp<kRor + 1>(x));
+  x = f(x, dpp<kRor + 2>(x));
+  x = f(x, dpp<kRor + 4>(x));
+  return f(x, dpp<kRor + 8>(x));
+}
+template <typename T, typename F>
+__device__ __forceinline__ T reduce64(T x, F f) {
+  x = reduce16(x, f);
+  x = f(x, __shfl_xor(x, 16));
+  return f(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ int lower(int a, int b) { return min(a, b); }
+__device__ __forceinline__ double plus(double a, double b) { return a + b; }
+
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ double scan64(double x) {
+  x += dpp<kShr + 1>(x);
+  x += dpp<kShr + 2>(x);
+  x += dpp<kShr + 4>(x);
+  x += dpp<kShr + 8>(x);
+  x += dpp<kBcast15, 0xa>(x);
+  return x + dpp<kBcast31, 0xc>(x);
+}
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+  const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)u, lane);
+  const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(u >> 32), lane);
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
 }
 
 template <typename L>
@@ -142,15 +203,15 @@ __device__ __forceinline__ void load_vec(const void* p, size_t at, float* out) {
   }
 }
 
-// A thread's kPer logits of a slice that begins at n0, as runs of kVec
-// neighbours (VEC) or single ones, NaN past the end; index of the j-th.
+// A lane's kPer of the kSub logits from n0 on, as runs of kVec neighbours (VEC)
+// or single ones, NaN past the end; place of the j-th.
 template <typename L, bool VEC>
 __device__ __forceinline__ int index_of(int j) {
   constexpr int W = VEC ? kVec<L> : 1;
-  return (j / W * kThreads + (int)threadIdx.x) * W + j % W;
+  return (j / W * 64 + (int)(threadIdx.x & 63)) * W + j % W;
 }
 template <typename L, bool VEC>
-__device__ __forceinline__ void load_slice(const void* row, int n0, int V, float (&l)[kPer]) {
+__device__ __forceinline__ void load_sub(const void* row, int n0, int V, float (&l)[kPer]) {
   if constexpr (VEC) {
     constexpr int W = kVec<L>;
 #pragma unroll
@@ -166,15 +227,10 @@ __device__ __forceinline__ void load_slice(const void* row, int n0, int V, float
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int n = n0 + index_of<L, false>(j);
-      l[j] = n < V ? logit<L>(row, n) : __builtin_nanf("");
+      const float x = logit<L>(row, min(n, V - 1));
+      l[j] = n < V ? x : __builtin_nanf("");
     }
   }
-}
-
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
-  return x;
 }
 
 __device__ __forceinline__ void take_first(float v, int i, float& bv, int& bi) {
@@ -198,10 +254,21 @@ __device__ __forceinline__ int find_row(const VerifyArgs& a, int t) {
 
 template <typename L, bool VEC>
 __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs a) {
+  __shared__ float sv[kWaves];
+  __shared__ int si[kWaves];
+  __shared__ double ss[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int slice = blockIdx.x, row = blockIdx.y, which = blockIdx.z;
-  if (slice == 0 && row == 0 && which == 0)
-    for (int i = tid; i < a.S; i += kThreads) a.arrived[i] = 0;
+  const void* src = static_cast<const L*>(which ? a.draft : a.logits) + (size_t)row * a.V;
+  const int n0 = slice * kSlice + wave * kSub;
+  float l[kPer];
+  load_sub<L, VEC>(src, n0, a.V, l);               // on its way while the row's sequence is found
+  if (row == 0 && which == 0) {
+    for (int i = tid; i < a.S * kWaves; i += kThreads)
+      a.weight[((size_t)(i / kWaves) * a.slices + slice) * kWaves + i % kWaves] = kNotYet;
+    if (slice == 0)
+      for (int i = tid; i < a.S; i += kThreads) a.arrived[i] = 0;
+  }
   const int s = find_row(a, row);
   if (s < 0) return;
   const Rows r = rows_of(a, s);
@@ -209,67 +276,69 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   const bool greedy = !(t > 0.0f);
   // The draft's last row drafted nothing, and a greedy sequence asks only the target.
   if (which == 1 && (greedy || row + 1 == r.q0 + r.n)) return;
-  const void* src = static_cast<const L*>(which ? a.draft : a.logits) + (size_t)row * a.V;
-  const int n0 = slice * kSlice;
-  float l[kPer];
-  load_slice<L, VEC>(src, n0, a.V, l);
+  // Each wave's maximum and sum, then the four joined.
   float top = kNegInf;
   int first = a.V;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) take_first(l[j], n0 + index_of<L, VEC>(j), top, first);
+  const float wtop = reduce64(top, larger);
+  first = reduce64(top == wtop ? first : a.V, lower);
+  double sum = 0.0;
+  const double c = 1.4426950408889634074 / (double)t;
+  if (!greedy) {
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const float ov = __shfl_xor(top, off);
-    const int oi = __shfl_xor(first, off);
-    take_first(ov, oi, top, first);
+    for (int j = 0; j < kPer; ++j) sum += weight_of(l[j], wtop, c);
+    sum = reduce64(sum, plus);
   }
-  __shared__ float sv[kThreads / 64];
-  __shared__ int si[kThreads / 64];
-  __shared__ double ss[kThreads / 64];
   if (lane == 0) {
-    sv[wave] = top;
+    sv[wave] = wtop;
     si[wave] = first;
+    ss[wave] = sum;
   }
   __syncthreads();
+  if (wave != 0) return;
+  const int w = lane & (kWaves - 1);
+  top = sv[w];
+  first = si[w];
+  float all = top;
+  int at = first;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) take_first(sv[w], si[w], top, first);
-  double sum = 0.0;
-  if (!greedy) {
-    const double inv = 1.0 / (double)t;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) sum += weight_of(l[j], top, inv);
-    sum = wave_sum(sum);
-    if (lane == 0) ss[wave] = sum;
-    __syncthreads();
-    sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
-  }
-  if (tid == 0)
-    a.stats[((size_t)which * a.T + row) * a.slices + slice] = Stat{sum, top, first};
+  for (int k = 0; k < kWaves; ++k) take_first(sv[k], si[k], all, at);
+  sum = greedy ? 0.0 : ss[w] * weight_of(top, all, c);
+  sum += dpp<kRor + 1>(sum);
+  sum += dpp<kRor + 2>(sum);
+  if (lane == 0) a.stats[((size_t)which * a.T + row) * a.slices + slice] = Stat{sum, all, at};
 }
 
 // A row's maximum, where it first is, and the sum of weights, from its slices:
-// the same in all kRowLanes lanes.
+// kRowLanes lanes take every kRowLanes-th, kAhead at a time, and end with the same.
 struct RowStat {
   float top;
   int first;
   double sum;
 };
-__device__ __forceinline__ RowStat row_stat(const Stat* st, int slices, double inv) {
-  const int l = threadIdx.x & (kRowLanes - 1);
-  RowStat r{kNegInf, 0x7fffffff, 0.0};
-  for (int i = l; i < slices; i += kRowLanes) take_first(st[i].max, st[i].first, r.top, r.first);
+constexpr int kAhead = 4;
+__device__ __forceinline__ void load_stats(const Stat* st, int i0, int slices, Stat (&x)[kAhead]) {
 #pragma unroll
-  for (int off = kRowLanes / 2; off > 0; off >>= 1) {
-    const float ov = __shfl_xor(r.top, off);
-    const int oi = __shfl_xor(r.first, off);
-    take_first(ov, oi, r.top, r.first);
+  for (int e = 0; e < kAhead; ++e) {
+    const int i = i0 + e * kRowLanes;
+    x[e] = st[min(i, slices - 1)];
+    if (i >= slices) x[e] = Stat{0.0, kNegInf, 0x7fffffff};
   }
-  if (inv > 0.0) {
-    for (int i = l; i < slices; i += kRowLanes) r.sum += st[i].sum * weight_of(st[i].max, r.top, inv);
+}
+__device__ __forceinline__ void add_stats(const Stat (&x)[kAhead], double c, RowStat& r) {
+  const float had = r.top;
 #pragma unroll
-    for (int off = kRowLanes / 2; off > 0; off >>= 1) r.sum += __shfl_xor(r.sum, off);
-  }
-  return r;
+  for (int e = 0; e < kAhead; ++e) take_first(x[e].max, x[e].first, r.top, r.first);
+  r.sum *= weight_of(had, r.top, c);
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e) r.sum += x[e].sum * weight_of(x[e].max, r.top, c);
+}
+__device__ __forceinline__ void row_end(double c, RowStat& r) {
+  const float had = r.top;
+  r.top = reduce16(r.top, larger);
+  r.first = reduce16(had == r.top ? r.first : 0x7fffffff, lower);
+  r.sum = reduce16(r.sum * weight_of(had, r.top, c), plus);
 }
 
 // Of the row that stops a sequence: what its weights are made of.
@@ -284,84 +353,93 @@ struct Stop {
 // max(0, p - q) of one entry; `plain`: p itself.  Both products are rounded
 // before the difference (no fused multiply-add), so equal rows leave exactly 0.
 template <typename L>
-__device__ __forceinline__ double residual(const Stop& st, double inv, float lp, float lq, int n,
+__device__ __forceinline__ double residual(const Stop& st, double c, float lp, float lq, int n,
                                            bool plain) {
 #pragma clang fp contract(off)
-  const double p = weight_of(lp, st.p_top, inv) * st.p_inv;
+  const double p = weight_of(lp, st.p_top, c) * st.p_inv;
   if (plain) return p;
   if (n == st.drafted) return 0.0;
-  return fmax(p - weight_of(lq, st.q_top, inv) * st.q_inv, 0.0);
+  return fmax(p - weight_of(lq, st.q_top, c) * st.q_inv, 0.0);
 }
 
 template <typename L, bool VEC>
 __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs a) {
-  __shared__ Stop stop;
-  __shared__ int first_stop;
-  __shared__ int is_last;
-  __shared__ double swave[kThreads / 64];
-  __shared__ int found;
-  __shared__ int last_positive;
+  __shared__ Stop stops[kWaves];
+  __shared__ int is_last, found, positive;
+  __shared__ double wsum[kWaves];
   __shared__ double goal_s, before_s;
-  __shared__ int slice_s, plain_s;
+  __shared__ int sub_s, plain_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int slice = blockIdx.x, s = blockIdx.y;
   const Rows r = rows_of(a, s);
+  const float t = temperature_of(a, s);
+  const double u = a.sample_u[s];
   if (r.n == 0) {
     if (slice == 0 && tid == 0) a.accepted[s] = 0;
     return;
   }
-  const float t = temperature_of(a, s);
   const bool greedy = !(t > 0.0f);
   if (greedy && slice != 0) return;
-  const double inv = greedy ? 0.0 : 1.0 / (double)t;
+  const double c = greedy ? 0.0 : 1.4426950408889634074 / (double)t;
 
   // The first row that stops: a rejection, or the last row.  kRowLanes lanes per row.
+  Stop st{};
   for (int i0 = 0;; i0 += kRowsAtOnce) {
-    if (tid == 0) first_stop = r.n;
-    __syncthreads();
-    const int i = i0 + tid / kRowLanes;
+    const int i = i0 + tid / kRowLanes, l = tid & (kRowLanes - 1);
     Stop mine{};
-    bool stops = false;
+    bool stop = false;
     if (i < r.n) {
       const int row = r.q0 + i;
       const bool final = i == r.n - 1;
-      const RowStat p = row_stat(a.stats + (size_t)row * a.slices, a.slices, inv);
+      const bool asks = !final && !greedy && a.draft;
       const int d = final ? -1 : a.tokens[row + 1];
+      const double au = a.accept_u[row];
       const bool in = d >= 0 && d < a.V;
+      RowStat p{kNegInf, 0x7fffffff, 0.0}, q{kNegInf, 0x7fffffff, 0.0};
+      const Stat* ps = a.stats + (size_t)row * a.slices;
+      const Stat* qs = a.stats + ((size_t)(asks ? a.T : 0) + row) * a.slices;
+      const float pl = in ? logit<L>(a.logits, (size_t)row * a.V + d) : kNegInf;
+      const float ql = in && asks ? logit<L>(a.draft, (size_t)row * a.V + d) : kNegInf;
+      for (int k = l; k - l < a.slices; k += kRowLanes * kAhead) {
+        Stat x[kAhead], y[kAhead];
+        load_stats(ps, k, a.slices, x);
+        if (asks) load_stats(qs, k, a.slices, y);
+        add_stats(x, c, p);
+        if (asks) add_stats(y, c, q);
+      }
+      row_end(c, p);
       mine.row = i;
       mine.greedy_token = p.top > kNegInf ? p.first : 0;
       mine.p_top = p.top;
       mine.p_inv = p.sum > 0.0 ? 1.0 / p.sum : 0.0;
       mine.drafted = -1;
-      const double u = a.accept_u[row];
       if (greedy) {
-        stops = !(in && p.top > kNegInf && d == p.first && u < 1.0);
+        stop = !(in && p.top > kNegInf && d == p.first && au < 1.0);
       } else {
-        double q = 1.0;
-        if (!final && a.draft) {
-          const RowStat qs = row_stat(a.stats + ((size_t)a.T + row) * a.slices, a.slices, inv);
-          mine.q_top = qs.top;
-          mine.q_inv = qs.sum > 0.0 ? 1.0 / qs.sum : 0.0;
-          if (in) q = weight_of(logit<L>(a.draft, (size_t)row * a.V + d), qs.top, inv) * mine.q_inv;
+        double qd = 1.0;
+        if (asks) {
+          row_end(c, q);
+          mine.q_top = q.top;
+          mine.q_inv = q.sum > 0.0 ? 1.0 / q.sum : 0.0;
+          qd = weight_of(ql, q.top, c) * mine.q_inv;
         } else if (!final) {
           mine.drafted = d;
         }
-        const double pd =
-            in ? weight_of(logit<L>(a.logits, (size_t)row * a.V + d), p.top, inv) * mine.p_inv : 0.0;
-        stops = final || !(u * q < pd);
+        const double pd = in ? weight_of(pl, p.top, c) * mine.p_inv : 0.0;
+        stop = final || !(au * qd < pd);
       }
     }
-    if (stops && tid % kRowLanes == 0) atomicMin(&first_stop, i);
+    const unsigned long long b = __ballot(stop);
+    if (lane == 0) stops[wave].row = r.n;
+    if (b && lane == __builtin_ctzll(b)) stops[wave] = mine;
     __syncthreads();
-    const int at = first_stop;
-    if (at < r.n) {
-      if (i == at && tid % kRowLanes == 0) stop = mine;
-      __syncthreads();
-      break;
-    }
+    st.row = r.n;
+#pragma unroll
+    for (int w = kWaves - 1; w >= 0; --w)
+      if (stops[w].row < r.n) st = stops[w];
+    if (st.row < r.n) break;
     __syncthreads();
   }
-  const Stop st = stop;
   const int row = r.q0 + st.row;
   const bool final = st.row == r.n - 1;
 
@@ -369,122 +447,155 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
   if (greedy) {
     token = st.greedy_token;
   } else {
-    // This slice's share of the weights.
+    // This wave's share of the weights.
     const void* lp_row = static_cast<const L*>(a.logits) + (size_t)row * a.V;
     const bool with_q = a.draft && !final;
     const void* lq_row = with_q ? static_cast<const L*>(a.draft) + (size_t)row * a.V : lp_row;
-    float lp[kPer], lq[kPer];
-    const int n0 = slice * kSlice;
-    load_slice<L, VEC>(lp_row, n0, a.V, lp);
-    if (with_q) load_slice<L, VEC>(lq_row, n0, a.V, lq);
-    double w = 0.0;
+    const int subs = a.slices * kWaves;
+    unsigned long long* words = a.weight + (size_t)s * subs;
+    {
+      float lp[kPer], lq[kPer];
+      const int n0 = (slice * kWaves + wave) * kSub;
+      load_sub<L, VEC>(lp_row, n0, a.V, lp);
+      if (with_q) load_sub<L, VEC>(lq_row, n0, a.V, lq);
+      double w = 0.0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      w += residual<L>(st, inv, lp[j], with_q ? lq[j] : kNegInf, n0 + index_of<L, VEC>(j), final);
-    w = wave_sum(w);
-    if (lane == 0) swave[wave] = w;
-    __syncthreads();
-    if (tid == 0) {
-      a.weight[(size_t)s * a.slices + slice] = (swave[0] + swave[1]) + (swave[2] + swave[3]);
-      __threadfence();
-      is_last = __hip_atomic_fetch_add(&a.arrived[s], 1, __ATOMIC_ACQ_REL,
-                                       __HIP_MEMORY_SCOPE_AGENT) == a.slices - 1;
+      for (int j = 0; j < kPer; ++j)
+        w += residual<L>(st, c, lp[j], with_q ? lq[j] : kNegInf, n0 + index_of<L, VEC>(j), final);
+      w = reduce64(w, plus);
+      if (lane == 0)
+        __hip_atomic_store(words + slice * kWaves + wave, __builtin_bit_cast(unsigned long long, w),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tid == 0)
+      is_last = __hip_atomic_fetch_add(&a.arrived[s], 1, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT) == a.slices - 1;
     __syncthreads();
     if (!is_last) return;
-    __threadfence();
 
-    // The slice where the running sum passes u times the total; without any
-    // weight (p nowhere above q), the same over p itself.
+    // The kSub entries where the running sum passes u times the total; without
+    // any weight (p nowhere above q), the same over p itself, slice by slice.
     if (wave == 0) {
-      const double* ws = a.weight + (size_t)s * a.slices;
       const Stat* ps = a.stats + (size_t)row * a.slices;
-      double total = 0.0;
-      for (int i = lane; i < a.slices; i += 64) total += ws[i];
-      total = wave_sum(total);
+      const auto word = [&](int i) {
+        unsigned long long x = kNotYet;
+        for (int k = 0; i < subs && x == kNotYet && k < kMaxPolls; ++k)
+          x = __hip_atomic_load(words + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return i < subs && x != kNotYet ? __builtin_bit_cast(double, x) : 0.0;
+      };
+      constexpr int kRun = 4;                        // words of a lane, neighbours
+      double w[kRun], total = 0.0;
+      for (int i0 = 0; i0 < subs; i0 += 64 * kRun) {
+        double x = 0.0;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) x += w[e] = word(i0 + lane * kRun + e);
+        total += lane_of(scan64(x), 63);
+      }
       const bool plain = !(total > 0.0);
+      // Word i of the distribution to sample from; with `plain` a slice's sum
+      // counts at its first word, and the slice is searched as a whole.
+      const auto share = [&](int i) {
+        if (!plain) return word(i);
+        if (i >= subs || i % kWaves) return 0.0;
+        const Stat x = ps[i / kWaves];
+        return x.sum * weight_of(x.max, st.p_top, c) * st.p_inv;
+      };
       if (plain) {
         total = 0.0;
-        for (int i = lane; i < a.slices; i += 64)
-          total += ps[i].sum * weight_of(ps[i].max, st.p_top, inv) * st.p_inv;
-        total = wave_sum(total);
-      }
-      const double u = a.sample_u[s];
-      const double goal = (u > 0.0 ? u : 0.0) * total;
-      double before = 0.0;
-      int at = -1, last = 0;
-      double at_before = 0.0, last_before = 0.0;
-      for (int i0 = 0; i0 < a.slices && at < 0; i0 += 64) {
-        const int i = i0 + lane;
-        double x = 0.0;
-        if (i < a.slices)
-          x = plain ? ps[i].sum * weight_of(ps[i].max, st.p_top, inv) * st.p_inv : ws[i];
-        double incl = x;
+        for (int i0 = 0; i0 < subs; i0 += 64 * kRun) {
+          double x = 0.0;
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-          const double o = __shfl_up(incl, off);
-          if (lane >= off) incl += o;
+          for (int e = 0; e < kRun; ++e) x += share(i0 + lane * kRun + e);
+          total += lane_of(scan64(x), 63);
         }
-        const unsigned long long over = __ballot(x > 0.0 && before + incl > goal);
-        const unsigned long long some = __ballot(x > 0.0);
-        if (some) {
-          const int b = 63 - __builtin_clzll(some);
-          last = i0 + b;
-          last_before = before + __shfl(incl, b) - __shfl(x, b);
+      }
+      const double goal = (u > 0.0 ? u : 0.0) * total;
+      double before = 0.0, at_before = 0.0;
+      int at = -1;                                   // else the last word with any weight
+      bool hit = false;
+      for (int i0 = 0; i0 < subs && !hit; i0 += 64 * kRun) {
+        double x = 0.0;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+          w[e] = share(i0 + lane * kRun + e);
+          x += w[e];
         }
-        if (over) {
-          const int b = __builtin_ctzll(over);
-          at = i0 + b;
-          const double prev = __shfl(incl, b ? b - 1 : 0);
-          at_before = b ? before + prev : before;
+        const double incl = scan64(x);
+        const double prev = dpp<0x138>(incl);        // the lane before (wave_shr:1), 0 for the first
+        double run = before + prev, b_over = 0.0, b_some = 0.0;
+        int over = -1, some = -1;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+          if (w[e] > 0.0) {
+            some = e;
+            b_some = run;
+            if (over < 0 && run + w[e] > goal) {
+              over = e;
+              b_over = run;
+            }
+          }
+          run += w[e];
         }
-        before += __shfl(incl, 63);
+        const unsigned long long bo = __ballot(over >= 0), bs = __ballot(some >= 0);
+        if (bo) {
+          const int b = __builtin_ctzll(bo);
+          at = i0 + b * kRun + __builtin_amdgcn_readlane(over, b);
+          at_before = lane_of(b_over, b);
+          hit = true;
+        } else if (bs) {
+          const int b = 63 - __builtin_clzll(bs);
+          at = i0 + b * kRun + __builtin_amdgcn_readlane(some, b);
+          at_before = lane_of(b_some, b);
+        }
+        before += lane_of(incl, 63);
       }
       if (lane == 0) {
-        slice_s = at < 0 ? last : at;
-        before_s = at < 0 ? last_before : at_before;
+        sub_s = max(at, 0);
+        before_s = at_before;
         goal_s = goal;
-        plain_s = plain || final;
+        plain_s = plain;
         found = a.V;
-        last_positive = 0;
+        positive = 0;
       }
     }
     __syncthreads();
-    // The entry in it: kPer neighbours per thread, in order.
-    const int m0 = slice_s * kSlice + tid * kPer;
+    // The entry among them: kFind neighbours per thread, in order.
     const bool plain = plain_s;
-    double x[kPer];
-    double sum = 0.0;
-    int positive = -1;
+    double before = before_s;
+    for (int k = 0; k < (plain ? kWaves : 1); ++k) {
+      const int m0 = (sub_s + k) * kSub + tid * kFind;
+      double x[kFind], sum = 0.0;
+      int some = -1;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int n = m0 + j;
-      const float vp = n < a.V ? logit<L>(lp_row, n) : __builtin_nanf("");
-      const float vq = with_q && n < a.V ? logit<L>(lq_row, n) : kNegInf;
-      const double y = residual<L>(st, inv, vp, vq, n, plain);
-      if (y > 0.0) positive = n;
-      sum += y;
-      x[j] = sum;
+      for (int j = 0; j < kFind; ++j) {
+        const int n = m0 + j, at = min(n, a.V - 1);
+        const float vp = logit<L>(lp_row, at), vq = with_q ? logit<L>(lq_row, at) : kNegInf;
+        const double y = n < a.V ? residual<L>(st, c, vp, vq, n, plain || final) : 0.0;
+        if (y > 0.0) some = n;
+        x[j] = y;
+        sum += y;
+      }
+      const double incl = scan64(sum);
+      if (lane == 63) wsum[wave] = incl;
+      __syncthreads();
+      double run = before + dpp<0x138>(incl);
+      for (int w = 0; w < wave; ++w) run += wsum[w];
+      int hit = a.V;
+#pragma unroll
+      for (int j = 0; j < kFind; ++j) {
+        run += x[j];
+        if (hit == a.V && x[j] > 0.0 && run > goal_s) hit = m0 + j;
+      }
+      if (hit < a.V) atomicMin(&found, hit);
+      if (some >= 0) atomicMax(&positive, some);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) before += wsum[w];
+      __syncthreads();
+      if (found < a.V) break;
     }
-    double incl = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
-    if (lane == 63) swave[wave] = incl;
-    __syncthreads();
-    double base = before_s;
-    for (int w2 = 0; w2 < wave; ++w2) base += swave[w2];
-    base += incl - sum;
-    int hit = a.V;
-#pragma unroll
-    for (int j = kPer - 1; j >= 0; --j)
-      if (base + x[j] > goal_s && x[j] > (j ? x[j - 1] : 0.0)) hit = m0 + j;
-    if (hit < a.V) atomicMin(&found, hit);
-    if (positive >= 0) atomicMax(&last_positive, positive);
-    __syncthreads();
-    token = found < a.V ? found : last_positive;
+    token = found < a.V ? found : positive;
   }
 
   for (int i = tid; i < r.n; i += kThreads)
@@ -508,7 +619,7 @@ Layout layout(int rows, int seqs, int vocab) {
   Layout w;
   w.stats = 0;
   w.weight = up((size_t)2 * rows * sl * sizeof(Stat));
-  w.arrived = w.weight + up((size_t)seqs * sl * sizeof(double));
+  w.arrived = w.weight + up((size_t)seqs * sl * kWaves * sizeof(double));
   w.total = w.arrived + up((size_t)seqs * sizeof(int));
   return w;
 }
@@ -600,7 +711,7 @@ skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
   a.accepted = v.accepted;
   unsigned char* ws = (unsigned char*)workspace;
   a.stats = (Stat*)(ws + w.stats);
-  a.weight = (double*)(ws + w.weight);
+  a.weight = (unsigned long long*)(ws + w.weight);
   a.arrived = (int*)(ws + w.arrived);
   a.T = v.rows;
   a.S = v.seqs;
