@@ -122,11 +122,15 @@ __device__ __forceinline__ double exp2_below(double y) {
   return y >= -1000.0 ? r : 0.0;
 }
 
-// exp((l - top) / t) with c = log2 e / t: 1 at the maximum (an infinite one
-// too), 0 for NaN and -inf.
+// exp((l - top) / t) with c = log2 e / t, top below +inf: 1 at the maximum, 0
+// for NaN and -inf (and for top -inf).
+__device__ __forceinline__ double finite_weight(float l, double top, double c) {
+  return exp2_below(((double)l - top) * c);
+}
+// The same for any top; where it is +inf, 1 at the infinite entries and 0 elsewhere.
 __device__ __forceinline__ double weight_of(float l, float top, double c) {
-  const double w = exp2_below(((double)l - (double)top) * c);
-  return l == top ? (top > kNegInf ? 1.0 : 0.0) : w;
+  const double w = finite_weight(l, top, c);
+  return top == -kNegInf ? (l == top ? 1.0 : 0.0) : w;
 }
 
 // Lane exchanges on the vector ALUs: rotation within 16 lanes, and with the
@@ -278,16 +282,24 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   if (which == 1 && (greedy || row + 1 == r.q0 + r.n)) return;
   // Each wave's maximum and sum, then the four joined.
   float top = kNegInf;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
+  const float wtop = reduce64(top, larger);
   int first = a.V;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) take_first(l[j], n0 + index_of<L, VEC>(j), top, first);
-  const float wtop = reduce64(top, larger);
-  first = reduce64(top == wtop ? first : a.V, lower);
+  for (int j = kPer - 1; j >= 0; --j) first = l[j] == wtop ? n0 + index_of<L, VEC>(j) : first;
+  first = reduce64(first, lower);
   double sum = 0.0;
   const double c = 1.4426950408889634074 / (double)t;
   if (!greedy) {
+    if (wtop < -kNegInf) {
+      const double dtop = wtop;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) sum += weight_of(l[j], wtop, c);
+      for (int j = 0; j < kPer; ++j) sum += finite_weight(l[j], dtop, c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) sum += l[j] == wtop ? 1.0 : 0.0;
+    }
     sum = reduce64(sum, plus);
   }
   if (lane == 0) {
@@ -479,50 +491,51 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
     // any weight (p nowhere above q), the same over p itself, slice by slice.
     if (wave == 0) {
       const Stat* ps = a.stats + (size_t)row * a.slices;
-      const auto word = [&](int i) {
-        unsigned long long x = kNotYet;
-        for (int k = 0; i < subs && x == kNotYet && k < kMaxPolls; ++k)
-          x = __hip_atomic_load(words + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        return i < subs && x != kNotYet ? __builtin_bit_cast(double, x) : 0.0;
-      };
       constexpr int kRun = 4;                        // words of a lane, neighbours
       double w[kRun], total = 0.0;
-      for (int i0 = 0; i0 < subs; i0 += 64 * kRun) {
+      // The lane's run of words from i0 on.  With `plain` a slice's sum counts
+      // at its first word, and the slice is searched as a whole.
+      static_assert(kRun == kWaves, "a lane's run is a slice");
+      const auto fetch = [&](int i0, bool plain) {
+        const int i = i0 + lane * kRun;
         double x = 0.0;
+        if (plain) {
+          const Stat y = ps[min(i / kWaves, a.slices - 1)];
+          w[0] = i < subs ? y.sum * weight_of(y.max, st.p_top, c) * st.p_inv : 0.0;
+          w[1] = w[2] = w[3] = 0.0;
+          x = w[0];
+        } else {
+          unsigned long long y[kRun];
+          bool all = false;
+          for (int k = 0; !all && k < kMaxPolls; ++k) {
+            all = true;
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) x += w[e] = word(i0 + lane * kRun + e);
-        total += lane_of(scan64(x), 63);
-      }
-      const bool plain = !(total > 0.0);
-      // Word i of the distribution to sample from; with `plain` a slice's sum
-      // counts at its first word, and the slice is searched as a whole.
-      const auto share = [&](int i) {
-        if (!plain) return word(i);
-        if (i >= subs || i % kWaves) return 0.0;
-        const Stat x = ps[i / kWaves];
-        return x.sum * weight_of(x.max, st.p_top, c) * st.p_inv;
-      };
-      if (plain) {
-        total = 0.0;
-        for (int i0 = 0; i0 < subs; i0 += 64 * kRun) {
-          double x = 0.0;
+            for (int e = 0; e < kRun; ++e)
+              y[e] = __hip_atomic_load(words + min(i, subs - kRun) + e, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-          for (int e = 0; e < kRun; ++e) x += share(i0 + lane * kRun + e);
-          total += lane_of(scan64(x), 63);
+            for (int e = 0; e < kRun; ++e) all = all && y[e] != kNotYet;
+          }
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) {
+            w[e] = i < subs && y[e] != kNotYet ? __builtin_bit_cast(double, y[e]) : 0.0;
+            x += w[e];
+          }
         }
+        return x;
+      };
+      bool plain = false;
+      for (int pass = 0; pass < 2 && !(total > 0.0); ++pass) {
+        plain = pass;
+        for (int i0 = 0; i0 < subs; i0 += 64 * kRun) total += lane_of(scan64(fetch(i0, plain)), 63);
       }
       const double goal = (u > 0.0 ? u : 0.0) * total;
       double before = 0.0, at_before = 0.0;
       int at = -1;                                   // else the last word with any weight
       bool hit = false;
       for (int i0 = 0; i0 < subs && !hit; i0 += 64 * kRun) {
-        double x = 0.0;
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-          w[e] = share(i0 + lane * kRun + e);
-          x += w[e];
-        }
-        const double incl = scan64(x);
+        if (subs > 64 * kRun) fetch(i0, plain);      // else they are still there
+        const double incl = scan64((w[0] + w[1]) + (w[2] + w[3]));
         const double prev = dpp<0x138>(incl);        // the lane before (wave_shr:1), 0 for the first
         double run = before + prev, b_over = 0.0, b_some = 0.0;
         int over = -1, some = -1;
