@@ -619,6 +619,49 @@ def moe_plan_query(experts: Experts, T: int, topk: int, x_per_route: bool = Fals
     return plan
 
 
+class _Torch:
+    """What the calls below ask torch for each time, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.device = torch.cuda.current_device
+        # The stream's handle without a Stream object around it (a microsecond
+        # of the host's time per call), where this torch has that.
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_torch = None
+
+
+def _operand(t, shape, dtype, what, dev):
+    """Device address of a tensor after the checks of _need and _ptr (which
+    name what is wrong), and that it lies on GPU `dev`."""
+    if t.shape != shape or t.dtype is not dtype:
+        _need(t, shape, {str(dtype).replace("torch.", "")}, what)
+    if dev < 0 or not t.is_contiguous() or t.get_device() != dev:
+        _ptr(t)
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors on GPU {dev}")
+    return t.data_ptr()
+
+
+def _call_device(t):
+    """GPU of a call's tensors, which has to be the current one: the library
+    launches there, on that device's current stream."""
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    dev = t.get_device()
+    if dev >= 0 and dev != _torch.device():
+        raise ValueError(f"tensors on {t.device}, but the current device is GPU {_torch.device()}")
+    return _torch, dev
+
+
+def _call_stream(tt, dev, stream):
+    return tt.raw_stream(dev) if stream is None else _stream(stream)
+
+
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
     """A skinny_kv_cache from GPU tensors k and v [pages][kv_heads][page_tokens]
     [head_dim]: bf16, or e4m3 codes (uint8 / float8_e4m3fn) with k_scale and
@@ -653,9 +696,10 @@ def make_batch(q_start, kv_len, page_table, tokens: int) -> KvBatch:
 
 def _heads(cache: KvCache, batch: KvBatch, t, what: str, extra: int = 0) -> int:
     """Query heads of a [tokens][(q_heads + extra) * head_dim] tensor."""
-    rows, width = _shape2(t)
+    width = t.shape[-1]
     heads = width // cache.head_dim - extra
-    _need(t, (batch.tokens, (heads + extra) * cache.head_dim), _BF16, what)
+    if t.shape != (batch.tokens, (heads + extra) * cache.head_dim):
+        _need(t, (batch.tokens, (heads + extra) * cache.head_dim), _BF16, what)
     return heads
 
 
@@ -665,15 +709,16 @@ def kv_append(cache: KvCache, batch: KvBatch, qkv, inv_freq, q_out, interleaved:
     queries into q_out [tokens][q_heads * head_dim].  qkv [tokens][(q_heads +
     2 kv_heads) * head_dim] is the QKV linear's y; inv_freq [rotary_dim / 2]
     float32, or None for no rotation."""
+    tt, dev = _call_device(qkv)
     heads = _heads(cache, batch, qkv, "qkv", 2 * cache.kv_heads)
-    _need(q_out, (batch.tokens, heads * cache.head_dim), _BF16, "q_out")
-    rot = 0
+    x = _operand(qkv, qkv.shape, tt.bf16, "qkv", dev)
+    y = _operand(q_out, (batch.tokens, heads * cache.head_dim), tt.bf16, "q_out", dev)
+    rot, f = 0, None
     if inv_freq is not None:
-        rot = 2 * int(inv_freq.shape[0])
-        _need(inv_freq, (rot // 2,), _F32, "inv_freq")
-    _check(lib().skinny_kv_append(cache, batch, _ptr(qkv), heads, _ptr(inv_freq), rot,
-                                  int(interleaved), _ptr(q_out), _stream(stream)),
-           "skinny_kv_append")
+        rot = 2 * inv_freq.shape[0]
+        f = _operand(inv_freq, (rot // 2,), tt.f32, "inv_freq", dev)
+    _check(lib().skinny_kv_append(cache, batch, x, heads, f, rot, int(interleaved), y,
+                                  _call_stream(tt, dev, stream)), "skinny_kv_append")
     return q_out
 
 
@@ -686,12 +731,14 @@ def kv_attention(cache: KvCache, batch: KvBatch, q, out, workspace, scale: float
     """out = softmax(scale q k^T) v over each sequence's cache, causal within
     the step's rows; q and out bf16 [tokens][q_heads * head_dim], scale
     1 / sqrt(head_dim) unless given."""
+    tt, dev = _call_device(q)
     heads = _heads(cache, batch, q, "q")
-    _need(out, (batch.tokens, heads * cache.head_dim), _BF16, "out")
+    x = _operand(q, q.shape, tt.bf16, "q", dev)
+    y = _operand(out, q.shape, tt.bf16, "out", dev)
     wp, wb = _ws(workspace)
-    _check(lib().skinny_kv_attention(cache, batch, _ptr(q), heads,
-                                     cache.head_dim ** -0.5 if scale is None else scale, _ptr(out),
-                                     wp, wb, _stream(stream)), "skinny_kv_attention")
+    _check(lib().skinny_kv_attention(cache, batch, x, heads,
+                                     cache.head_dim ** -0.5 if scale is None else scale, y, wp, wb,
+                                     _call_stream(tt, dev, stream)), "skinny_kv_attention")
     return out
 
 
@@ -707,21 +754,26 @@ def verify_draft(q_start, logits, tokens, accept_u, sample_u, out_tokens, accept
     sample_u and temperature float32 [seqs]; out_tokens int32 [rows] gets each
     sequence's kept drafts, its next token, then -1, and accepted int32 [seqs]
     the number kept."""
+    tt, dev = _call_device(logits)
     rows, vocab = _shape2(logits)
-    seqs = int(sample_u.shape[0])
-    name = _dtype_name(logits)
-    _need(logits, (rows, vocab), _BF16 | _F32, "logits")
-    _need(draft_logits, (rows, vocab), {name}, "draft_logits")
-    _need(q_start, (seqs + 1,), _I32, "q_start")
-    _need(tokens, (rows,), _I32, "tokens")
-    _need(accept_u, (rows,), _F32, "accept_u")
-    _need(sample_u, (seqs,), _F32, "sample_u")
-    _need(temperature, (seqs,), _F32, "temperature")
-    _need(out_tokens, (rows,), _I32, "out_tokens")
-    _need(accepted, (seqs,), _I32, "accepted")
-    v = Verify(LOGITS_BF16 if name == "bfloat16" else LOGITS_F32, vocab, rows, seqs, _ptr(q_start),
-               _ptr(logits), _ptr(draft_logits), _ptr(tokens), _ptr(temperature), _ptr(accept_u),
-               _ptr(sample_u), _ptr(out_tokens), _ptr(accepted))
+    seqs = sample_u.shape[0]
+    kind = logits.dtype
+    if kind is not tt.bf16 and kind is not tt.f32:
+        _need(logits, (rows, vocab), _BF16 | _F32, "logits")
+    per_row, per_seq, i32, f32 = (rows,), (seqs,), tt.i32, tt.f32
+    v = Verify(
+        LOGITS_BF16 if kind is tt.bf16 else LOGITS_F32, vocab, rows, seqs,
+        _operand(q_start, (seqs + 1,), i32, "q_start", dev),
+        _operand(logits, logits.shape, kind, "logits", dev),
+        None if draft_logits is None else _operand(draft_logits, (rows, vocab), kind,
+                                                   "draft_logits", dev),
+        _operand(tokens, per_row, i32, "tokens", dev),
+        None if temperature is None else _operand(temperature, per_seq, f32, "temperature", dev),
+        _operand(accept_u, per_row, f32, "accept_u", dev),
+        _operand(sample_u, per_seq, f32, "sample_u", dev),
+        _operand(out_tokens, per_row, i32, "out_tokens", dev),
+        _operand(accepted, per_seq, i32, "accepted", dev))
     wp, wb = _ws(workspace)
-    _check(lib().skinny_verify_draft(v, wp, wb, _stream(stream)), "skinny_verify_draft")
+    _check(lib().skinny_verify_draft(v, wp, wb, _call_stream(tt, dev, stream)),
+           "skinny_verify_draft")
     return out_tokens
