@@ -640,7 +640,7 @@ def _operand(t, shape, dtype, what, dev):
     name what is wrong), and that it lies on GPU `dev`."""
     if t.shape != shape or t.dtype is not dtype:
         _need(t, shape, {str(dtype).replace("torch.", "")}, what)
-    if dev < 0 or not t.is_contiguous() or t.get_device() != dev:
+    if not t.is_contiguous() or t.get_device() != dev:
         _ptr(t)
         raise ValueError(f"{what} is on {t.device}, the call's other tensors on GPU {dev}")
     return t.data_ptr()
@@ -659,6 +659,8 @@ def _call_device(t):
 
 
 def _call_stream(tt, dev, stream):
+    if dev < 0:
+        raise ValueError("tensors passed to the library must be on the GPU, not cpu")
     return tt.raw_stream(dev) if stream is None else _stream(stream)
 
 
