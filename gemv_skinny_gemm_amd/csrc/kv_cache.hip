@@ -586,22 +586,32 @@ __device__ __forceinline__ unsigned not_finite(unsigned x) {
   }
 }
 
-// Loads of the cache: every byte is read once per call (per row group).
-__device__ __forceinline__ u32x4 load16(const unsigned char* p) {
-  return *reinterpret_cast<const u32x4*>(p);
+// A use of a loaded value that costs no instruction: the wait for it stands
+// here, and later ones in a loop need not allow for it.
+template <typename T>
+__device__ __forceinline__ void arrived(T& x) {
+  asm volatile("" : "+v"(x));
 }
-template <int W>
+
+// Loads of the cache; NT with the nontemporal hint, for bytes that one wave of
+// the call reads, in whole cache lines.
+template <bool NT, typename T>
+__device__ __forceinline__ T load_as(const unsigned char* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  else return *reinterpret_cast<const T*>(p);
+}
+template <bool NT, int W>
 __device__ __forceinline__ void load_words(const unsigned char* p, unsigned (&out)[W]) {
   if constexpr (W == 1) {
-    out[0] = *reinterpret_cast<const unsigned*>(p);
+    out[0] = load_as<NT, unsigned>(p);
   } else if constexpr (W == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 x = load_as<NT, u32x2>(p);
     out[0] = x[0];
     out[1] = x[1];
   } else {
 #pragma unroll
     for (int i = 0; i < W; i += 4) {
-      const u32x4 x = load16(p + 4 * i);
+      const u32x4 x = load_as<NT, u32x4>(p + 4 * i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[i + e] = x[e];
     }
@@ -676,6 +686,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
   constexpr int kAll = 64 * NW;                      // threads
   constexpr int kStride = D + 4;                     // LDS row of the waves' sums, padded
   constexpr Cut cut{ROWS, 32 * KW};
+  constexpr bool kOnce = RW == 1 && Sh::kRowBytes >= 128;
   __shared__ __attribute__((aligned(16))) float sums[NW][16][kStride];
   __shared__ float sm[NW][16], sl[NW][16];
   const KvArgs& kv = a.kv;
@@ -754,6 +765,8 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
           const size_t at = (size_t)max(w_page, 0) * kv.kv_heads + h;
           w_ks = good ? kv.k_scale[at] : 0.0f;
           w_vs = good ? kv.v_scale[at] : 0.0f;
+          arrived(w_ks);
+          arrived(w_vs);
         }
       }
     };
@@ -783,7 +796,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
       for (int u = 0; u < 2; ++u) {
         const unsigned char* kp = kv.k + at[u].off + c * Sh::kRowBytes + g * 16;
 #pragma unroll
-        for (int i = 0; i < Sh::kLoads; ++i) kf[u][i] = load16(kp + 64 * i);
+        for (int i = 0; i < Sh::kLoads; ++i) kf[u][i] = load_as<kOnce, u32x4>(kp + 64 * i);
       }
     };
     const auto load_v = [&](const Half (&at)[2]) {
@@ -791,117 +804,122 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
       for (int u = 0; u < 2; ++u) {
         const unsigned char* vp = kv.v + at[u].off + 4 * g * Sh::kRowBytes + c * (4 * Sh::kWords);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) load_words<Sh::kWords>(vp + r * Sh::kRowBytes, vf[4 * u + r]);
+        for (int r = 0; r < 4; ++r) load_words<kOnce, Sh::kWords>(vp + r * Sh::kRowBytes, vf[4 * u + r]);
       }
     };
 
     // The next tile's keys load behind this tile's scores, its values behind
     // this tile's output; the last tile loads itself once more.
     Half now[2];
+    bool dirty = false;                              // a masked tile had such values
     if (tiles > 0) {
       look(key0);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int st = 0; st < Sh::kSteps; ++st) arrived(qf[rt][st]);
       now[0] = half_of(key0);
       now[1] = half_of(key0 + 16);
       load_k(now);
       load_v(now);
-    }
-    bool dirty = false;                              // a masked tile had such values
-    for (int t = 0; t < tiles; ++t) {
-      const int key = key0 + 32 * t;
-      const float ks[2] = {now[0].ks, now[1].ks}, vs[2] = {now[0].vs, now[1].vs};
-      const bool there[2] = {now[0].there, now[1].there};
-      const bool good = there[0] && there[1];
-      const bool masked = !good || key + 32 > lim_lo;   // some row does not see some key
+      int t = 0;
+      do {
+        const int key = key0 + 32 * t;
+        const float ks[2] = {now[0].ks, now[1].ks}, vs[2] = {now[0].vs, now[1].vs};
+        const bool there[2] = {now[0].there, now[1].there};
+        const bool good = there[0] && there[1];
+        const bool masked = !good || key + 32 > lim_lo;   // some row does not see some key
 
-      u32x4 pf[RT];
-      f32x4 sc[RT][2];
+        u32x4 pf[RT];
+        f32x4 sc[RT][2];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          f32x4 s{0, 0, 0, 0};
+          for (int u = 0; u < 2; ++u) {
+            f32x4 s{0, 0, 0, 0};
 #pragma unroll
-          for (int st = 0; st < Sh::kSteps; ++st) {
-            u32x4 kk;
-            if constexpr (DT == kBF16) {
-              kk = kf[u][st];
-            } else {
-              const u32x4 raw = kf[u][st / 2];
-              const unsigned x = raw[2 * (st % 2)], y = raw[2 * (st % 2) + 1];
-              kk = u32x4{e4m3x2_to_bf16<false>(x), e4m3x2_to_bf16<true>(x),
-                         e4m3x2_to_bf16<false>(y), e4m3x2_to_bf16<true>(y)};
+            for (int st = 0; st < Sh::kSteps; ++st) {
+              u32x4 kk;
+              if constexpr (DT == kBF16) {
+                kk = kf[u][st];
+              } else {
+                const u32x4 raw = kf[u][st / 2];
+                const unsigned x = raw[2 * (st % 2)], y = raw[2 * (st % 2) + 1];
+                kk = u32x4{e4m3x2_to_bf16<false>(x), e4m3x2_to_bf16<true>(x),
+                           e4m3x2_to_bf16<false>(y), e4m3x2_to_bf16<true>(y)};
+              }
+              s = mfma_bf16(kk, qf[rt][st], s);
             }
-            s = mfma_bf16(kk, qf[rt][st], s);
-          }
-          const float f = a.scale * ks[u];
+            const float f = a.scale * ks[u];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sc[rt][u][r] = s[r] * f;
+            for (int r = 0; r < 4; ++r) sc[rt][u][r] = s[r] * f;
+            if (masked) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (!there[u] || key + 16 * u + 4 * g + r >= lim[rt]) sc[rt][u][r] = kNegInf;
+            }
+          }
+        const int next = key0 + 32 * min(t + 1, tiles - 1);
+        look(next);
+        now[0] = half_of(next);
+        now[1] = half_of(next + 16);
+        load_k(now);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float top = m[rt];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][u][r]);
+          top = row_max(top);
+          if (__any(top > m[rt] + kSlack)) {
+            const float f = top > m[rt] ? __builtin_amdgcn_exp2f(m[rt] - top) : 1.0f;
+            l[rt] *= f;
+#pragma unroll
+            for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] *= f;
+            m[rt] = fmaxf(m[rt], top);
+          }
+          const float ref = m[rt] == kNegInf ? 0.0f : m[rt];
+          float p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(sc[rt][i / 4][i % 4] - ref);
+            l[rt] += p[i];
+            if constexpr (DT == kFP8) p[i] *= vs[i / 4];
+          }
           if (masked) {
+            // A key that the row does not see takes no part, whatever its page's scale holds.
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (!there[u] || key + 16 * u + 4 * g + r >= lim[rt]) sc[rt][u][r] = kNegInf;
+            for (int i = 0; i < 8; ++i)
+              if (!there[i / 4] || key + 16 * (i / 4) + 4 * g + i % 4 >= lim[rt]) p[i] = 0.0f;
           }
-        }
-      const int next = key0 + 32 * min(t + 1, tiles - 1);
-      look(next);
-      now[0] = half_of(next);
-      now[1] = half_of(next + 16);
-      load_k(now);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float top = m[rt];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][u][r]);
-        top = row_max(top);
-        if (__any(top > m[rt] + kSlack)) {
-          const float f = top > m[rt] ? __builtin_amdgcn_exp2f(m[rt] - top) : 1.0f;
-          l[rt] *= f;
-#pragma unroll
-          for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] *= f;
-          m[rt] = fmaxf(m[rt], top);
-        }
-        const float ref = m[rt] == kNegInf ? 0.0f : m[rt];
-        float p[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(sc[rt][i / 4][i % 4] - ref);
-          l[rt] += p[i];
-          if constexpr (DT == kFP8) p[i] *= vs[i / 4];
+          for (int i = 0; i < 4; ++i) pf[rt][i] = pack_bf16(p[2 * i], p[2 * i + 1]);
         }
         if (masked) {
-          // A key that the row does not see takes no part, whatever its page's scale holds.
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!there[i / 4] || key + 16 * (i / 4) + 4 * g + i % 4 >= lim[rt]) p[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pf[rt][i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-      }
-      if (masked) {
-        // 0 * inf and 0 * NaN are NaN: values that are no finite numbers leave
-        // the product, and come back below for the rows that do see their keys.
-        unsigned any = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int w = 0; w < Sh::kWords; ++w) any |= not_finite<DT>(vf[i][w]);
-        if (__any(any != 0)) {
-          dirty = true;
+          // 0 * inf and 0 * NaN are NaN: values that are no finite numbers leave
+          // the product, and come back below for the rows that do see their keys.
+          unsigned any = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int w = 0; w < Sh::kWords; ++w) vf[i][w] &= ~not_finite<DT>(vf[i][w]);
+            for (int w = 0; w < Sh::kWords; ++w) any |= not_finite<DT>(vf[i][w]);
+          if (__any(any != 0)) {
+            dirty = true;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int w = 0; w < Sh::kWords; ++w) vf[i][w] &= ~not_finite<DT>(vf[i][w]);
+          }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < Sh::kTiles; ++j) {
-        const u32x4 vt = v_tile<DT, D>(vf, j);
+        for (int j = 0; j < Sh::kTiles; ++j) {
+          const u32x4 vt = v_tile<DT, D>(vf, j);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_bf16(vt, pf[rt], o[rt][j]);
-      }
-      load_v(now);
+          for (int rt = 0; rt < RT; ++rt) o[rt][j] = mfma_bf16(vt, pf[rt], o[rt][j]);
+        }
+        load_v(now);
+      } while (++t < tiles);
     }
 
     for (int t = dirty ? 0 : tiles; t < tiles; ++t) {
