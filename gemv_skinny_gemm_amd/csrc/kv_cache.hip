@@ -96,14 +96,20 @@ __device__ __forceinline__ int add_count(int a, int b) {
   return (int)min((unsigned)a + (unsigned)b, (unsigned)kMaxCount);
 }
 
-// Inclusive sum over the wave's lanes of counts.
+// Inclusive sum over the wave's lanes of counts: shifts by 1, 2, 4, 8 within
+// each 16 lanes, then the last lane of a row into the next row and of the lower
+// half into the upper.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_from(int v) {
+  return add_count(v, __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true));
+}
 __device__ __forceinline__ int wave_scan(int v) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(v, off);
-    if ((int)(threadIdx.x & 63) >= off) v = add_count(v, o);
-  }
-  return v;
+  v = add_from<0x111, 0xf>(v);                       // row_shr
+  v = add_from<0x112, 0xf>(v);
+  v = add_from<0x114, 0xf>(v);
+  v = add_from<0x118, 0xf>(v);
+  v = add_from<0x142, 0xa>(v);                       // row_bcast15
+  return add_from<0x143, 0xc>(v);                    // row_bcast31
 }
 
 // In a list of counts (one per sequence, `incl` their running sums over the
@@ -421,6 +427,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
 // other waves stream through.)
 
 constexpr int kMaxGroups = 512;          // workgroups of the grid at most
+constexpr size_t kSplitBytes = kMaxGroups * 32;
 constexpr float kNegInf = -__builtin_inff();
 // m need not be the maximum itself, only near it: sums are scaled again when a
 // score passes it by more than this (probabilities then reach 2^8, far from
@@ -428,10 +435,22 @@ constexpr float kNegInf = -__builtin_inff();
 // every time, one of its 16 rows finding a new maximum.
 constexpr float kSlack = 8.0f;
 
+// What a share leaves for the second launch: the item that begins in it and
+// goes on in the next ones, if there is one.
+struct Split {
+  int n;          // segments, one per share from this one on (0: no such item)
+  int rows;       // rows of the item
+  int row0;       // the first one's number: token * group + query head of its KV head
+  int q0;         // the sequence's first row in the batch
+  int h;          // KV head
+};
+static_assert(kMaxGroups * sizeof(Split) <= kSplitBytes, "room for every share's");
+
 struct AttnArgs {
   KvArgs kv;
   const __bf16* q;         // [T][q_heads D]
   __bf16* out;             // [T][q_heads D]
+  Split* splits;           // [grid]
   float* part;             // [2 grid] segments: [ROWS][D] sums, [ROWS] m, [ROWS] l
   float scale;             // softmax scale * log2 e
   int groups;              // workgroups
@@ -593,6 +612,27 @@ __device__ __forceinline__ void arrived(T& x) {
   asm volatile("" : "+v"(x));
 }
 
+// Results of matrix instructions, before vector instructions read them.  The
+// hardware does not hold a vector read back until the matrix instruction has
+// written (12 slots are enough for these); the compiler fills the slots between
+// instructions of one basic block, but where a branch came in between it was
+// seen to leave them out, and the scores then lacked their last product.  The
+// slots stand here, and what depends on the values stays behind them.
+__device__ __forceinline__ void settle(f32x4& x) {
+  asm volatile("s_nop 7\n\ts_nop 3" : "+v"(x));
+}
+__device__ __forceinline__ void settle(f32x4 (&x)[2], f32x4 (&y)[2]) {
+  asm volatile("s_nop 7\n\ts_nop 3" : "+v"(x[0]), "+v"(x[1]), "+v"(y[0]), "+v"(y[1]));
+}
+template <int A, int B>
+__device__ __forceinline__ void settle(f32x4 (&x)[A][B]) {
+  settle(x[0][0]);
+#pragma unroll
+  for (int i = 0; i < A; ++i)
+#pragma unroll
+    for (int j = 0; j < B; ++j) asm volatile("" : "+v"(x[i][j]));
+}
+
 // Loads of the cache; NT with the nontemporal hint, for bytes that one wave of
 // the call reads, in whole cache lines.
 template <bool NT, typename T>
@@ -623,9 +663,19 @@ struct Shape {
   static constexpr int kRowBytes = D * (DT == kBF16 ? 2 : 1);
   static constexpr int kLoads = kRowBytes / 64;      // 16-byte K loads per lane and 16 keys
   static constexpr int kSteps = D / 32;              // products over D per 16 keys
+  static constexpr int kPart = DT == kBF16 ? 1 : 2;  // of them from one K load
   static constexpr int kTiles = D / 16;              // output tiles
   static constexpr int kWords = kRowBytes / 64;      // dwords of a lane's part of a V row
 };
+
+// A operand of the e-th product with a K load.
+template <int DT>
+__device__ __forceinline__ u32x4 k_part(u32x4 raw, int e) {
+  if constexpr (DT == kBF16) return raw;
+  const unsigned x = raw[2 * e], y = raw[2 * e + 1];
+  return u32x4{e4m3x2_to_bf16<false>(x), e4m3x2_to_bf16<true>(x), e4m3x2_to_bf16<false>(y),
+               e4m3x2_to_bf16<true>(y)};
+}
 
 // Value j of a lane's part of two keys' V rows, side by side: in the dword's
 // low (j even) or high half's bytes for e4m3 codes, in its halves for bf16.
@@ -686,7 +736,11 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
   constexpr int kAll = 64 * NW;                      // threads
   constexpr int kStride = D + 4;                     // LDS row of the waves' sums, padded
   constexpr Cut cut{ROWS, 32 * KW};
+  // Keys that one wave reads come in whole 128-byte lines: lane (c, g) loads
+  // 16-byte part g + 4 (c % 2) of a line of key c & ~1, then of c | 1.  Products
+  // with both halves of q leave each score in two neighbouring rows, in one lane.
   constexpr bool kOnce = RW == 1 && Sh::kRowBytes >= 128;
+  constexpr bool kLines = kOnce;
   __shared__ __attribute__((aligned(16))) float sums[NW][16][kStride];
   __shared__ float sm[NW][16], sl[NW][16];
   const KvArgs& kv = a.kv;
@@ -702,6 +756,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
   const Shares shares(work.total, a.groups);
   int pos = shares.begin(blockIdx.x);
   const int end = shares.begin(blockIdx.x + 1);
+  Split split{};
 
   while (pos < end) {
     const Place pl = place_of(kv, cut, work, pos);
@@ -765,27 +820,21 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
           const size_t at = (size_t)max(w_page, 0) * kv.kv_heads + h;
           w_ks = good ? kv.k_scale[at] : 0.0f;
           w_vs = good ? kv.v_scale[at] : 0.0f;
-          arrived(w_ks);
-          arrived(w_vs);
         }
       }
     };
-    // A tile's two halves of 16 keys: where they lie, and their scales.
+    // A tile's two halves of 16 keys: where they lie, and the lane that has
+    // their page's scales.
     struct Half {
       size_t off;
-      float ks, vs;
+      int at;
       bool there;
     };
     const auto half_of = [&](int key) {
       Half x;
-      const int at = (key >> kv.log2p) - window;
-      const int page = lane_of(w_page, at);
+      x.at = (key >> kv.log2p) - window;
+      const int page = lane_of(w_page, x.at);
       x.there = page >= 0;
-      x.ks = x.vs = 1.0f;
-      if constexpr (DT == kFP8) {
-        x.ks = lane_of(w_ks, at);
-        x.vs = lane_of(w_vs, at);
-      }
       x.off = (size_t)max(page, 0) * page_bytes + (size_t)(h * P + (key & (P - 1))) * Sh::kRowBytes;
       return x;
     };
@@ -794,9 +843,17 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
     const auto load_k = [&](const Half (&at)[2]) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const unsigned char* kp = kv.k + at[u].off + c * Sh::kRowBytes + g * 16;
+        if constexpr (kLines) {
+          const unsigned char* kp =
+              kv.k + at[u].off + (c & ~1) * Sh::kRowBytes + (g + 4 * (c & 1)) * 16;
 #pragma unroll
-        for (int i = 0; i < Sh::kLoads; ++i) kf[u][i] = load_as<kOnce, u32x4>(kp + 64 * i);
+          for (int i = 0; i < Sh::kLoads; ++i)
+            kf[u][i] = load_as<kOnce, u32x4>(kp + Sh::kRowBytes * (i % 2) + 128 * (i / 2));
+        } else {
+          const unsigned char* kp = kv.k + at[u].off + c * Sh::kRowBytes + g * 16;
+#pragma unroll
+          for (int i = 0; i < Sh::kLoads; ++i) kf[u][i] = load_as<kOnce, u32x4>(kp + 64 * i);
+        }
       }
     };
     const auto load_v = [&](const Half (&at)[2]) {
@@ -825,7 +882,6 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
       int t = 0;
       do {
         const int key = key0 + 32 * t;
-        const float ks[2] = {now[0].ks, now[1].ks}, vs[2] = {now[0].vs, now[1].vs};
         const bool there[2] = {now[0].there, now[1].there};
         const bool good = there[0] && there[1];
         const bool masked = !good || key + 32 > lim_lo;   // some row does not see some key
@@ -836,23 +892,40 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            f32x4 s{0, 0, 0, 0};
+            if constexpr (kLines) {
+              f32x4 lo[2]{}, hi[2]{};                // even and odd keys
 #pragma unroll
-            for (int st = 0; st < Sh::kSteps; ++st) {
-              u32x4 kk;
-              if constexpr (DT == kBF16) {
-                kk = kf[u][st];
-              } else {
-                const u32x4 raw = kf[u][st / 2];
-                const unsigned x = raw[2 * (st % 2)], y = raw[2 * (st % 2) + 1];
-                kk = u32x4{e4m3x2_to_bf16<false>(x), e4m3x2_to_bf16<true>(x),
-                           e4m3x2_to_bf16<false>(y), e4m3x2_to_bf16<true>(y)};
-              }
-              s = mfma_bf16(kk, qf[rt][st], s);
+              for (int i = 0; i < Sh::kLoads; ++i)
+#pragma unroll
+                for (int e = 0; e < Sh::kPart; ++e) {
+                  const u32x4 kk = k_part<DT>(kf[u][i], e);
+                  const int st = 2 * Sh::kPart * (i / 2) + e;
+                  lo[i % 2] = mfma_bf16(kk, qf[rt][st], lo[i % 2]);
+                  hi[i % 2] = mfma_bf16(kk, qf[rt][st + Sh::kPart], hi[i % 2]);
+                }
+              settle(lo, hi);
+              sc[rt][u] = f32x4{lo[0][0] + hi[0][1], lo[1][0] + hi[1][1], lo[0][2] + hi[0][3],
+                                lo[1][2] + hi[1][3]};
+            } else {
+              f32x4 s{0, 0, 0, 0};
+#pragma unroll
+              for (int st = 0; st < Sh::kSteps; ++st)
+                s = mfma_bf16(k_part<DT>(kf[u][st / Sh::kPart], st % Sh::kPart), qf[rt][st], s);
+              sc[rt][u] = s;
             }
-            const float f = a.scale * ks[u];
+          }
+        settle(sc);
+        float ks[2], vs[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[rt][u][r] = s[r] * f;
+        for (int u = 0; u < 2; ++u) {
+          ks[u] = DT == kFP8 ? a.scale * lane_of(w_ks, now[u].at) : a.scale;
+          vs[u] = DT == kFP8 ? lane_of(w_vs, now[u].at) : 1.0f;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            sc[rt][u] *= ks[u];
             if (masked) {
 #pragma unroll
               for (int r = 0; r < 4; ++r)
@@ -940,7 +1013,8 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
         for (int sign = 0; sign < (DT == kBF16 ? 2 : 1); ++sign)
 #pragma unroll
           for (int j = 0; j < Sh::kTiles; ++j) {
-            const f32x4 hits = mfma_bf16(v_marks<DT, D>(vf, j, sign), seen, f32x4{0, 0, 0, 0});
+            f32x4 hits = mfma_bf16(v_marks<DT, D>(vf, j, sign), seen, f32x4{0, 0, 0, 0});
+            settle(hits);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
               if (hits[r] > 0.0f)
@@ -950,6 +1024,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
     }
 
     // The waves' sums, 16 rows of each row wave at a time.
+    settle(o);
     const bool whole = blocks == pl.nb;
     float* part = a.part + (size_t)(2 * blockIdx.x + (pl.blk == 0 ? 1 : 0)) * part_floats<D>(ROWS);
 #pragma unroll
@@ -1006,66 +1081,39 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
       }
       __syncthreads();
     }
+    if (pl.blk == 0 && !whole)
+      split = Split{shares.of(pos + pl.nb - 1) - (int)blockIdx.x + 1, row_count, rg * ROWS, q.q0, h};
     pos += blocks;
   }
+  if (tid == 0) a.splits[blockIdx.x] = split;
 }
 
-// Joins the segments of item blockIdx.x, kJoinRows<D> of its rows from blockIdx.y
-// on: per row D / 4 lanes (4 values each) in kJoinSets sets that take every
-// kJoinSets-th segment, kJoinAhead of them in flight, with the running maximum
-// and sum of a softmax; the sets' results are then added in order.
+// Joins the segments of the item that goes on from share blockIdx.x, kJoinRows<D>
+// of its rows from blockIdx.y on: per row D / 4 lanes (4 values each) in kJoinSets
+// sets that take every kJoinSets-th segment, kJoinAhead of them in flight, with
+// the running maximum and sum of a softmax; the sets' results are then added in
+// order.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinSets = 4;
 constexpr int kJoinAhead = 8;
 template <int D>
 constexpr int kJoinRows = kJoinThreads / (kJoinSets * (D / 4));
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const AttnArgs a, Cut cut) {
+__global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const AttnArgs a, int rows) {
   constexpr int kLanes = D / 4;
   __shared__ f32x4 sx[kJoinSets][kJoinRows<D>][kLanes];
   __shared__ float st[kJoinSets][kJoinRows<D>], sl[kJoinSets][kJoinRows<D>];
-  const KvArgs& kv = a.kv;
-  const int lane = threadIdx.x & 63;
-  const int rows = cut.rows;
-  // The item's sequence, its first block, and the number of all blocks.
-  int items = 0, total = 0, at_item = -1, first = 0;
-  Seq q{};
-  for (int s0 = 0; s0 < kv.S; s0 += 64) {
-    Seq mine{};
-    int n = 0, w = 0;
-    if (s0 + lane < kv.S) {
-      mine = load_seq(kv, s0 + lane);
-      n = seq_row_groups(mine, kv.group, cut) * kv.kv_heads;
-      w = seq_work(kv, mine, cut);
-    }
-    const int ni = add_count(wave_scan(n), items), wi = add_count(wave_scan(w), total);
-    int idx;
-    const int at = at_item < 0 ? scan_find(ni, items, blockIdx.x, idx) : -1;
-    if (at >= 0) {
-      at_item = idx;
-      q = Seq{lane_of(mine.q0, at), lane_of(mine.n, at), lane_of(mine.base, at),
-              lane_of(mine.cap, at)};
-      first = (at ? lane_of(wi, max(at - 1, 0)) : total) + idx * seq_blocks(q, cut);
-    }
-    items = lane_of(ni, 63);
-    total = lane_of(wi, 63);
-  }
-  if (at_item < 0) return;
-  const int nb = seq_blocks(q, cut);
-  const Shares shares(total, a.groups);
-  const int b0 = shares.of(first), n = shares.of(first + nb - 1) - b0 + 1;
-  if (n == 1) return;                                // one share holds the whole item
-  const int rgs = seq_row_groups(q, kv.group, cut);
-  const int h = at_item / rgs, rg = at_item % rgs;
-  const int row_count = min(q.n * kv.group - rg * rows, rows);
+  const Split sp = a.splits[blockIdx.x];
+  if (sp.n == 0 || blockIdx.y * kJoinRows<D> >= sp.rows) return;
+  const int n = sp.n;
   const int d = threadIdx.x % kLanes, set = threadIdx.x / kLanes % kJoinSets;
   const int slot = threadIdx.x / (kLanes * kJoinSets);
   const int row = blockIdx.y * kJoinRows<D> + slot;
-  if (blockIdx.y * kJoinRows<D> >= row_count) return;
-  const int from = min(row, row_count - 1);
-  // Segment k is share b0 + k's; the item's first one stands second in its share's pair.
+  const int from = min(row, sp.rows - 1);
+  // Segment k is share blockIdx.x + k's; the item's first one stands second in
+  // its share's pair.
   const size_t stride = part_floats<D>(rows);
-  const float* part = a.part + (size_t)(2 * b0) * stride;
+  const float* part = a.part + (size_t)(2 * blockIdx.x) * stride;
   float top = kNegInf, sum = 0.0f;
   f32x4 x{0, 0, 0, 0};
   for (int k0 = set; k0 < n; k0 += kJoinSets * kJoinAhead) {
@@ -1101,7 +1149,7 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
     sl[set][slot] = sum;
   }
   __syncthreads();
-  if (set != 0 || row >= row_count) return;
+  if (set != 0 || row >= sp.rows) return;
 #pragma unroll
   for (int k = 1; k < kJoinSets; ++k) top = fmaxf(top, st[k][slot]);
   sum = 0.0f;
@@ -1114,9 +1162,9 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
     x += f * sx[k][slot][d];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int r = rg * rows + row;
-  *reinterpret_cast<u32x2*>(a.out + ((size_t)(q.q0 + r / kv.group) * kv.kv_heads * kv.group +
-                                     h * kv.group + r % kv.group) * D + 4 * d) =
+  const int group = a.kv.group, r = sp.row0 + row;
+  *reinterpret_cast<u32x2*>(a.out + ((size_t)(sp.q0 + r / group) * a.kv.kv_heads * group +
+                                     sp.h * group + r % group) * D + 4 * d) =
       u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
 }
 
@@ -1250,13 +1298,13 @@ size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, i
   const RowCut r = row_cut(c, b, q_heads);
   const long long w = max_work(c, b, q_heads, r);
   const long long groups = w < kMaxGroups ? w : kMaxGroups;
-  return (size_t)(2 * groups) * (16 * r.rt * r.rw) * (c.head_dim + 2) * sizeof(float);
+  return kSplitBytes + (size_t)(2 * groups) * (16 * r.rt * r.rw) * (c.head_dim + 2) * sizeof(float);
 }
 
 constexpr int kGroupsPerCU = 1;
 
 template <int DT, int D, int RT, int RW>
-skinny_status launch_attention(const AttnArgs& a, int items, int rows, hipStream_t stream) {
+skinny_status launch_attention(const AttnArgs& a, int rows, hipStream_t stream) {
   constexpr int NW = waves_of(D);
   constexpr int ROWS = 16 * RT * RW;
   hipLaunchKernelGGL((skinny_kv_attention_k<DT, D, RT, RW, NW>), dim3(a.groups), dim3(64 * NW), 0,
@@ -1265,29 +1313,27 @@ skinny_status launch_attention(const AttnArgs& a, int items, int rows, hipStream
   if (a.groups == 1) return SKINNY_OK;               // nothing is split
   if (rows > ROWS) rows = ROWS;
   hipLaunchKernelGGL((skinny_kv_attention_join<D>),
-                     dim3(items, (rows + kJoinRows<D> - 1) / kJoinRows<D>), dim3(kJoinThreads), 0,
-                     stream, a, Cut{ROWS, 32 * (NW / RW)});
+                     dim3(a.groups - 1, (rows + kJoinRows<D> - 1) / kJoinRows<D>),
+                     dim3(kJoinThreads), 0, stream, a, ROWS);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 
 template <int DT, int D>
-skinny_status launch_rows(const AttnArgs& a, RowCut r, int items, int rows,
-                          hipStream_t stream) {
+skinny_status launch_rows(const AttnArgs& a, RowCut r, int rows, hipStream_t stream) {
   constexpr int RT = most_row_tiles(DT, D);
-  if (r.rt == 1 && r.rw == 1) return launch_attention<DT, D, 1, 1>(a, items, rows, stream);
-  if (r.rw == 2) return launch_attention<DT, D, RT, 2>(a, items, rows, stream);
-  if (r.rw == 4) return launch_attention<DT, D, RT, 4>(a, items, rows, stream);
-  if constexpr (RT == 2) return launch_attention<DT, D, 2, 1>(a, items, rows, stream);
-  if constexpr (RT == 1 && waves_of(D) == 8) return launch_attention<DT, D, 1, 8>(a, items, rows, stream);
+  if (r.rt == 1 && r.rw == 1) return launch_attention<DT, D, 1, 1>(a, rows, stream);
+  if (r.rw == 2) return launch_attention<DT, D, RT, 2>(a, rows, stream);
+  if (r.rw == 4) return launch_attention<DT, D, RT, 4>(a, rows, stream);
+  if constexpr (RT == 2) return launch_attention<DT, D, 2, 1>(a, rows, stream);
+  if constexpr (RT == 1 && waves_of(D) == 8) return launch_attention<DT, D, 1, 8>(a, rows, stream);
   return SKINNY_ERR_UNSUPPORTED;
 }
 
 template <int DT>
-skinny_status launch_dim(const AttnArgs& a, int d, RowCut r, int items, int rows,
-                          hipStream_t stream) {
-  if (d == 64) return launch_rows<DT, 64>(a, r, items, rows, stream);
-  if (d == 128) return launch_rows<DT, 128>(a, r, items, rows, stream);
-  return launch_rows<DT, 256>(a, r, items, rows, stream);
+skinny_status launch_dim(const AttnArgs& a, int d, RowCut r, int rows, hipStream_t stream) {
+  if (d == 64) return launch_rows<DT, 64>(a, r, rows, stream);
+  if (d == 128) return launch_rows<DT, 128>(a, r, rows, stream);
+  return launch_rows<DT, 256>(a, r, rows, stream);
 }
 
 }  // namespace
@@ -1386,8 +1432,7 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   if (!aligned(q, 16) || !aligned(out, 16)) return SKINNY_ERR_UNSUPPORTED;
   const RowCut r = row_cut(c, b, q_heads);
   const long long work = max_work(c, b, q_heads, r);
-  const long long items = max_items(c, b, q_heads, r);
-  if (work >= kMaxCount || items * kJoinThreads > 0xffffffffLL) return SKINNY_ERR_UNSUPPORTED;
+  if (work >= kMaxCount) return SKINNY_ERR_UNSUPPORTED;
   if (!workspace ||
       workspace_bytes < skinny_kv_attention_workspace_bytes(cache, batch, q_heads))
     return SKINNY_ERR_WORKSPACE;
@@ -1409,7 +1454,8 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   a.kv = kv_args(c, b, q_heads / c.kv_heads);
   a.q = (const __bf16*)q;
   a.out = (__bf16*)out;
-  a.part = (float*)workspace;
+  a.splits = (Split*)workspace;
+  a.part = (float*)((unsigned char*)workspace + kSplitBytes);
   a.scale = scale * 1.44269504088896340736f;         // log2 e: the kernel's softmax is in exp2
   long long groups = (long long)d.cus * kGroupsPerCU;
   if (groups > kMaxGroups) groups = kMaxGroups;
@@ -1418,8 +1464,8 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   const long long rows = (long long)b.tokens * (q_heads / c.kv_heads);
   const int most = rows < 128 ? (int)rows : 128;     // rows of an item at most
   if (c.dtype == SKINNY_KV_FP8)
-    return launch_dim<kFP8>(a, c.head_dim, r, (int)items, most, (hipStream_t)stream);
-  return launch_dim<kBF16>(a, c.head_dim, r, (int)items, most, (hipStream_t)stream);
+    return launch_dim<kFP8>(a, c.head_dim, r, most, (hipStream_t)stream);
+  return launch_dim<kBF16>(a, c.head_dim, r, most, (hipStream_t)stream);
 }
 
 }  // extern "C"
