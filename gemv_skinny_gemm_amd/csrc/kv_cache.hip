@@ -611,26 +611,24 @@ template <typename T>
 __device__ __forceinline__ void arrived(T& x) {
   asm volatile("" : "+v"(x));
 }
+template <typename T, int N>
+__device__ __forceinline__ void arrived(T (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) arrived(x[i]);
+}
 
 // Results of matrix instructions, before vector instructions read them.  The
 // hardware does not hold a vector read back until the matrix instruction has
 // written (12 slots are enough for these); the compiler fills the slots between
 // instructions of one basic block, but where a branch came in between it was
 // seen to leave them out, and the scores then lacked their last product.  The
-// slots stand here, and what depends on the values stays behind them.
-__device__ __forceinline__ void settle(f32x4& x) {
-  asm volatile("s_nop 7\n\ts_nop 3" : "+v"(x));
-}
-__device__ __forceinline__ void settle(f32x4 (&x)[2], f32x4 (&y)[2]) {
-  asm volatile("s_nop 7\n\ts_nop 3" : "+v"(x[0]), "+v"(x[1]), "+v"(y[0]), "+v"(y[1]));
-}
-template <int A, int B>
-__device__ __forceinline__ void settle(f32x4 (&x)[A][B]) {
-  settle(x[0][0]);
-#pragma unroll
-  for (int i = 0; i < A; ++i)
-#pragma unroll
-    for (int j = 0; j < B; ++j) asm volatile("" : "+v"(x[i][j]));
+// slots stand here: behind every value's matrix instructions, and what depends
+// on the values behind the slots (volatile asm keeps its order).
+template <typename... T>
+__device__ __forceinline__ void settle(T&... x) {
+  (arrived(x), ...);
+  asm volatile("s_nop 7\n\ts_nop 3");
+  (arrived(x), ...);
 }
 
 // Loads of the cache; NT with the nontemporal hint, for bytes that one wave of
