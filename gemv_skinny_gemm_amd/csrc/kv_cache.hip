@@ -133,12 +133,17 @@ struct AppendArgs {
   const float* inv_freq;   // [rot / 2], or NULL
   int q_heads;
   int head_dim;
-  int rot;                 // rotated values of a head, a multiple of 4
+  int rot;                 // rotated values of a head, a multiple of 16
   int interleaved;         // pairs (2i, 2i + 1) rather than (i, i + rot / 2)
-  int kv_blocks;           // leading workgroups, one per (touched page, head, k or v)
+  int turn_rows;           // rows whose cosines and sines lie in LDS at a time
+  int kv_blocks;           // workgroups of (touched page, head, k or v), the first of a launch
 };
 
-constexpr int kQHeadsPerBlock = 16;
+// A step of few rows takes a launch of skinny_kv_append_few, whose threads hold
+// four values each; more rows take two, of skinny_kv_append_q and
+// skinny_kv_append_kv, whose threads hold 16 and share the angles.
+constexpr int kQHeadsPerBlock = 16;  // few rows: query heads of one row's workgroup
+constexpr int kUnit = 16;            // values of a unit: two runs of 8, at pa and pb
 
 // cos and sin of pos * f.  The angle of a far position needs more than fp32
 // (an error of 2^-24 of 10^6 rad is 0.06 rad), so it is taken in fp64 and
@@ -157,13 +162,13 @@ __device__ __forceinline__ void rotation(int pos, float f, double& c, double& s)
 __device__ __forceinline__ float to_odd(double x) {
   const float f = (float)x;
   const double back = (double)f;
-  unsigned u = __builtin_bit_cast(unsigned, f);
-  if (back != x && x == x && (u & 0x7f800000u) != 0x7f800000u) {
-    // The nearest fp32 is one of the two neighbours; take the odd one.
-    if (!(u & 1)) u = (back < x) == (f > 0.0f || (f == 0.0f && x > 0.0)) ? u + 1 : u - 1;
-    if (f == 0.0f) u = 1u | (x < 0.0 ? 0x80000000u : 0u);
-  }
-  return __builtin_bit_cast(float, u);
+  const unsigned u = __builtin_bit_cast(unsigned, f);
+  // The nearest fp32 is one of the two neighbours; of an even one, take the other.
+  const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+  const bool move = back != x && finite && !(u & 1);
+  unsigned r = fabs(back) < fabs(x) ? u + 1 : u - 1;
+  if (f == 0.0f) r = 1u | (x < 0.0 ? 0x80000000u : 0u);
+  return __builtin_bit_cast(float, move ? r : u);
 }
 
 __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
@@ -189,16 +194,16 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b) {
   return r;
 }
 
-// A unit of four values of a head: two neighbours at pa and two at pb that
+// A quad is four values of a head: two neighbours at pa and two at pb that
 // rotate together (half-split: partners lie rot / 2 apart), or, unrotated or
 // interleaved, four in a row.
-struct Unit {
+struct Quad {
   int pa, pb;
   bool turned;
 };
 
-__device__ __forceinline__ Unit unit_of(int j, int rot, int interleaved) {
-  Unit u;
+__device__ __forceinline__ Quad quad_of(int j, int rot, int interleaved) {
+  Quad u;
   u.turned = 4 * j < rot;
   const bool split = u.turned && !interleaved;
   u.pa = split ? 2 * j : 4 * j;
@@ -206,7 +211,7 @@ __device__ __forceinline__ Unit unit_of(int j, int rot, int interleaved) {
   return u;
 }
 
-// Rotates a unit's values by the frequencies (c0, s0), (c1, s1) in fp64.
+// Rotates a quad's values by the frequencies (c0, s0), (c1, s1) in fp64.
 __device__ __forceinline__ f32x4 turn(unsigned a, unsigned b, int interleaved, double c0, double s0,
                                       double c1, double s1) {
   const double a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
@@ -223,6 +228,85 @@ __device__ __forceinline__ f32x4 turn(unsigned a, unsigned b, int interleaved, d
     r[3] = to_odd(a1 * s1 + b1 * c1);
   }
   return r;
+}
+
+// Unit j of a head: half-split, its runs lie rot / 2 apart and rotate with each
+// other; interleaved, or not rotated, they are neighbours.
+struct Unit {
+  int pa, pb;
+  bool turned;
+};
+
+__device__ __forceinline__ Unit unit_of(int j, int rot, int interleaved) {
+  Unit u;
+  u.turned = kUnit * j < rot;
+  const bool split = u.turned && !interleaved;
+  u.pa = split ? 8 * j : kUnit * j;
+  u.pb = split ? rot / 2 + 8 * j : kUnit * j + 8;
+  return u;
+}
+
+// cos and sin of one row's angles in LDS: unit j rotates by frequencies 8j .. 8j
+// + 7, and entry e of all units lies together, so that the units' lanes read
+// neighbours.
+__device__ __forceinline__ int turn_at(int freq, int rot) {
+  return freq % 8 * (rot / kUnit) + freq / 8;
+}
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+
+// A unit's values in fp64, rotated.
+struct Values {
+  double a[8], b[8];
+};
+__device__ __forceinline__ Values unpack(u32x4 x, u32x4 y) {
+  Values v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.a[2 * i] = bf16_lo(x[i]);
+    v.a[2 * i + 1] = bf16_hi(x[i]);
+    v.b[2 * i] = bf16_lo(y[i]);
+    v.b[2 * i + 1] = bf16_hi(y[i]);
+  }
+  return v;
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(Values& v, const f64x2* cs, int j, int rot) {
+  const int step = rot / kUnit;
+  const auto pair = [&](double& a, double& b, int e) {
+    const f64x2 t = cs[e * step + j];
+    const double x = a * t[0] - b * t[1];
+    b = a * t[1] + b * t[0];
+    a = x;
+  };
+  if constexpr (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pair(v.a[2 * i], v.a[2 * i + 1], i);
+      pair(v.b[2 * i], v.b[2 * i + 1], 4 + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pair(v.a[i], v.b[i], i);
+  }
+}
+
+// Eight fp64 -> bf16, each rounded once, to nearest even.  fp64 -> fp32 -> bf16
+// rounds wrongly only where the fp32 value lies half way between two bf16 ones
+// (its low 16 bits are 0x8000), once in 2^16; then it goes over rounding to odd.
+__device__ __forceinline__ u32x4 round_bf16(const double (&v)[8]) {
+  float f[8];
+  bool half = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[i] = (float)v[i];
+    half = half || (__builtin_bit_cast(unsigned, f[i]) & 0xffffu) == 0x8000u;
+  }
+  if (half) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_odd(v[i]);
+  }
+  return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+               pack_bf16(f[6], f[7])};
 }
 
 // Sequence of batch row t, or -1 for a row behind the last one.
@@ -249,7 +333,7 @@ __device__ __forceinline__ int touched(const Seq& q, int log2p, int& first) {
 // kQHeadsPerBlock query heads.  The rotated rows wait in LDS (as fp32 rounded
 // to odd) between the maximum and the rounding.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs a) {
+__global__ __launch_bounds__(kThreads) void skinny_kv_append_few(const AppendArgs a) {
   extern __shared__ f32x4 rows[];                    // [new rows][D / 4]
   __shared__ float smax[kWaves];
   const KvArgs& kv = a.kv;
@@ -276,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
     unsigned* dst = reinterpret_cast<unsigned*>(a.q_out + (size_t)t * a.q_heads * D);
     for (int i = h0 * upr + tid; i < h1 * upr; i += kThreads) {
       const int h = i / upr, j = i % upr;
-      const Unit u = unit_of(j, a.rot, a.interleaved);
+      const Quad u = quad_of(j, a.rot, a.interleaved);
       unsigned x = src[(h * D + u.pa) / 2], y = src[(h * D + u.pb) / 2];
       if (u.turned) {
         const f32x4 r = turn(x, y, a.interleaved, cs[4 * j], cs[4 * j + 1], cs[4 * j + 2],
@@ -326,7 +410,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
   float top = 0.0f;
   for (int i = tid; i < count * upr; i += kThreads) {
     const int r = i / upr, j = i % upr;
-    const Unit u = unit_of(j, rot, a.interleaved);
+    const Quad u = quad_of(j, rot, a.interleaved);
     const unsigned x = src[(r * row_elems + u.pa) / 2], y = src[(r * row_elems + u.pb) / 2];
     f32x4 w{bf16_lo(x), bf16_hi(x), bf16_lo(y), bf16_hi(y)};
     if (u.turned) {
@@ -378,11 +462,259 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_k(const AppendArgs 
     }
     for (int i = tid; i < count * upr; i += kThreads) {
       const int r = i / upr, j = i % upr;
-      const Unit u = unit_of(j, rot, a.interleaved);
+      const Quad u = quad_of(j, rot, a.interleaved);
       const f32x4 w = rows[i];
       unsigned short* dst = reinterpret_cast<unsigned short*>(block + (size_t)(older + r) * D);
       dst[u.pa / 2] = (unsigned short)pack_e4m3((float)(w[0] * inv), (float)(w[1] * inv));
       dst[u.pb / 2] = (unsigned short)pack_e4m3((float)(w[2] * inv), (float)(w[3] * inv));
+    }
+    if (tid == 0) *scale = now;
+  }
+}
+
+// Query heads of many rows: a workgroup takes kQRows rows, one per wave, whose
+// angles its threads compute together.
+constexpr int kQRows = kWaves;
+constexpr int kQAhead = 2;           // units of a lane in flight
+template <bool INTERLEAVED>
+__global__ __launch_bounds__(kThreads) void skinny_kv_append_q(const AppendArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ int places[kQRows];
+  const KvArgs& kv = a.kv;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = uniform(tid >> 6);
+  const int D = a.head_dim;
+  const int upr = D / kUnit;                         // units of a head
+  const int units = a.q_heads * upr;
+  const size_t row_elems = (size_t)(a.q_heads + 2 * kv.kv_heads) * D;
+  f64x2* cs = reinterpret_cast<f64x2*>(lds);         // [kQRows][rot / 2]
+  const int t = blockIdx.x * kQRows + wave;
+  const __bf16* src = a.qkv + t * row_elems;
+  __bf16* dst = a.q_out + (size_t)t * a.q_heads * D;
+  u32x4 x[kQAhead], y[kQAhead];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int e = 0; e < kQAhead; ++e) {
+      const int i = min(i0 + 64 * e + lane, units - 1);
+      const Unit u = unit_of(i % upr, a.rot, INTERLEAVED);
+      x[e] = *reinterpret_cast<const u32x4*>(src + (size_t)(i / upr) * D + u.pa);
+      y[e] = *reinterpret_cast<const u32x4*>(src + (size_t)(i / upr) * D + u.pb);
+    }
+  };
+  int s = -1;
+  if (t < kv.T) {
+    load(0);                                         // on their way while the row is looked up
+    s = find_row(kv, t);
+    if (s >= 0) {
+      const Seq q = load_seq(kv, s);
+      if (lane == 0) places[wave] = q.base + (t - q.q0);
+    }
+  }
+  if (s < 0 && lane == 0) places[wave] = 0;
+  __syncthreads();
+  for (int i = tid; i < kQRows * (a.rot / 2); i += kThreads) {
+    const int r = i / (a.rot / 2), f = i % (a.rot / 2);
+    double c, sn;
+    rotation(places[r], a.inv_freq[f], c, sn);
+    cs[r * (a.rot / 2) + turn_at(f, a.rot)] = f64x2{c, sn};
+  }
+  __syncthreads();
+  if (s < 0) return;
+  const f64x2* mine = cs + wave * (a.rot / 2);
+  for (int i0 = 0; i0 < units; i0 += 64 * kQAhead) {
+    u32x4 nx[kQAhead], ny[kQAhead];
+#pragma unroll
+    for (int e = 0; e < kQAhead; ++e) {
+      nx[e] = x[e];
+      ny[e] = y[e];
+    }
+    if (i0 + 64 * kQAhead < units) load(i0 + 64 * kQAhead);
+#pragma unroll
+    for (int e = 0; e < kQAhead; ++e) {
+      const int i = i0 + 64 * e + lane;
+      if (i >= units) continue;
+      const Unit u = unit_of(i % upr, a.rot, INTERLEAVED);
+      if (u.turned) {
+        Values v = unpack(nx[e], ny[e]);
+        turn<INTERLEAVED>(v, mine, i % upr, a.rot);
+        nx[e] = round_bf16(v.a);
+        ny[e] = round_bf16(v.b);
+      }
+      *reinterpret_cast<u32x4*>(dst + (size_t)(i / upr) * D + u.pa) = nx[e];
+      *reinterpret_cast<u32x4*>(dst + (size_t)(i / upr) * D + u.pb) = ny[e];
+    }
+  }
+}
+
+// The same of many rows: one workgroup per (page, KV head, k or v),
+// turn_rows rows' angles in LDS at a time.
+template <int DT, bool INTERLEAVED>
+__global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ float smax[kWaves];
+  const KvArgs& kv = a.kv;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int D = a.head_dim;
+  const int upr = D / kUnit;                         // units of a head
+  const size_t row_elems = (size_t)(a.q_heads + 2 * kv.kv_heads) * D;
+  f64x2* cs = reinterpret_cast<f64x2*>(lds);         // [turn_rows][rot / 2]
+
+  const bool is_v = blockIdx.x & 1;
+  const int h = (blockIdx.x >> 1) % kv.kv_heads;
+  const int unit = (blockIdx.x >> 1) / kv.kv_heads;
+  // The unit-th page touched, sequences in order.
+  int s = -1, page_no = 0, before = 0;
+  for (int s0 = 0; s0 < kv.S && s < 0; s0 += 64) {
+    int first = 0, c = 0;
+    if (s0 + lane < kv.S) c = touched(load_seq(kv, s0 + lane), kv.log2p, first);
+    const int incl = add_count(wave_scan(c), before);
+    int idx;
+    const int at = scan_find(incl, before, unit, idx);
+    if (at >= 0) {
+      s = s0 + at;
+      page_no = lane_of(first, at) + idx;
+    }
+    before = lane_of(incl, 63);
+  }
+  if (s < 0) return;
+  const Seq q = uniform(load_seq(kv, s));
+  const int P = 1 << kv.log2p;
+  const int lo = max(max(q.base, 0), page_no << kv.log2p);
+  const int hi = min(min(q.base + q.n, q.cap), (page_no + 1) << kv.log2p);
+  const int count = hi - lo;                         // new rows, 1 .. P
+  const int older = lo & (P - 1);                    // rows of this sequence before them
+  const int page = kv.table[(size_t)s * kv.max_pages + page_no];
+  if (page < 0 || page >= kv.pages) return;
+  constexpr int kEsize = DT == kBF16 ? 2 : 1;
+  unsigned char* block = (is_v ? kv.v : kv.k) + ((size_t)page * kv.kv_heads + h) * P * D * kEsize;
+  const int rot = is_v ? 0 : a.rot;
+  f32x4* rows = reinterpret_cast<f32x4*>(lds + (size_t)a.turn_rows * a.rot * 8);   // [count][D / 4]
+  const __bf16* src = a.qkv + (size_t)(q.q0 + (lo - q.base)) * row_elems +
+                      (size_t)(a.q_heads + (is_v ? kv.kv_heads : 0) + h) * D;
+  float* scale = nullptr;
+  float had = 0.0f;
+  if constexpr (DT == kFP8) {
+    scale = (is_v ? kv.v_scale : kv.k_scale) + (size_t)page * kv.kv_heads + h;
+    if (older) had = *scale;
+  }
+
+  float top = 0.0f;
+  const int step = rot ? a.turn_rows : count;
+  for (int r0 = 0; r0 < count; r0 += step) {
+    const int n = min(step, count - r0);
+    if (rot) {
+      if (r0) __syncthreads();
+      // A thread takes a frequency over a run of rows: the first row's angle, then
+      // a complex product by the frequency's own per row (fp64: a few 2^-53).
+      const int half = rot / 2, runs = max(1, kThreads / half), run = (n + runs - 1) / runs;
+      for (int i = tid; i < half * runs; i += kThreads) {
+        const int f = i % half, r1 = i / half * run;
+        if (r1 >= n) continue;
+        double c, sn, cf, sf;
+        rotation(lo + r0 + r1, a.inv_freq[f], c, sn);
+        rotation(1, a.inv_freq[f], cf, sf);
+        for (int r = r1; r < min(r1 + run, n); ++r) {
+          cs[r * half + turn_at(f, rot)] = f64x2{c, sn};
+          const double next = c * cf - sn * sf;
+          sn = c * sf + sn * cf;
+          c = next;
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = r0 * upr + tid; i < (r0 + n) * upr; i += kThreads) {
+      const int r = i / upr, j = i % upr;
+      const Unit u = unit_of(j, rot, INTERLEAVED);
+      u32x4 x = *reinterpret_cast<const u32x4*>(src + r * row_elems + u.pa);
+      u32x4 y = *reinterpret_cast<const u32x4*>(src + r * row_elems + u.pb);
+      if constexpr (DT == kBF16) {
+        if (u.turned) {
+          Values v = unpack(x, y);
+          turn<INTERLEAVED>(v, cs + (r - r0) * (rot / 2), j, rot);
+          x = round_bf16(v.a);
+          y = round_bf16(v.b);
+        }
+        __bf16* dst = reinterpret_cast<__bf16*>(block) + (size_t)(older + r) * D;
+        *reinterpret_cast<u32x4*>(dst + u.pa) = x;
+        *reinterpret_cast<u32x4*>(dst + u.pb) = y;
+      } else {
+        float w[kUnit];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[2 * e] = bf16_lo(x[e]);
+          w[2 * e + 1] = bf16_hi(x[e]);
+          w[8 + 2 * e] = bf16_lo(y[e]);
+          w[8 + 2 * e + 1] = bf16_hi(y[e]);
+        }
+        if (u.turned) {
+          Values v = unpack(x, y);
+          turn<INTERLEAVED>(v, cs + (r - r0) * (rot / 2), j, rot);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[e] = to_odd(v.a[e]);
+            w[8 + e] = to_odd(v.b[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) {
+          const float m = fabsf(w[e]);
+          if (m < __builtin_inff()) top = fmaxf(top, m);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)                  // neighbours in LDS: one quarter of all units
+          rows[e * count * upr + i] = f32x4{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]};
+      }
+    }
+  }
+  if constexpr (DT == kFP8) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if (lane == 0) smax[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+    // The smallest power of two that brings the largest value to 448 = 1.75 * 2^8 or below.
+    const unsigned bits = __builtin_bit_cast(unsigned, top);
+    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+    e = max(e, kMinScaleExp);
+    const float need = __builtin_bit_cast(float, (unsigned)(e + 127) << 23);
+    const float now = had >= need ? had : need;
+    const double inv = 1.0 / (double)now;
+    if (older && now != had) {
+      // The older codes move to the larger scale: exact for a power of two,
+      // but for codes that become subnormal.
+      const float ratio = (float)((double)had * inv);
+      unsigned* old = reinterpret_cast<unsigned*>(block);
+      for (int i = tid; i < older * D / 4; i += kThreads) {
+        const unsigned c = old[i];
+        const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
+        const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+        old[i] = pack_e4m3(x[0] * ratio, x[1] * ratio) |
+                 pack_e4m3(y[0] * ratio, y[1] * ratio) << 16;
+      }
+    }
+    // A power of two divides exactly in fp32; another scale (the user's) in fp64.
+    const bool exact = (__builtin_bit_cast(unsigned, now) & 0x7fffffu) == 0;
+    const float finv = (float)inv;
+    for (int i = tid; i < count * upr; i += kThreads) {
+      const int r = i / upr, j = i % upr;
+      const Unit u = unit_of(j, rot, INTERLEAVED);
+      unsigned c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f32x4 w = rows[e * count * upr + i];
+        if (exact) {
+          w *= finv;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = (float)(w[k] * inv);
+        }
+        c[e] = pack_e4m3(w[0], w[1]) | pack_e4m3(w[2], w[3]) << 16;
+      }
+      unsigned char* dst = block + (size_t)(older + r) * D;
+      *reinterpret_cast<u32x2*>(dst + u.pa) = u32x2{c[0], c[1]};
+      *reinterpret_cast<u32x2*>(dst + u.pb) = u32x2{c[2], c[3]};
     }
     if (tid == 0) *scale = now;
   }
@@ -1169,6 +1501,9 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
 // ---------------------------------------------------------------------------
 // Host side.
 
+// Most rows of a step that skinny_kv_append_few takes.
+constexpr int kFewRows = 1024;
+
 size_t pool_elems(const skinny_kv_cache& c) {
   return (size_t)c.pages * c.kv_heads * c.page_tokens * c.head_dim;
 }
@@ -1351,7 +1686,7 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
   if (rotary_dim < 0 || rotary_dim > c.head_dim || (rotary_dim > 0) != (inv_freq != nullptr) ||
       (interleaved != 0 && interleaved != 1))
     return SKINNY_ERR_INVALID_ARG;
-  if (rotary_dim % 4 != 0) return SKINNY_ERR_UNSUPPORTED;
+  if (rotary_dim % kUnit != 0) return SKINNY_ERR_UNSUPPORTED;
   if (!aligned(qkv, 16) || !aligned(q_out, 16) || (inv_freq && !aligned(inv_freq, 4)))
     return SKINNY_ERR_UNSUPPORTED;
   const size_t width = (size_t)(q_heads + 2 * c.kv_heads) * c.head_dim;
@@ -1373,7 +1708,10 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
   long long units = b.tokens / c.page_tokens + 2 * seqs;
   if (units > b.tokens) units = b.tokens;
   const long long kvb = units * c.kv_heads * 2;
-  const long long qb = (long long)b.tokens * ((q_heads + kQHeadsPerBlock - 1) / kQHeadsPerBlock);
+  const bool few = b.tokens <= kFewRows;
+  const long long qb = few
+      ? (long long)b.tokens * ((q_heads + kQHeadsPerBlock - 1) / kQHeadsPerBlock)
+      : (b.tokens + kQRows - 1) / kQRows;
   if ((kvb + qb) * kThreads > 0xffffffffLL) return SKINNY_ERR_UNSUPPORTED;   // threads of a launch
   DeviceInfo d;
   st = device_info(&d);
@@ -1390,21 +1728,33 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
   a.rot = rotary_dim;
   a.interleaved = interleaved;
   a.kv_blocks = (int)kvb;
+  const bool fp8 = c.dtype == SKINNY_KV_FP8;
   const int most = b.tokens < c.page_tokens ? b.tokens : c.page_tokens;
-  const size_t rows = c.dtype == SKINNY_KV_FP8 ? (size_t)most * c.head_dim * 4 : 0;
-  const size_t turns = (size_t)rotary_dim * 8;      // cos and sin in fp64
-  const size_t lds = rows > turns ? rows : turns;
-  const void* fn = c.dtype == SKINNY_KV_FP8 ? (const void*)skinny_kv_append_k<kFP8>
-                                            : (const void*)skinny_kv_append_k<kBF16>;
+  const size_t rows = fp8 ? (size_t)most * c.head_dim * 4 : 0;
+  const dim3 kvg((unsigned)kvb), qg((unsigned)qb), all((unsigned)(kvb + qb)), threads(kThreads);
+  const hipStream_t hs = (hipStream_t)stream;
+  if (few) {
+    const size_t turns = (size_t)rotary_dim * 8;    // cos and sin in fp64
+    const size_t lds = rows > turns ? rows : turns;
+    if (fp8) hipLaunchKernelGGL(skinny_kv_append_few<kFP8>, all, threads, lds, hs, a);
+    else hipLaunchKernelGGL(skinny_kv_append_few<kBF16>, all, threads, lds, hs, a);
+    return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
+  }
+  // Angles in 32 KB of LDS beside the rows, in 16 KB where the rows take most of it.
+  const int room = rows <= 64 * 1024 ? 32 * 1024 : 16 * 1024;
+  a.turn_rows = rotary_dim ? room / (rotary_dim * 8) : 0;
+  const size_t lds = (size_t)a.turn_rows * rotary_dim * 8 + rows;
+  using Kernel = void (*)(AppendArgs);
+  const Kernel fn = fp8 ? (interleaved ? skinny_kv_append_kv<kFP8, true> : skinny_kv_append_kv<kFP8, false>)
+                        : (interleaved ? skinny_kv_append_kv<kBF16, true> : skinny_kv_append_kv<kBF16, false>);
+  const Kernel fq = interleaved ? skinny_kv_append_q<true> : skinny_kv_append_q<false>;
   if (lds > 64 * 1024 &&
-      hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+      hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) !=
+          hipSuccess)
     return SKINNY_ERR_HIP;
-  if (c.dtype == SKINNY_KV_FP8)
-    hipLaunchKernelGGL(skinny_kv_append_k<kFP8>, dim3((unsigned)(kvb + qb)), dim3(kThreads), lds,
-                       (hipStream_t)stream, a);
-  else
-    hipLaunchKernelGGL(skinny_kv_append_k<kBF16>, dim3((unsigned)(kvb + qb)), dim3(kThreads), lds,
-                       (hipStream_t)stream, a);
+  hipLaunchKernelGGL(fn, kvg, threads, lds, hs, a);
+  if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
+  hipLaunchKernelGGL(fq, qg, threads, (size_t)kQRows * rotary_dim * 8, hs, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 

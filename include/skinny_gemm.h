@@ -495,7 +495,7 @@ typedef struct skinny_kv_batch {
  *             y: query heads, then key heads, then value heads; 16-byte aligned
  *   inv_freq  [rotary_dim / 2] fp32, or NULL with rotary_dim 0 (no rotation)
  *   q_out     [tokens][q_heads head_dim] bf16, written, 16-byte aligned
- * Of each query and key head the first rotary_dim values (a multiple of 4) are
+ * Of each query and key head the first rotary_dim values (a multiple of 16) are
  * rotated in pairs (a, b) = (x[i], x[i + rotary_dim / 2]), or (x[2i], x[2i + 1])
  * with interleaved = 1, by the angle t = position * inv_freq[i]:
  * a' = a cos t - b sin t, b' = a sin t + b cos t, angles and products in fp64.

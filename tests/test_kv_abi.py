@@ -75,7 +75,7 @@ def test_bad_batches(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(qkv=None), INVALID), (dict(out=None), INVALID), (dict(q_heads=0), INVALID),
     (dict(q_heads=7), INVALID), (dict(q_heads=2048), UNSUPPORTED), (dict(rot=-4), INVALID),
-    (dict(rot=68), INVALID), (dict(rot=6), UNSUPPORTED), (dict(rot=0), INVALID),
+    (dict(rot=68), INVALID), (dict(rot=24), UNSUPPORTED), (dict(rot=0), INVALID),
     (dict(freq=None), INVALID), (dict(inter=2), INVALID), (dict(qkv=QKV + 8), UNSUPPORTED),
     (dict(out=OUT + 2), UNSUPPORTED), (dict(freq=FREQ + 1), UNSUPPORTED),
     (dict(out=QKV), INVALID), (dict(out=K + 64), INVALID), (dict(out=KS + 16), INVALID),

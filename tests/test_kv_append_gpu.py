@@ -38,10 +38,38 @@ def test_shapes(dtype, seqs, P, D):
 
 @pytest.mark.parametrize("dtype", ["fp8", "bf16"])
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("rot", [0, 4, 12, 64, 128])
+@pytest.mark.parametrize("rot", [0, 16, 48, 64, 128])
 def test_rotations(dtype, interleaved, rot):
     c = kv.Case([(3, 50), (2, 2)], D=128, dtype=dtype, seed=rot)
     check(c, kv.frequencies(rot) if rot else None, interleaved)
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "bf16"])
+@pytest.mark.parametrize("P,D,rot,interleaved", [(64, 128, 128, False), (16, 64, 48, True),
+                                                 (128, 256, 256, False), (32, 128, 0, False),
+                                                 (128, 128, 16, True)])
+def test_many_rows(dtype, P, D, rot, interleaved):
+    """More than a thousand rows: the kernels of long steps, ragged, with rows of
+    no sequence, a sequence in the middle of a page, one that begins and one
+    without rows."""
+    c = kv.Case([(700, 1003), (1, 77), (0, 40), (333, 333), (3, 300), (40, 40 + P)], P=P, D=D,
+                hq=5 if D < 256 else 2, hkv=1, dtype=dtype, seed=D + rot, tail=5)
+    check(c, kv.frequencies(rot) if rot else None, interleaved)
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "bf16"])
+def test_many_rows_bad_batches(dtype):
+    """Long steps with lengths below the rows and past the table, pages outside
+    the pool and values that are no finite numbers."""
+    c = kv.Case([(600, 700), (500, 900), (30, 50)], D=64, hq=3, hkv=3, dtype=dtype, seed=70, tail=3,
+                max_pages=50)
+    c.kv_len[0] = 580                     # 20 rows at positions below 0
+    c.table[1, 28] = -1                   # 900 positions: 100 past the table's 800
+    c.table[1, 45] = c.pages
+    x = c.qkv.reshape(c.T, -1)
+    x[40, 3 * 64 + 5] = kv.BF16_NAN
+    x[300, 6 * 64 + 7] = kv.BF16_INF
+    check(c, kv.frequencies(64) if dtype == "bf16" else None)
 
 
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (64, 8), (5, 5), (40, 8), (33, 3)])
@@ -171,6 +199,27 @@ def test_twice_is_once():
     torch.cuda.synchronize()
     for n, t in first.items():
         assert torch.equal(t.view(torch.uint8), c.dev[n].view(torch.uint8)), n
+
+
+def test_few_and_many_rows_agree():
+    """The same rows in one long step and in short ones: the same cache and
+    queries (bf16, where a row's bytes do not depend on its neighbours)."""
+    f = kv.frequencies(128)
+    long = kv.Case([(1500, 1600)], P=64, D=128, hq=4, hkv=2, dtype="bf16", seed=71).upload()
+    long.append(f)
+    torch.cuda.synchronize()
+    want = {n: long.dev[n].clone() for n in ("k", "v", "out")}
+    short = kv.Case([(1500, 1600)], P=64, D=128, hq=4, hkv=2, dtype="bf16", seed=71).upload()
+    freq = torch.from_numpy(f).cuda()
+    for at in range(0, 1500, 300):
+        q0 = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+        n = torch.tensor([100 + at + 300], dtype=torch.int32, device="cuda")
+        batch = sg.make_batch(q0, n, short.dev["table"], 300)
+        sg.kv_append(short.cache, batch, short.dev["qkv"][at:at + 300], freq,
+                     short.dev["out"][at:at + 300])
+    torch.cuda.synchronize()
+    for name, t in want.items():
+        assert torch.equal(t.view(torch.uint8), short.dev[name].view(torch.uint8)), name
 
 
 def test_graph_replays_and_streams():
