@@ -135,13 +135,12 @@ struct AppendArgs {
   int head_dim;
   int rot;                 // rotated values of a head, a multiple of 16
   int interleaved;         // pairs (2i, 2i + 1) rather than (i, i + rot / 2)
-  int turn_rows;           // rows whose cosines and sines lie in LDS at a time
   int kv_blocks;           // workgroups of (touched page, head, k or v), the first of a launch
 };
 
-// A step of few rows takes a launch of skinny_kv_append_few, whose threads hold
-// four values each; more rows take two, of skinny_kv_append_q and
-// skinny_kv_append_kv, whose threads hold 16 and share the angles.
+// A step of few rows takes skinny_kv_append_few, whose threads hold four values
+// each; more rows take skinny_kv_append_many, whose threads hold 16 and share the
+// angles.
 constexpr int kQHeadsPerBlock = 16;  // few rows: query heads of one row's workgroup
 constexpr int kUnit = 16;            // values of a unit: two runs of 8, at pa and pb
 
@@ -192,6 +191,27 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b) {
   if (a != a) r = (r & 0xff00u) | 0x7fu;
   if (b != b) r = (r & 0x00ffu) | 0x7f00u;
   return r;
+}
+
+// The smallest power of two that brings a page's largest value to 448 = 1.75 *
+// 2^8 or below.
+__device__ __forceinline__ float page_scale(float top) {
+  const unsigned bits = __builtin_bit_cast(unsigned, top);
+  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+  return __builtin_bit_cast(float, (unsigned)(max(e, kMinScaleExp) + 127) << 23);
+}
+
+// A page's older codes, four to a dword, from scale `had` to 1 / inv: exact for
+// a power of two, but for codes that become subnormal.
+__device__ __forceinline__ void rescale(unsigned* codes, int n, float had, double inv, int tid) {
+  const float ratio = (float)((double)had * inv);
+  for (int i = tid; i < n; i += kThreads) {
+    const unsigned c = codes[i];
+    const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
+    const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+    codes[i] = pack_e4m3(x[0] * ratio, x[1] * ratio) |
+               pack_e4m3(y[0] * ratio, y[1] * ratio) << 16;
+  }
 }
 
 // A quad is four values of a head: two neighbours at pa and two at pb that
@@ -440,26 +460,10 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_few(const AppendArg
     const float had = older ? *scale : 0.0f;
     __syncthreads();
     top = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
-    // The smallest power of two that brings the largest value to 448 = 1.75 * 2^8 or below.
-    const unsigned bits = __builtin_bit_cast(unsigned, top);
-    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-    e = max(e, kMinScaleExp);
-    const float need = __builtin_bit_cast(float, (unsigned)(e + 127) << 23);
+    const float need = page_scale(top);
     const float now = had >= need ? had : need;
     const double inv = 1.0 / (double)now;
-    if (older && now != had) {
-      // The older codes move to the larger scale: exact for a power of two,
-      // but for codes that become subnormal.
-      const float ratio = (float)((double)had * inv);
-      unsigned* old = reinterpret_cast<unsigned*>(block);
-      for (int i = tid; i < older * upr; i += kThreads) {
-        const unsigned c = old[i];
-        const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
-        const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
-        old[i] = pack_e4m3(x[0] * ratio, x[1] * ratio) |
-                 pack_e4m3(y[0] * ratio, y[1] * ratio) << 16;
-      }
-    }
+    if (older && now != had) rescale(reinterpret_cast<unsigned*>(block), older * upr, had, inv, tid);
     for (int i = tid; i < count * upr; i += kThreads) {
       const int r = i / upr, j = i % upr;
       const Quad u = quad_of(j, rot, a.interleaved);
@@ -473,13 +477,12 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_few(const AppendArg
 }
 
 // Query heads of many rows: a workgroup takes kQRows rows, one per wave, whose
-// angles its threads compute together.
+// angles (cs: [kQRows][rot / 2]) its threads compute together.
 constexpr int kQRows = kWaves;
 constexpr int kQAhead = 2;           // units of a lane in flight
 template <bool INTERLEAVED>
-__global__ __launch_bounds__(kThreads) void skinny_kv_append_q(const AppendArgs a) {
-  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ int places[kQRows];
+__device__ __forceinline__ void append_queries(const AppendArgs& a, int block, f64x2* cs,
+                                               int (&places)[kQRows]) {
   const KvArgs& kv = a.kv;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -488,8 +491,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_q(const AppendArgs 
   const int upr = D / kUnit;                         // units of a head
   const int units = a.q_heads * upr;
   const size_t row_elems = (size_t)(a.q_heads + 2 * kv.kv_heads) * D;
-  f64x2* cs = reinterpret_cast<f64x2*>(lds);         // [kQRows][rot / 2]
-  const int t = blockIdx.x * kQRows + wave;
+  const int t = block * kQRows + wave;
   const __bf16* src = a.qkv + t * row_elems;
   __bf16* dst = a.q_out + (size_t)t * a.q_heads * D;
   u32x4 x[kQAhead], y[kQAhead];
@@ -547,19 +549,27 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_q(const AppendArgs 
   }
 }
 
-// The same of many rows: one workgroup per (page, KV head, k or v),
-// turn_rows rows' angles in LDS at a time.
-template <int DT, bool INTERLEAVED>
-__global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs a) {
+// A step of many rows: one workgroup per (page, KV head, k or v), then those of
+// the query heads, which fill the chip beside the pages' arithmetic.  A pass takes a
+// unit per thread, kThreads * kUnit / D rows, whose angles lie in LDS; an e4m3
+// page's values wait in registers between the maximum and the rounding (PASSES of
+// 16 fp32, rounded to odd).
+template <int DT, bool INTERLEAVED, int PASSES>
+__global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ float smax[kWaves];
+  __shared__ int places[kQRows];
   const KvArgs& kv = a.kv;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int D = a.head_dim;
   const int upr = D / kUnit;                         // units of a head
   const size_t row_elems = (size_t)(a.q_heads + 2 * kv.kv_heads) * D;
-  f64x2* cs = reinterpret_cast<f64x2*>(lds);         // [turn_rows][rot / 2]
+  f64x2* cs = reinterpret_cast<f64x2*>(lds);         // [rows of a pass][rot / 2]
+  if ((int)blockIdx.x >= a.kv_blocks) {
+    append_queries<INTERLEAVED>(a, blockIdx.x - a.kv_blocks, cs, places);
+    return;
+  }
 
   const bool is_v = blockIdx.x & 1;
   const int h = (blockIdx.x >> 1) % kv.kv_heads;
@@ -590,7 +600,6 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs
   constexpr int kEsize = DT == kBF16 ? 2 : 1;
   unsigned char* block = (is_v ? kv.v : kv.k) + ((size_t)page * kv.kv_heads + h) * P * D * kEsize;
   const int rot = is_v ? 0 : a.rot;
-  f32x4* rows = reinterpret_cast<f32x4*>(lds + (size_t)a.turn_rows * a.rot * 8);   // [count][D / 4]
   const __bf16* src = a.qkv + (size_t)(q.q0 + (lo - q.base)) * row_elems +
                       (size_t)(a.q_heads + (is_v ? kv.kv_heads : 0) + h) * D;
   float* scale = nullptr;
@@ -599,13 +608,25 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs
     scale = (is_v ? kv.v_scale : kv.k_scale) + (size_t)page * kv.kv_heads + h;
     if (older) had = *scale;
   }
+  const int step = kThreads / upr;                   // rows of a pass
+  const int j = tid % upr;
+  const Unit u = unit_of(j, rot, INTERLEAVED);
+  u32x4 x[PASSES], y[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const __bf16* row = src + (size_t)min(p * step + tid / upr, count - 1) * row_elems;
+    x[p] = *reinterpret_cast<const u32x4*>(row + u.pa);
+    y[p] = *reinterpret_cast<const u32x4*>(row + u.pb);
+  }
 
   float top = 0.0f;
-  const int step = rot ? a.turn_rows : count;
-  for (int r0 = 0; r0 < count; r0 += step) {
-    const int n = min(step, count - r0);
+  float w[DT == kFP8 ? PASSES : 1][kUnit];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int r0 = p * step, n = min(step, count - r0), r = r0 + tid / upr;
+    if (n <= 0) break;
     if (rot) {
-      if (r0) __syncthreads();
+      if (p) __syncthreads();
       // A thread takes a frequency over a run of rows: the first row's angle, then
       // a complex product by the frequency's own per row (fp64: a few 2^-53).
       const int half = rot / 2, runs = max(1, kThreads / half), run = (n + runs - 1) / runs;
@@ -615,8 +636,8 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs
         double c, sn, cf, sf;
         rotation(lo + r0 + r1, a.inv_freq[f], c, sn);
         rotation(1, a.inv_freq[f], cf, sf);
-        for (int r = r1; r < min(r1 + run, n); ++r) {
-          cs[r * half + turn_at(f, rot)] = f64x2{c, sn};
+        for (int k = r1; k < min(r1 + run, n); ++k) {
+          cs[k * half + turn_at(f, rot)] = f64x2{c, sn};
           const double next = c * cf - sn * sf;
           sn = c * sf + sn * cf;
           c = next;
@@ -624,47 +645,41 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs
       }
       __syncthreads();
     }
-    for (int i = r0 * upr + tid; i < (r0 + n) * upr; i += kThreads) {
-      const int r = i / upr, j = i % upr;
-      const Unit u = unit_of(j, rot, INTERLEAVED);
-      u32x4 x = *reinterpret_cast<const u32x4*>(src + r * row_elems + u.pa);
-      u32x4 y = *reinterpret_cast<const u32x4*>(src + r * row_elems + u.pb);
-      if constexpr (DT == kBF16) {
+    const bool live = r < count;
+    Values v;
+    if (live && u.turned) {
+      v = unpack(x[p], y[p]);
+      turn<INTERLEAVED>(v, cs + (r - r0) * (rot / 2), j, rot);
+    }
+    if constexpr (DT == kBF16) {
+      if (live) {
         if (u.turned) {
-          Values v = unpack(x, y);
-          turn<INTERLEAVED>(v, cs + (r - r0) * (rot / 2), j, rot);
-          x = round_bf16(v.a);
-          y = round_bf16(v.b);
+          x[p] = round_bf16(v.a);
+          y[p] = round_bf16(v.b);
         }
         __bf16* dst = reinterpret_cast<__bf16*>(block) + (size_t)(older + r) * D;
-        *reinterpret_cast<u32x4*>(dst + u.pa) = x;
-        *reinterpret_cast<u32x4*>(dst + u.pb) = y;
-      } else {
-        float w[kUnit];
+        *reinterpret_cast<u32x4*>(dst + u.pa) = x[p];
+        *reinterpret_cast<u32x4*>(dst + u.pb) = y[p];
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[2 * e] = bf16_lo(x[e]);
-          w[2 * e + 1] = bf16_hi(x[e]);
-          w[8 + 2 * e] = bf16_lo(y[e]);
-          w[8 + 2 * e + 1] = bf16_hi(y[e]);
+      for (int e = 0; e < 4; ++e) {
+        w[p][2 * e] = bf16_lo(x[p][e]);
+        w[p][2 * e + 1] = bf16_hi(x[p][e]);
+        w[p][8 + 2 * e] = bf16_lo(y[p][e]);
+        w[p][8 + 2 * e + 1] = bf16_hi(y[p][e]);
+      }
+      if (live && u.turned) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[p][e] = to_odd(v.a[e]);
+          w[p][8 + e] = to_odd(v.b[e]);
         }
-        if (u.turned) {
-          Values v = unpack(x, y);
-          turn<INTERLEAVED>(v, cs + (r - r0) * (rot / 2), j, rot);
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            w[e] = to_odd(v.a[e]);
-            w[8 + e] = to_odd(v.b[e]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kUnit; ++e) {
-          const float m = fabsf(w[e]);
-          if (m < __builtin_inff()) top = fmaxf(top, m);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)                  // neighbours in LDS: one quarter of all units
-          rows[e * count * upr + i] = f32x4{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]};
+      for (int e = 0; e < kUnit; ++e) {
+        const float m = fabsf(w[p][e]);
+        if (live && m < __builtin_inff()) top = fmaxf(top, m);
       }
     }
   }
@@ -674,44 +689,24 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_kv(const AppendArgs
     if (lane == 0) smax[tid >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
-    // The smallest power of two that brings the largest value to 448 = 1.75 * 2^8 or below.
-    const unsigned bits = __builtin_bit_cast(unsigned, top);
-    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-    e = max(e, kMinScaleExp);
-    const float need = __builtin_bit_cast(float, (unsigned)(e + 127) << 23);
+    const float need = page_scale(top);
     const float now = had >= need ? had : need;
     const double inv = 1.0 / (double)now;
-    if (older && now != had) {
-      // The older codes move to the larger scale: exact for a power of two,
-      // but for codes that become subnormal.
-      const float ratio = (float)((double)had * inv);
-      unsigned* old = reinterpret_cast<unsigned*>(block);
-      for (int i = tid; i < older * D / 4; i += kThreads) {
-        const unsigned c = old[i];
-        const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
-        const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
-        old[i] = pack_e4m3(x[0] * ratio, x[1] * ratio) |
-                 pack_e4m3(y[0] * ratio, y[1] * ratio) << 16;
-      }
-    }
+    if (older && now != had) rescale(reinterpret_cast<unsigned*>(block), older * D / 4, had, inv, tid);
     // A power of two divides exactly in fp32; another scale (the user's) in fp64.
     const bool exact = (__builtin_bit_cast(unsigned, now) & 0x7fffffu) == 0;
     const float finv = (float)inv;
-    for (int i = tid; i < count * upr; i += kThreads) {
-      const int r = i / upr, j = i % upr;
-      const Unit u = unit_of(j, rot, INTERLEAVED);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = p * step + tid / upr;
+      if (r >= count) break;
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) w[p][e] = exact ? w[p][e] * finv : (float)(w[p][e] * inv);
       unsigned c[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f32x4 w = rows[e * count * upr + i];
-        if (exact) {
-          w *= finv;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = (float)(w[k] * inv);
-        }
-        c[e] = pack_e4m3(w[0], w[1]) | pack_e4m3(w[2], w[3]) << 16;
-      }
+      for (int e = 0; e < 4; ++e)
+        c[e] = pack_e4m3(w[p][4 * e], w[p][4 * e + 1]) |
+               pack_e4m3(w[p][4 * e + 2], w[p][4 * e + 3]) << 16;
       unsigned char* dst = block + (size_t)(older + r) * D;
       *reinterpret_cast<u32x2*>(dst + u.pa) = u32x2{c[0], c[1]};
       *reinterpret_cast<u32x2*>(dst + u.pb) = u32x2{c[2], c[3]};
@@ -1501,8 +1496,25 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
 // ---------------------------------------------------------------------------
 // Host side.
 
-// Most rows of a step that skinny_kv_append_few takes.
-constexpr int kFewRows = 1024;
+using Kernel = void (*)(AppendArgs);
+template <int DT, bool INTERLEAVED>
+Kernel append_many_as(int passes) {
+  return passes <= 1   ? skinny_kv_append_many<DT, INTERLEAVED, 1>
+         : passes <= 2 ? skinny_kv_append_many<DT, INTERLEAVED, 2>
+         : passes <= 4 ? skinny_kv_append_many<DT, INTERLEAVED, 4>
+                       : skinny_kv_append_many<DT, INTERLEAVED, 8>;
+}
+template <int DT>
+Kernel append_many(int passes, bool interleaved) {
+  return interleaved ? append_many_as<DT, true>(passes) : append_many_as<DT, false>(passes);
+}
+
+// Steps that skinny_kv_append_few takes: as many rows, their e4m3 pages' values
+// within that much LDS.  Measured on MI355X with 64 + 2 x 8 heads of 128, few
+// against many: 4.3 / 7.8 us at 1 row, 7.1 / 8.7 at 32, 8.9 / 9.2 at 64, 10.9 /
+// 9.9 at 128, 21.9 / 15.7 at 1024.
+constexpr int kFewRows = 64;
+constexpr size_t kFewLds = 32 * 1024;
 
 size_t pool_elems(const skinny_kv_cache& c) {
   return (size_t)c.pages * c.kv_heads * c.page_tokens * c.head_dim;
@@ -1703,12 +1715,15 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
   for (int i = 0; i < 4; ++i)                       // the pools and scales are written too
     if (sh[i].lo != sh[i].hi && meets(sh[i], sh + i + 1, kSharedRanges + 1 - i))
       return SKINNY_ERR_INVALID_ARG;
+  const bool fp8 = c.dtype == SKINNY_KV_FP8;
+  const int most = b.tokens < c.page_tokens ? b.tokens : c.page_tokens;   // rows of a page
+  const size_t rows = fp8 ? (size_t)most * c.head_dim * 4 : 0;
+  const bool few = b.tokens <= kFewRows && rows <= kFewLds;
   // n rows of a sequence fall into at most n pages, and at most (n - 2) / P + 2.
   const long long seqs = b.seqs < b.tokens ? b.seqs : b.tokens;
   long long units = b.tokens / c.page_tokens + 2 * seqs;
   if (units > b.tokens) units = b.tokens;
   const long long kvb = units * c.kv_heads * 2;
-  const bool few = b.tokens <= kFewRows;
   const long long qb = few
       ? (long long)b.tokens * ((q_heads + kQHeadsPerBlock - 1) / kQHeadsPerBlock)
       : (b.tokens + kQRows - 1) / kQRows;
@@ -1728,10 +1743,7 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
   a.rot = rotary_dim;
   a.interleaved = interleaved;
   a.kv_blocks = (int)kvb;
-  const bool fp8 = c.dtype == SKINNY_KV_FP8;
-  const int most = b.tokens < c.page_tokens ? b.tokens : c.page_tokens;
-  const size_t rows = fp8 ? (size_t)most * c.head_dim * 4 : 0;
-  const dim3 kvg((unsigned)kvb), qg((unsigned)qb), all((unsigned)(kvb + qb)), threads(kThreads);
+  const dim3 all((unsigned)(kvb + qb)), threads(kThreads);
   const hipStream_t hs = (hipStream_t)stream;
   if (few) {
     const size_t turns = (size_t)rotary_dim * 8;    // cos and sin in fp64
@@ -1740,21 +1752,11 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
     else hipLaunchKernelGGL(skinny_kv_append_few<kBF16>, all, threads, lds, hs, a);
     return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
   }
-  // Angles in 32 KB of LDS beside the rows, in 16 KB where the rows take most of it.
-  const int room = rows <= 64 * 1024 ? 32 * 1024 : 16 * 1024;
-  a.turn_rows = rotary_dim ? room / (rotary_dim * 8) : 0;
-  const size_t lds = (size_t)a.turn_rows * rotary_dim * 8 + rows;
-  using Kernel = void (*)(AppendArgs);
-  const Kernel fn = fp8 ? (interleaved ? skinny_kv_append_kv<kFP8, true> : skinny_kv_append_kv<kFP8, false>)
-                        : (interleaved ? skinny_kv_append_kv<kBF16, true> : skinny_kv_append_kv<kBF16, false>);
-  const Kernel fq = interleaved ? skinny_kv_append_q<true> : skinny_kv_append_q<false>;
-  if (lds > 64 * 1024 &&
-      hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) !=
-          hipSuccess)
-    return SKINNY_ERR_HIP;
-  hipLaunchKernelGGL(fn, kvg, threads, lds, hs, a);
-  if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
-  hipLaunchKernelGGL(fq, qg, threads, (size_t)kQRows * rotary_dim * 8, hs, a);
+  const int step = kThreads * kUnit / c.head_dim;   // rows of a pass
+  const int passes = (most + step - 1) / step;      // at most 8
+  const Kernel fn = fp8 ? append_many<kFP8>(passes, interleaved) : append_many<kBF16>(passes, interleaved);
+  const size_t lds = (size_t)(step > kQRows ? step : kQRows) * rotary_dim * 8;   // cos and sin in fp64
+  hipLaunchKernelGGL(fn, all, threads, lds, hs, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 

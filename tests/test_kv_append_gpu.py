@@ -49,9 +49,8 @@ def test_rotations(dtype, interleaved, rot):
                                                  (128, 256, 256, False), (32, 128, 0, False),
                                                  (128, 128, 16, True)])
 def test_many_rows(dtype, P, D, rot, interleaved):
-    """More than a thousand rows: the kernels of long steps, ragged, with rows of
-    no sequence, a sequence in the middle of a page, one that begins and one
-    without rows."""
+    """The kernel of long steps, ragged, with rows of no sequence, a sequence in
+    the middle of a page, one that begins and one without rows."""
     c = kv.Case([(700, 1003), (1, 77), (0, 40), (333, 333), (3, 300), (40, 40 + P)], P=P, D=D,
                 hq=5 if D < 256 else 2, hkv=1, dtype=dtype, seed=D + rot, tail=5)
     check(c, kv.frequencies(rot) if rot else None, interleaved)
@@ -201,6 +200,13 @@ def test_twice_is_once():
         assert torch.equal(t.view(torch.uint8), c.dev[n].view(torch.uint8)), n
 
 
+@pytest.mark.parametrize("rows", [63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("dtype,D", [("fp8", 64), ("fp8", 256), ("bf16", 128)])
+def test_row_counts_around_the_kernels_border(rows, dtype, D):
+    check(kv.Case([(rows - 3, rows + 30), (3, 3)], P=128, D=D, hq=2, hkv=1, dtype=dtype, seed=rows),
+          kv.frequencies(D))
+
+
 def test_few_and_many_rows_agree():
     """The same rows in one long step and in short ones: the same cache and
     queries (bf16, where a row's bytes do not depend on its neighbours)."""
@@ -211,12 +217,12 @@ def test_few_and_many_rows_agree():
     want = {n: long.dev[n].clone() for n in ("k", "v", "out")}
     short = kv.Case([(1500, 1600)], P=64, D=128, hq=4, hkv=2, dtype="bf16", seed=71).upload()
     freq = torch.from_numpy(f).cuda()
-    for at in range(0, 1500, 300):
-        q0 = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
-        n = torch.tensor([100 + at + 300], dtype=torch.int32, device="cuda")
-        batch = sg.make_batch(q0, n, short.dev["table"], 300)
-        sg.kv_append(short.cache, batch, short.dev["qkv"][at:at + 300], freq,
-                     short.dev["out"][at:at + 300])
+    for at in range(0, 1500, 60):
+        q0 = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
+        n = torch.tensor([100 + at + 60], dtype=torch.int32, device="cuda")
+        batch = sg.make_batch(q0, n, short.dev["table"], 60)
+        sg.kv_append(short.cache, batch, short.dev["qkv"][at:at + 60], freq,
+                     short.dev["out"][at:at + 60])
     torch.cuda.synchronize()
     for name, t in want.items():
         assert torch.equal(t.view(torch.uint8), short.dev[name].view(torch.uint8)), name
