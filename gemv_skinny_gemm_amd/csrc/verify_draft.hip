@@ -79,6 +79,7 @@ struct VerifyArgs {
   int* accepted;         // [S]
   Stat* stats;           // [2][T][slices]
   unsigned long long* weight;   // [S][slices][kWaves] fp64
+  float* drafted;        // [2][T] logit of the token drafted at each row (NaN: none)
   int* arrived;          // [S]
   int T, S, V, slices;
 };
@@ -159,11 +160,43 @@ __device__ __forceinline__ T reduce16(T x, F f) {
   x = f(x, dpp<kRor + 4>(x));
   return f(x, dpp<kRor + 8>(x));
 }
+struct Halves {
+  unsigned a, b;
+};
+__device__ __forceinline__ Halves across16(unsigned u) {
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned a = s[0], b = s[1];
+  return Halves{a, b};
+}
+__device__ __forceinline__ Halves across32(unsigned u) {
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned a = s[0], b = s[1];
+  return Halves{a, b};
+}
+// f of a value and that of the lane 16 (32) away, in the same order for both.
+#define SKINNY_JOIN(across)                                                           \
+  if constexpr (sizeof(T) == 4) {                                                      \
+    const Halves h = across(__builtin_bit_cast(unsigned, x));                          \
+    return f(__builtin_bit_cast(T, h.a), __builtin_bit_cast(T, h.b));                  \
+  } else {                                                                             \
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);            \
+    const Halves lo = across((unsigned)u), hi = across((unsigned)(u >> 32));           \
+    const unsigned long long a = (unsigned long long)hi.a << 32 | lo.a;                \
+    const unsigned long long b = (unsigned long long)hi.b << 32 | lo.b;                \
+    return f(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));                      \
+  }
+template <typename T, typename F>
+__device__ __forceinline__ T join16(T x, F f) {
+  SKINNY_JOIN(across16)
+}
+template <typename T, typename F>
+__device__ __forceinline__ T join32(T x, F f) {
+  SKINNY_JOIN(across32)
+}
+#undef SKINNY_JOIN
 template <typename T, typename F>
 __device__ __forceinline__ T reduce64(T x, F f) {
-  x = reduce16(x, f);
-  x = f(x, __shfl_xor(x, 16));
-  return f(x, __shfl_xor(x, 32));
+  return join32(join16(reduce16(x, f), f), f);
 }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ int lower(int a, int b) { return min(a, b); }
@@ -267,6 +300,11 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   const int n0 = slice * kSlice + wave * kSub;
   float l[kPer];
   load_sub<L, VEC>(src, n0, a.V, l);               // on its way while the row's sequence is found
+  if (slice == 0 && tid == 0) {
+    const int d = row + 1 < a.T ? a.tokens[row + 1] : -1;
+    a.drafted[(size_t)which * a.T + row] =
+        d >= 0 && d < a.V ? logit<L>(src, d) : __builtin_nanf("");
+  }
   if (row == 0 && which == 0) {
     for (int i = tid; i < a.S * kWaves; i += kThreads)
       a.weight[((size_t)(i / kWaves) * a.slices + slice) * kWaves + i % kWaves] = kNotYet;
@@ -392,6 +430,8 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
   }
   const bool greedy = !(t > 0.0f);
   if (greedy && slice != 0) return;
+  // What a row gives out if its draft is kept; on its way while it is decided.
+  const int kept = tid + 1 < r.n ? a.tokens[r.q0 + tid + 1] : -1;
   const double c = greedy ? 0.0 : 1.4426950408889634074 / (double)t;
 
   // The first row that stops: a rejection, or the last row.  kRowLanes lanes per row.
@@ -410,8 +450,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
       RowStat p{kNegInf, 0x7fffffff, 0.0}, q{kNegInf, 0x7fffffff, 0.0};
       const Stat* ps = a.stats + (size_t)row * a.slices;
       const Stat* qs = a.stats + ((size_t)(asks ? a.T : 0) + row) * a.slices;
-      const float pl = in ? logit<L>(a.logits, (size_t)row * a.V + d) : kNegInf;
-      const float ql = in && asks ? logit<L>(a.draft, (size_t)row * a.V + d) : kNegInf;
+      const float pl = a.drafted[row], ql = a.drafted[(asks ? a.T : 0) + row];
       for (int k = l; k - l < a.slices; k += kRowLanes * kAhead) {
         Stat x[kAhead], y[kAhead];
         load_stats(ps, k, a.slices, x);
@@ -479,7 +518,6 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
         __hip_atomic_store(words + slice * kWaves + wave, __builtin_bit_cast(unsigned long long, w),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (tid == 0)
       is_last = __hip_atomic_fetch_add(&a.arrived[s], 1, __ATOMIC_RELAXED,
@@ -611,8 +649,10 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
     token = found < a.V ? found : positive;
   }
 
-  for (int i = tid; i < r.n; i += kThreads)
-    a.out_tokens[r.q0 + i] = i < st.row ? a.tokens[r.q0 + i + 1] : i == st.row ? token : -1;
+  for (int i = tid; i < r.n; i += kThreads) {
+    const int next = i == tid ? kept : i + 1 < r.n ? a.tokens[r.q0 + i + 1] : -1;
+    a.out_tokens[r.q0 + i] = i < st.row ? next : i == st.row ? token : -1;
+  }
   if (tid == 0) a.accepted[s] = st.row;
 }
 
@@ -624,7 +664,7 @@ int slices_of(int vocab) { return (vocab + kSlice - 1) / kSlice; }
 size_t up(size_t b) { return (b + 255) / 256 * 256; }
 
 struct Layout {
-  size_t stats, weight, arrived, total;
+  size_t stats, weight, drafted, arrived, total;
 };
 
 Layout layout(int rows, int seqs, int vocab) {
@@ -632,7 +672,8 @@ Layout layout(int rows, int seqs, int vocab) {
   Layout w;
   w.stats = 0;
   w.weight = up((size_t)2 * rows * sl * sizeof(Stat));
-  w.arrived = w.weight + up((size_t)seqs * sl * kWaves * sizeof(double));
+  w.drafted = w.weight + up((size_t)seqs * sl * kWaves * sizeof(double));
+  w.arrived = w.drafted + up((size_t)2 * rows * sizeof(float));
   w.total = w.arrived + up((size_t)seqs * sizeof(int));
   return w;
 }
@@ -725,6 +766,7 @@ skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
   unsigned char* ws = (unsigned char*)workspace;
   a.stats = (Stat*)(ws + w.stats);
   a.weight = (unsigned long long*)(ws + w.weight);
+  a.drafted = (float*)(ws + w.drafted);
   a.arrived = (int*)(ws + w.arrived);
   a.T = v.rows;
   a.S = v.seqs;
