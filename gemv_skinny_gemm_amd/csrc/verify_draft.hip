@@ -57,6 +57,7 @@ constexpr int kPer = kSub / 64;                    // per lane
 constexpr int kRowLanes = 16;                      // lanes that read one row's slices
 constexpr int kRowsAtOnce = kThreads / kRowLanes;
 constexpr int kFind = kSub / kThreads;             // entries of a thread in the last search
+constexpr int kBatch = 4;                          // exponentials at a time
 constexpr float kNegInf = -__builtin_inff();
 constexpr unsigned long long kNotYet = ~0ull;      // a NaN that no sum is
 constexpr int kMaxPolls = 1 << 16;
@@ -110,28 +111,56 @@ struct Taylor {
     for (int k = 1; k < 12; ++k) c[k] = c[k - 1] * 0.69314718055994530942 / k;
   }
 };
-__device__ __forceinline__ double exp2_below(double y) {
+// N at a time, step by step: a chain of dependent fp64 instructions alone leaves
+// the ALUs waiting.
+template <int N>
+__device__ __forceinline__ void exp2_below(double (&y)[N]) {
   constexpr Taylor t;
   constexpr double kShift = 6755399441055744.0;    // 1.5 * 2^52
-  const double s = y + kShift;
-  const double f = y - (s - kShift);
-  double p = t.c[11];
+  double s[N], f[N], p[N];
 #pragma unroll
-  for (int k = 10; k >= 0; --k) p = fma(p, f, t.c[k]);
-  const unsigned long long n = __builtin_bit_cast(unsigned long long, s) << 52;
-  const double r = __builtin_bit_cast(double, __builtin_bit_cast(unsigned long long, p) + n);
-  return y >= -1000.0 ? r : 0.0;
+  for (int i = 0; i < N; ++i) s[i] = y[i] + kShift;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[i] = y[i] - (s[i] - kShift);
+    p[i] = t.c[11];
+  }
+#pragma unroll
+  for (int k = 10; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], f[i], t.c[k]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const unsigned n = (unsigned)__builtin_bit_cast(unsigned long long, s[i]);
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, p[i]);
+    const unsigned hi = (unsigned)(b >> 32) + (n << 20);
+    const double r = __builtin_bit_cast(double, (unsigned long long)hi << 32 | (unsigned)b);
+    y[i] = y[i] >= -1000.0 ? r : 0.0;
+  }
 }
 
 // exp((l - top) / t) with c = log2 e / t, top below +inf: 1 at the maximum, 0
 // for NaN and -inf (and for top -inf).
-__device__ __forceinline__ double finite_weight(float l, double top, double c) {
-  return exp2_below(((double)l - top) * c);
+template <int N>
+__device__ __forceinline__ void finite_weights(const float* l, double top, double c,
+                                               double (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = ((double)l[i] - top) * c;
+  exp2_below(w);
 }
 // The same for any top; where it is +inf, 1 at the infinite entries and 0 elsewhere.
+template <int N>
+__device__ __forceinline__ void weights_of(const float* l, float top, double c, double (&w)[N]) {
+  finite_weights(l, (double)top, c, w);
+  if (top == -kNegInf) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = l[i] == top ? 1.0 : 0.0;
+  }
+}
 __device__ __forceinline__ double weight_of(float l, float top, double c) {
-  const double w = finite_weight(l, top, c);
-  return top == -kNegInf ? (l == top ? 1.0 : 0.0) : w;
+  double w[1];
+  weights_of(&l, top, c, w);
+  return w[0];
 }
 
 // Lane exchanges on the vector ALUs: rotation within 16 lanes, and with the
@@ -333,7 +362,12 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
     if (wtop < -kNegInf) {
       const double dtop = wtop;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) sum += finite_weight(l[j], dtop, c);
+      for (int j = 0; j < kPer; j += kBatch) {
+        double w[kBatch];
+        finite_weights(l + j, dtop, c, w);
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) sum += w[e];
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) sum += l[j] == wtop ? 1.0 : 0.0;
@@ -380,9 +414,15 @@ __device__ __forceinline__ void add_stats(const Stat (&x)[kAhead], double c, Row
   const float had = r.top;
 #pragma unroll
   for (int e = 0; e < kAhead; ++e) take_first(x[e].max, x[e].first, r.top, r.first);
-  r.sum *= weight_of(had, r.top, c);
+  float top[kAhead + 1];
+  double w[kAhead + 1];
 #pragma unroll
-  for (int e = 0; e < kAhead; ++e) r.sum += x[e].sum * weight_of(x[e].max, r.top, c);
+  for (int e = 0; e < kAhead; ++e) top[e] = x[e].max;
+  top[kAhead] = had;
+  weights_of(top, r.top, c, w);
+  r.sum *= w[kAhead];
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e) r.sum += x[e].sum * w[e];
 }
 __device__ __forceinline__ void row_end(double c, RowStat& r) {
   const float had = r.top;
@@ -400,16 +440,28 @@ struct Stop {
   int drafted;           // without a draft distribution: the rejected token, else -1
 };
 
-// max(0, p - q) of one entry; `plain`: p itself.  Both products are rounded
-// before the difference (no fused multiply-add), so equal rows leave exactly 0.
-template <typename L>
-__device__ __forceinline__ double residual(const Stop& st, double c, float lp, float lq, int n,
-                                           bool plain) {
+// max(0, p - q) of N entries from logits lp and lq (without with_q, q is 1 at the
+// rejected token, or nothing); n: their places; `plain`: p itself.  Both products
+// are rounded before the difference (no fused multiply-add), so equal rows leave
+// exactly 0.
+template <int N>
+__device__ __forceinline__ void residuals(const Stop& st, double c, const float* lp,
+                                          const float* lq, bool with_q, const int (&n)[N],
+                                          bool plain, double (&w)[N]) {
 #pragma clang fp contract(off)
-  const double p = weight_of(lp, st.p_top, c) * st.p_inv;
-  if (plain) return p;
-  if (n == st.drafted) return 0.0;
-  return fmax(p - weight_of(lq, st.q_top, c) * st.q_inv, 0.0);
+  weights_of(lp, st.p_top, c, w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] *= st.p_inv;
+  if (plain) return;
+  if (with_q) {
+    double q[N];
+    weights_of(lq, st.q_top, c, q);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = fmax(w[i] - q[i] * st.q_inv, 0.0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = n[i] == st.drafted ? 0.0 : w[i];
+  }
 }
 
 template <typename L, bool VEC>
@@ -508,11 +560,18 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
       float lp[kPer], lq[kPer];
       const int n0 = (slice * kWaves + wave) * kSub;
       load_sub<L, VEC>(lp_row, n0, a.V, lp);
-      if (with_q) load_sub<L, VEC>(lq_row, n0, a.V, lq);
+      load_sub<L, VEC>(lq_row, n0, a.V, lq);         // without q, lp again
       double w = 0.0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        w += residual<L>(st, c, lp[j], with_q ? lq[j] : kNegInf, n0 + index_of<L, VEC>(j), final);
+      for (int j = 0; j < kPer; j += kBatch) {
+        int n[kBatch];
+        double x[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) n[e] = n0 + index_of<L, VEC>(j + e);
+        residuals(st, c, lp + j, lq + j, with_q, n, final, x);
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) w += x[e];
+      }
       w = reduce64(w, plus);
       if (lane == 0)
         __hip_atomic_store(words + slice * kWaves + wave, __builtin_bit_cast(unsigned long long, w),
@@ -618,15 +677,21 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
     for (int k = 0; k < (plain ? kWaves : 1); ++k) {
       const int m0 = (sub_s + k) * kSub + tid * kFind;
       double x[kFind], sum = 0.0;
-      int some = -1;
+      float lp[kFind], lq[kFind];
+      int n[kFind], some = -1;
 #pragma unroll
       for (int j = 0; j < kFind; ++j) {
-        const int n = m0 + j, at = min(n, a.V - 1);
-        const float vp = logit<L>(lp_row, at), vq = with_q ? logit<L>(lq_row, at) : kNegInf;
-        const double y = n < a.V ? residual<L>(st, c, vp, vq, n, plain || final) : 0.0;
-        if (y > 0.0) some = n;
-        x[j] = y;
-        sum += y;
+        n[j] = m0 + j;
+        const int at = min(n[j], a.V - 1);
+        lp[j] = logit<L>(lp_row, at);
+        lq[j] = with_q ? logit<L>(lq_row, at) : kNegInf;
+        if (n[j] >= a.V) lp[j] = __builtin_nanf("");
+      }
+      residuals(st, c, lp, lq, with_q, n, plain || final, x);
+#pragma unroll
+      for (int j = 0; j < kFind; ++j) {
+        if (x[j] > 0.0) some = n[j];
+        sum += x[j];
       }
       const double incl = scan64(sum);
       if (lane == 63) wsum[wave] = incl;
@@ -639,8 +704,11 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
         run += x[j];
         if (hit == a.V && x[j] > 0.0 && run > goal_s) hit = m0 + j;
       }
-      if (hit < a.V) atomicMin(&found, hit);
-      if (some >= 0) atomicMax(&positive, some);
+      // One lane per wave: the lanes' places ascend, and 64 atomics on one word
+      // are 64 in a row.
+      const unsigned long long bh = __ballot(hit < a.V), bs = __ballot(some >= 0);
+      if (bh && lane == __builtin_ctzll(bh)) atomicMin(&found, hit);
+      if (bs && lane == 63 - __builtin_clzll(bs)) atomicMax(&positive, some);
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) before += wsum[w];
       __syncthreads();
