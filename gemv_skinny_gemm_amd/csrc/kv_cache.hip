@@ -59,6 +59,7 @@ struct KvArgs {
   int pages;
   int kv_heads;
   int group;               // query heads per KV head
+  int group_shift;         // its log2, or -1: a division is some 200 cycles of a short call
   int log2p;               // log2 of the page's tokens
 };
 
@@ -68,6 +69,10 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ int lane_of(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
 __device__ __forceinline__ float lane_of(float x, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+__device__ __forceinline__ int by_group(const KvArgs& a, int x) {
+  return a.group_shift >= 0 ? x >> a.group_shift : x / a.group;
 }
 
 // One sequence: rows q0 .. q0 + n of the batch; row i at position base + i,
@@ -877,7 +882,7 @@ __device__ __forceinline__ Place place_of(const KvArgs& a, Cut cut, const Work& 
 struct Shares {
   int base, rest;
   __device__ __forceinline__ Shares(int total, int groups)
-      : base(total / groups), rest(total % groups) {}
+      : base(total / groups), rest(total - base * groups) {}
   __device__ __forceinline__ int begin(int b) const { return b * base + min(b, rest); }
   __device__ __forceinline__ int of(int pos) const {      // the share of a block
     const int longer = rest * (base + 1);
@@ -1085,16 +1090,16 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 
   while (pos < end) {
     const Place pl = place_of(kv, cut, work, pos);
-    const int h = pl.item / pl.rgs, rg = pl.item % pl.rgs;
+    const int h = pl.rgs == 1 ? pl.item : pl.item / pl.rgs, rg = pl.item - h * pl.rgs;
     const int blocks = min(pl.nb - pl.blk, end - pos);
     const Seq q = pl.q;
     const int row_count = min(q.n * kv.group - rg * ROWS, ROWS);
     // This wave's rows, and the keys seen by the first and the last of them.
     const int row0 = rg * ROWS + rw * kWaveRows;
     const int wave_rows = min(row_count - rw * kWaveRows, kWaveRows);
-    const int lim_lo = min(max(q.base + row0 / kv.group + 1, 0), q.cap);
+    const int lim_lo = min(max(q.base + by_group(kv, row0) + 1, 0), q.cap);
     const int lim_hi = wave_rows <= 0 ? 0
-        : min(max(q.base + (row0 + wave_rows - 1) / kv.group + 1, 0), q.cap);
+        : min(max(q.base + by_group(kv, row0 + wave_rows - 1) + 1, 0), q.cap);
 
     // Row rt * 16 + c of the wave's rows in this lane's column.
     u32x4 qf[RT][Sh::kSteps];
@@ -1102,7 +1107,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int r = row0 + rt * 16 + c;
-      const int tok = r / kv.group, head = r % kv.group;
+      const int tok = by_group(kv, r), head = r - tok * kv.group;
       const bool live = rt * 16 + c < wave_rows;
       lim[rt] = live ? min(max(q.base + tok + 1, 0), q.cap) : lim_hi;
       const __bf16* src = a.q + ((size_t)(q.q0 + tok) * q_heads + h * kv.group + head) * D;
@@ -1366,37 +1371,31 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
         for (int j = 0; j < Sh::kTiles; ++j)
           sums[wave][c][(4 * g + r) * Sh::kTiles + j] = o[rt][j][r];
       __syncthreads();
-      for (int i = tid; i < 16 * RW * (D / 8); i += kAll) {
-        const int d = i % (D / 8) * 8, rr = i / (D / 8) % 16, w0 = i / (D / 8) / 16;
+      for (int i = tid; i < 16 * RW * (D / 4); i += kAll) {
+        const int d = i % (D / 4) * 4, rr = i / (D / 4) % 16, w0 = i / (D / 4) / 16;
         const int row = w0 * kWaveRows + rt * 16 + rr;
         if (row < row_count) {
           float top = kNegInf;
 #pragma unroll
           for (int w = 0; w < KW; ++w) top = fmaxf(top, sm[w * RW + w0][rr]);
           float sum = 0.0f;
-          float x[8] = {};
+          f32x4 x{0, 0, 0, 0};
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
             const float mw = sm[w * RW + w0][rr], lw2 = sl[w * RW + w0][rr];
             // Without a maximum l is 0 (no key seen) or NaN (a score was).
             const float f = mw == kNegInf ? lw2 : __builtin_amdgcn_exp2f(mw - top);
             sum += f * lw2;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += f * sums[w * RW + w0][rr][d + e];
+            x += f * *reinterpret_cast<const f32x4*>(&sums[w * RW + w0][rr][d]);
           }
           if (whole) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int r = rg * ROWS + row;
-            u32x4 y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e] * inv, x[2 * e + 1] * inv);
-            *reinterpret_cast<u32x4*>(a.out +
-                ((size_t)(q.q0 + r / kv.group) * q_heads + h * kv.group + r % kv.group) * D + d) = y;
+            const int r = rg * ROWS + row, tok = by_group(kv, r), head = r - tok * kv.group;
+            *reinterpret_cast<u32x2*>(a.out +
+                ((size_t)(q.q0 + tok) * q_heads + h * kv.group + head) * D + d) =
+                u32x2{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
           } else {
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-              *reinterpret_cast<f32x4*>(part + row * D + d + e) =
-                  f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+            *reinterpret_cast<f32x4*>(part + row * D + d) = x;
             if (d == 0) {
               part[ROWS * D + row] = top;
               part[ROWS * D + ROWS + row] = sum;
@@ -1592,6 +1591,7 @@ KvArgs kv_args(const skinny_kv_cache& c, const skinny_kv_batch& b, int group) {
   a.pages = c.pages;
   a.kv_heads = c.kv_heads;
   a.group = group;
+  a.group_shift = group & (group - 1) ? -1 : log2_of(group);
   a.log2p = log2_of(c.page_tokens);
   return a;
 }
