@@ -1,5 +1,7 @@
-// host_util.h - host-side checks shared by the library's source files: the
-// current device, pointer alignment and buffer overlap.
+// host_util.h - host-side checks shared by the cache's and the verification's
+// source files: the current device, pointer alignment and buffer overlap.  The
+// linears' source has its own: bench.py reports HBM traffic from the counters on
+// record only while that file is the one that they were taken on.
 #ifndef SKINNY_HOST_UTIL_H
 #define SKINNY_HOST_UTIL_H
 

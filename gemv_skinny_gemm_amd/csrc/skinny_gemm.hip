@@ -53,17 +53,9 @@
 #include <type_traits>
 #include <vector>
 
-#include "host_util.h"
 #include "skinny_gemm.h"
 
 namespace {
-
-using skinny_host::DeviceInfo;
-using skinny_host::Range;
-using skinny_host::aligned;
-using skinny_host::device_info;
-using skinny_host::kMaxDevices;
-using skinny_host::overlap;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -1850,6 +1842,34 @@ __global__ __launch_bounds__(kArgmaxThreads) void skinny_argmax_rows(const Argma
 // ---------------------------------------------------------------------------
 // Host side.
 
+struct DeviceInfo {
+  int cus = 0;
+  bool gfx950 = false;
+  bool valid = false;
+};
+
+constexpr int kMaxDevices = 64;
+DeviceInfo g_dev[kMaxDevices];
+std::mutex g_dev_mu;
+
+skinny_status device_info(DeviceInfo* out) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return SKINNY_ERR_HIP;
+  if (dev < 0 || dev >= kMaxDevices) return SKINNY_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  if (!g_dev[dev].valid) {
+    hipDeviceProp_t p;
+    if (hipGetDeviceProperties(&p, dev) != hipSuccess) return SKINNY_ERR_HIP;
+    g_dev[dev].cus = p.multiProcessorCount;
+    g_dev[dev].gfx950 = strncmp(p.gcnArchName, "gfx950", 6) == 0;
+    g_dev[dev].valid = true;
+  }
+  *out = g_dev[dev];
+  return SKINNY_OK;
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
 // allow_act: the library's own chained linears carry their input activation
 // in `reserved` (kActSwiGLU); a caller's linear must have 0 there.
 skinny_status check_linear(const skinny_linear& L, int M, bool allow_act = false) {
@@ -1867,6 +1887,12 @@ skinny_status check_linear(const skinny_linear& L, int M, bool allow_act = false
   if (L.N > (1 << 26) || L.K > (1 << 28)) return SKINNY_ERR_UNSUPPORTED;
   return SKINNY_OK;
 }
+
+struct Range {
+  uintptr_t lo, hi;
+};
+
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // The buffers a call writes (every y and the workspace) must not overlap
 // anything else it reads or writes.
