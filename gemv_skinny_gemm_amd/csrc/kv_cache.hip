@@ -145,7 +145,10 @@ struct AppendArgs {
 
 // A step of few rows takes skinny_kv_append_few, whose threads hold four values
 // each; more rows take skinny_kv_append_many, whose threads hold 16 and share the
-// angles.
+// angles.  Few rows cost a launch and one chain of reads (4 us in a graph); many
+// are bound by bytes and the rotation in fp64 side by side: 4099 rows of 64
+// + 2 x 8 heads of 128 into e4m3 pages take 44 us (160 MB: 3.6 TB/s, where
+// a copy would take 33), 101 on the kernel of few rows.
 constexpr int kQHeadsPerBlock = 16;  // few rows: query heads of one row's workgroup
 constexpr int kUnit = 16;            // values of a unit: two runs of 8, at pa and pb
 
@@ -757,6 +760,19 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 // to arrive, was measured at 1.5 to 3 times the whole call: the fences between
 // workgroups of different XCDs write back and invalidate the L2 caches that the
 // other waves stream through.)
+//
+// What bounds it, measured: long contexts the reads (bf16, 16 sequences, 64
+// query and 8 KV heads of 128: 538 MB of pages in 99.5 us = 5.4 TB/s, six
+// times the pages 6.3; e4m3, one sequence of 131072 keys: 51.7 us = 5.2 TB/s,
+// where 4 us are the second launch and about 5 the start and the waves' join);
+// a short call the chain start - page numbers - keys - join - second launch
+// (4000 keys under one KV head: 9.8 us, of which 3.3 the second launch).  Rows of
+// several tokens share the keys' bytes but not the work on them: two sequences
+// of 12 verified tokens between them read 77 MB in 35 us.  Tried there and no
+// faster: three row tiles per wave with q in LDS (36.6 us), four row waves
+// (45.9), a second tile of keys and values in flight in registers (82; it
+// spills).  One workgroup per CU, not two: 35.6 against 45.0 us there, 51.7
+// against 59.6 on the long sequence.
 
 constexpr int kMaxGroups = 512;          // workgroups of the grid at most
 constexpr size_t kSplitBytes = kMaxGroups * 32;
@@ -764,7 +780,8 @@ constexpr float kNegInf = -__builtin_inff();
 // m need not be the maximum itself, only near it: sums are scaled again when a
 // score passes it by more than this (probabilities then reach 2^8, far from
 // fp32's and bf16's ends).  A wave's first tiles would otherwise do so nearly
-// every time, one of its 16 rows finding a new maximum.
+// every time, one of its 16 rows finding a new maximum (1 to 2% of a verify step's
+// time, nothing elsewhere).
 constexpr float kSlack = 8.0f;
 
 // What a share leaves for the second launch: the item that begins in it and
@@ -1069,6 +1086,9 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
   // Keys that one wave reads come in whole 128-byte lines: lane (c, g) loads
   // 16-byte part g + 4 (c % 2) of a line of key c & ~1, then of c | 1.  Products
   // with both halves of q leave each score in two neighbouring rows, in one lane.
+  // Whole lines and the nontemporal hint: 51.7 us against 53.0 with the hint on
+  // half lines and 56.2 without it (131072 keys, e4m3), 99.6, 102.5 and 106.1 us
+  // (16 sequences, bf16).
   constexpr bool kOnce = RW == 1 && Sh::kRowBytes >= 128;
   constexpr bool kLines = kOnce;
   __shared__ __attribute__((aligned(16))) float sums[NW][16][kStride];

@@ -29,6 +29,13 @@
 // launch set to a mark: a word read before it arrived is read again.  Fences in
 // their place cost about 8 us a call here (they write back and invalidate an
 // XCD's whole L2).
+//
+// What bounds it, measured: one exponential per logit in fp64 (11 FMA and the
+// conversion, some 20 fp64 instructions) and two passes; 37 rows of 152064 bf16
+// logits with as many of the draft's in 29 us, where reading them would take 3.
+// A few rows are the two launches' latency: 12.9 us for 2 rows of 32003, 14.8
+// for 6 of 152064.  Slices of 4096 entries: 2048 take 11.3, 16.8 and 33.1 us on
+// the three, 8192 take 16.3, 17.2 and 31.5.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
