@@ -52,6 +52,7 @@ using skinny_host::device_info;
 using skinny_host::overlap;
 using skinny_host::range_of;
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -72,7 +73,7 @@ constexpr int kMaxPolls = 1 << 16;
 struct Stat {
   double sum;            // sum over the slice of exp((l - max) / t)
   float max;             // -inf: no entry above -inf
-  int first;             // lowest index of max
+  int first;             // lowest index of max (a greedy sequence's rows)
 };
 
 struct VerifyArgs {
@@ -110,7 +111,8 @@ __device__ __forceinline__ float temperature_of(const VerifyArgs& a, int s) {
 // 2^y for -1000 <= y <= 0 in fp64: y = n + f, |f| <= 1/2, n from the low bits of
 // y + 1.5 * 2^52, and the Taylor series of exp(f ln 2) to the 11th power (the
 // next term is below 2^-47 of it); n is added to the exponent's bits.  Below
-// that, and for NaN, 0.
+// that, and for NaN, 0, or without EXACT 2^-1000, which adds nothing to a sum
+// that has a 1 in it.
 struct Taylor {
   double c[12];
   constexpr Taylor() : c{} {
@@ -120,17 +122,22 @@ struct Taylor {
 };
 // N at a time, step by step: a chain of dependent fp64 instructions alone leaves
 // the ALUs waiting.
-template <int N>
+template <bool EXACT, int N>
 __device__ __forceinline__ void exp2_below(double (&y)[N]) {
   constexpr Taylor t;
+  double last = t.c[11];
+  asm("" : "+v"(last));                            // a register, not two moves at each use
   constexpr double kShift = 6755399441055744.0;    // 1.5 * 2^52
   double s[N], f[N], p[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = y[i] + kShift;
+  for (int i = 0; i < N; ++i) {
+    if constexpr (!EXACT) y[i] = __builtin_fmax(y[i], -1000.0);
+    s[i] = y[i] + kShift;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     f[i] = y[i] - (s[i] - kShift);
-    p[i] = t.c[11];
+    p[i] = last;
   }
 #pragma unroll
   for (int k = 10; k >= 0; --k)
@@ -138,27 +145,27 @@ __device__ __forceinline__ void exp2_below(double (&y)[N]) {
     for (int i = 0; i < N; ++i) p[i] = fma(p[i], f[i], t.c[k]);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const unsigned n = (unsigned)__builtin_bit_cast(unsigned long long, s[i]);
-    const unsigned long long b = __builtin_bit_cast(unsigned long long, p[i]);
-    const unsigned hi = (unsigned)(b >> 32) + (n << 20);
-    const double r = __builtin_bit_cast(double, (unsigned long long)hi << 32 | (unsigned)b);
-    y[i] = y[i] >= -1000.0 ? r : 0.0;
+    const u32x2 n = __builtin_bit_cast(u32x2, s[i]);
+    u32x2 r = __builtin_bit_cast(u32x2, p[i]);
+    r[1] += n[0] << 20;
+    const double x = __builtin_bit_cast(double, r);
+    y[i] = !EXACT || y[i] >= -1000.0 ? x : 0.0;
   }
 }
 
 // exp((l - top) / t) with c = log2 e / t, top below +inf: 1 at the maximum, 0
 // for NaN and -inf (and for top -inf).
-template <int N>
+template <bool EXACT, int N>
 __device__ __forceinline__ void finite_weights(const float* l, double top, double c,
                                                double (&w)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) w[i] = ((double)l[i] - top) * c;
-  exp2_below(w);
+  exp2_below<EXACT>(w);
 }
 // The same for any top; where it is +inf, 1 at the infinite entries and 0 elsewhere.
 template <int N>
 __device__ __forceinline__ void weights_of(const float* l, float top, double c, double (&w)[N]) {
-  finite_weights(l, (double)top, c, w);
+  finite_weights<true>(l, (double)top, c, w);
   if (top == -kNegInf) {
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = l[i] == top ? 1.0 : 0.0;
@@ -360,18 +367,19 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
   const float wtop = reduce64(top, larger);
   int first = a.V;
-#pragma unroll
-  for (int j = kPer - 1; j >= 0; --j) first = l[j] == wtop ? n0 + index_of<L, VEC>(j) : first;
-  first = reduce64(first, lower);
   double sum = 0.0;
   const double c = 1.4426950408889634074 / (double)t;
-  if (!greedy) {
+  if (greedy) {
+#pragma unroll
+    for (int j = kPer - 1; j >= 0; --j) first = l[j] == wtop ? n0 + index_of<L, VEC>(j) : first;
+    first = reduce64(first, lower);
+  } else {
     if (wtop < -kNegInf) {
       const double dtop = wtop;
 #pragma unroll
       for (int j = 0; j < kPer; j += kBatch) {
         double w[kBatch];
-        finite_weights(l + j, dtop, c, w);
+        finite_weights<false>(l + j, dtop, c, w);
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) sum += w[e];
       }
