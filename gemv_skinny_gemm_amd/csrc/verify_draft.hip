@@ -30,12 +30,13 @@
 // their place cost about 8 us a call here (they write back and invalidate an
 // XCD's whole L2).
 //
-// What bounds it, measured: one exponential per logit in fp64 (11 FMA and the
-// conversion, some 20 fp64 instructions) and two passes; 37 rows of 152064 bf16
-// logits with as many of the draft's in 29 us, where reading them would take 3.
-// A few rows are the two launches' latency: 12.9 us for 2 rows of 32003, 14.8
-// for 6 of 152064.  Slices of 4096 entries: 2048 take 11.3, 16.8 and 33.1 us on
-// the three, 8192 take 16.3, 17.2 and 31.5.
+// What bounds it, measured: one exponential per logit in fp64 (11 FMA and some
+// ten instructions around them) in the first launch, instruction issue there, and
+// the latency of the second one's chain: 37 rows of 152064 bf16 logits with as
+// many of the draft's take 26.5 us (15.4 + 11.2), where reading them would take 3.
+// A few rows are the two launches' latency: 12.5 us for 2 rows of 32003, 14.1 for
+// 6 of 152064.  Slices of 2048 entries take 11.1, 16.0 and 31.1 us on the three,
+// of 8192 15.2, 16.1 and 28.3.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -527,7 +528,8 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
       }
       row_end(c, p);
       mine.row = i;
-      mine.greedy_token = p.top > kNegInf ? p.first : 0;
+      // (Rows that two sequences claim may have been the other's, who sampled.)
+      mine.greedy_token = p.top > kNegInf && p.first < a.V ? p.first : 0;
       mine.p_top = p.top;
       mine.p_inv = p.sum > 0.0 ? 1.0 / p.sum : 0.0;
       mine.drafted = -1;

@@ -251,6 +251,19 @@ def test_bad_row_ranges():
     assert d["out"].tolist()[:2] == [-9, -9] and d["accepted"].tolist()[1] == 0
 
 
+@pytest.mark.parametrize("temps", [[1.0, 1.0, 0.0], [0.0, 1.0, 1.0]])
+def test_rows_of_two_sequences_give_tokens_of_the_vocabulary(temps):
+    """Rows 2 and 3 belong to a sampling and to a greedy sequence; which of
+    them writes last is open, but not what a token can be."""
+    c = case([4, 0, 2], 5000, seed=21, temps=temps)
+    d = upload(c)
+    d["q_start"].copy_(torch.tensor([0, 4, 2, 6], dtype=torch.int32))
+    run(d)
+    torch.cuda.synchronize()
+    assert all(-1 <= t < 5000 for t in d["out"].tolist())
+    assert all(0 <= n <= 3 for n in d["accepted"].tolist())
+
+
 def test_workspace_is_enough_and_results_repeat():
     c = case([6, 4, 1], 32003, seed=16, temps=[0.9])
     d = upload(c)
