@@ -90,6 +90,7 @@ class KvCache(ctypes.Structure):
                 ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("reserved", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+    gpu = None                 # of the tensors that make_kv_cache was given
 
 
 class KvBatch(ctypes.Structure):
@@ -97,6 +98,7 @@ class KvBatch(ctypes.Structure):
     _fields_ = [("seqs", ctypes.c_int), ("tokens", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("reserved", ctypes.c_int), ("q_start", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+    gpu = None                 # of the tensors that make_batch was given
 
 
 class Verify(ctypes.Structure):
@@ -658,10 +660,31 @@ def _call_device(t):
     return _torch, dev
 
 
-def _call_stream(tt, dev, stream):
+def _call_stream(tt, dev, stream, cache=None, batch=None):
     if dev < 0:
         raise ValueError("tensors passed to the library must be on the GPU, not cpu")
+    if cache is not None and (cache.gpu not in (None, dev) or batch.gpu not in (None, dev)):
+        raise ValueError(f"cache on GPU {cache.gpu} and batch on GPU {batch.gpu}, the call's "
+                         f"tensors on GPU {dev}")
     return tt.raw_stream(dev) if stream is None else _stream(stream)
+
+
+def _space(workspace, dev):
+    """A call's workspace as the library takes it, on the call's GPU."""
+    wp, wb = _ws(workspace)
+    if workspace is not None and not isinstance(workspace, tuple) and workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the call's other tensors on GPU {dev}")
+    return wp, wb
+
+
+def _one_gpu(struct, *tensors):
+    """`struct` with the tensors' GPU and the tensors, whose memory it points to."""
+    struct.gpu = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != struct.gpu:
+            raise ValueError(f"tensors on {tensors[0].device} and on {t.device}")
+    struct.tensors = tensors
+    return struct
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
@@ -679,8 +702,9 @@ def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
     if fp8:
         _need(k_scale, shape[:2], _F32, "k_scale")
         _need(v_scale, shape[:2], _F32, "v_scale")
-    return KvCache(KV_FP8 if fp8 else KV_BF16, *shape, 0, _ptr(k), _ptr(v), _ptr(k_scale),
-                   _ptr(v_scale))
+    return _one_gpu(KvCache(KV_FP8 if fp8 else KV_BF16, *shape, 0, _ptr(k), _ptr(v),
+                            _ptr(k_scale), _ptr(v_scale)),
+                    *((k, v, k_scale, v_scale) if fp8 else (k, v)))
 
 
 def make_batch(q_start, kv_len, page_table, tokens: int) -> KvBatch:
@@ -693,7 +717,8 @@ def make_batch(q_start, kv_len, page_table, tokens: int) -> KvBatch:
     _need(q_start, (seqs + 1,), _I32, "q_start")
     _need(kv_len, (seqs,), _I32, "kv_len")
     _need(page_table, (seqs, width), _I32, "page_table")
-    return KvBatch(seqs, int(tokens), width, 0, _ptr(q_start), _ptr(kv_len), _ptr(page_table))
+    return _one_gpu(KvBatch(seqs, int(tokens), width, 0, _ptr(q_start), _ptr(kv_len),
+                            _ptr(page_table)), q_start, kv_len, page_table)
 
 
 def _heads(cache: KvCache, batch: KvBatch, t, what: str, extra: int = 0) -> int:
@@ -720,7 +745,7 @@ def kv_append(cache: KvCache, batch: KvBatch, qkv, inv_freq, q_out, interleaved:
         rot = 2 * inv_freq.shape[0]
         f = _operand(inv_freq, (rot // 2,), tt.f32, "inv_freq", dev)
     _check(lib().skinny_kv_append(cache, batch, x, heads, f, rot, int(interleaved), y,
-                                  _call_stream(tt, dev, stream)), "skinny_kv_append")
+                                  _call_stream(tt, dev, stream, cache, batch)), "skinny_kv_append")
     return q_out
 
 
@@ -737,10 +762,11 @@ def kv_attention(cache: KvCache, batch: KvBatch, q, out, workspace, scale: float
     heads = _heads(cache, batch, q, "q")
     x = _operand(q, q.shape, tt.bf16, "q", dev)
     y = _operand(out, q.shape, tt.bf16, "out", dev)
-    wp, wb = _ws(workspace)
+    wp, wb = _space(workspace, dev)
     _check(lib().skinny_kv_attention(cache, batch, x, heads,
                                      cache.head_dim ** -0.5 if scale is None else scale, y, wp, wb,
-                                     _call_stream(tt, dev, stream)), "skinny_kv_attention")
+                                     _call_stream(tt, dev, stream, cache, batch)),
+           "skinny_kv_attention")
     return out
 
 
@@ -775,7 +801,7 @@ def verify_draft(q_start, logits, tokens, accept_u, sample_u, out_tokens, accept
         _operand(sample_u, per_seq, f32, "sample_u", dev),
         _operand(out_tokens, per_row, i32, "out_tokens", dev),
         _operand(accepted, per_seq, i32, "accepted", dev))
-    wp, wb = _ws(workspace)
+    wp, wb = _space(workspace, dev)
     _check(lib().skinny_verify_draft(v, wp, wb, _call_stream(tt, dev, stream)),
            "skinny_verify_draft")
     return out_tokens

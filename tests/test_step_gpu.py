@@ -176,3 +176,32 @@ def test_prompt_then_verify_steps(dtype, graph):
         rows = nxt
         s.tokens.copy_(torch.from_numpy(tokens))
     assert min(sure) > P and kept > 0                 # pages were crossed, drafts kept
+
+
+def test_structs_know_their_tensors_and_gpu():
+    """A cache or batch holds the tensors that it points to, and a call whose
+    tensors lie on another GPU than either is refused."""
+    def ints(*x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    k = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+    cache = sg.make_kv_cache(k, k.clone())
+    batch = sg.make_batch(ints(0, 1), ints(1), ints(0)[None], 1)
+    assert cache.v == cache.tensors[1].data_ptr()
+    assert batch.page_table == batch.tensors[2].data_ptr()
+    qkv = torch.zeros((1, 3 * 64), dtype=torch.bfloat16, device="cuda")
+    q = qkv[:, :64].clone()
+    ws = torch.empty(sg.kv_attention_workspace_bytes(cache, batch, 1), dtype=torch.uint8,
+                     device="cuda")
+    for struct in (cache, batch):
+        struct.gpu += 1
+        with pytest.raises(ValueError, match="the call's tensors on GPU 0"):
+            sg.kv_append(cache, batch, qkv, None, q)
+        with pytest.raises(ValueError, match="the call's tensors on GPU 0"):
+            sg.kv_attention(cache, batch, q, q.clone(), ws)
+        struct.gpu -= 1
+    with pytest.raises(ValueError, match="on the GPU"):
+        sg.kv_attention(cache, batch, q, q.clone(), ws.cpu())
+    sg.kv_append(cache, batch, qkv, None, q)
+    sg.kv_attention(cache, batch, q, q.clone(), ws)
+    torch.cuda.synchronize()
