@@ -17,13 +17,13 @@
 //
 // Two launches:
 //   skinny_verify_stats   workgroup (slice, row, target or draft): the largest
-//     logit of kSlice, the first place of it, and the sum of exp((l - max) / t);
+//     logit of a slice, the first place of it, and the sum of exp((l - max) / t);
 //   skinny_verify_pick    workgroup (slice, sequence): from the rows' slices,
 //     the normalisers and with them the first row that stops (each workgroup
 //     the same, in the same order), then its waves' sums of the weights to
-//     sample from, max(0, p - q), over kSub entries each.  The sequence's last
+//     sample from, max(0, p - q), over a quarter slice each.  The sequence's last
 //     workgroup to arrive (a counter that the first launch cleared) finds the
-//     entries of kSub, then the entry, where the running sum passes u times the
+//     quarter, then the entry, where the running sum passes u times the
 //     total; sums are added in index order, so it does not matter who came last.
 // The sums pass between workgroups as relaxed device-scope words that the first
 // launch set to a mark: a word read before it arrived is read again.  Fences in
@@ -34,12 +34,17 @@
 // ten instructions around them) in the first launch, instruction issue there, and
 // the latency of the second one's chain: 37 rows of 152064 bf16 logits with as
 // many of the draft's take 26.5 us (15.4 + 11.2), where reading them would take 3.
-// A few rows are the two launches' latency: 12.5 us for 2 rows of 32003, 14.1 for
-// 6 of 152064.  Slices of 2048 entries take 11.1, 16.0 and 31.1 us on the three,
-// of 8192 15.2, 16.1 and 28.3.
+// A few rows are the two launches' latency: 11.1 us for 2 rows of 32003, 14.1 for
+// 6 of 152064.  Slices are 4096 entries, or 2048 where that makes at most 64 of a
+// row (what one trip of the second launch reads) and 1024 of all rows: 32003
+// entries 11.8 against 13.2 us at 4 rows, 13.5 against 14.2 at 32; beyond the
+// one bound (152064) 15.3 against 13.9 at 4 rows, beyond the other (64 rows of
+// 64000) 23.5 against 21.1.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "host_util.h"
 #include "skinny_gemm.h"
@@ -60,12 +65,14 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kSlice = 4096;                       // logits per workgroup
-constexpr int kSub = kSlice / kWaves;              // per wave
-constexpr int kPer = kSub / 64;                    // per lane
+// Logits of a slice, one workgroup's: PER per lane.
+template <int PER>
+constexpr int kSlice = kThreads * PER;
+template <int PER>
+constexpr int kSub = 64 * PER;                     // per wave
+constexpr int kPerLong = 16, kPerShort = 8;
 constexpr int kRowLanes = 16;                      // lanes that read one row's slices
 constexpr int kRowsAtOnce = kThreads / kRowLanes;
-constexpr int kFind = kSub / kThreads;             // entries of a thread in the last search
 constexpr int kBatch = 4;                          // exponentials at a time
 constexpr float kNegInf = -__builtin_inff();
 constexpr unsigned long long kNotYet = ~0ull;      // a NaN that no sum is
@@ -284,19 +291,19 @@ __device__ __forceinline__ void load_vec(const void* p, size_t at, float* out) {
   }
 }
 
-// A lane's kPer of the kSub logits from n0 on, as runs of kVec neighbours (VEC)
+// A lane's PER of the wave's logits from n0 on, as runs of kVec neighbours (VEC)
 // or single ones, NaN past the end; place of the j-th.
 template <typename L, bool VEC>
 __device__ __forceinline__ int index_of(int j) {
   constexpr int W = VEC ? kVec<L> : 1;
   return (j / W * 64 + (int)(threadIdx.x & 63)) * W + j % W;
 }
-template <typename L, bool VEC>
-__device__ __forceinline__ void load_sub(const void* row, int n0, int V, float (&l)[kPer]) {
+template <typename L, bool VEC, int PER>
+__device__ __forceinline__ void load_sub(const void* row, int n0, int V, float (&l)[PER]) {
   if constexpr (VEC) {
     constexpr int W = kVec<L>;
 #pragma unroll
-    for (int j = 0; j < kPer; j += W) {
+    for (int j = 0; j < PER; j += W) {
       const int n = n0 + index_of<L, true>(j);
       load_vec<L>(row, min(n, V - W), l + j);
       if (n >= V) {
@@ -306,7 +313,7 @@ __device__ __forceinline__ void load_sub(const void* row, int n0, int V, float (
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
       const int n = n0 + index_of<L, false>(j);
       const float x = logit<L>(row, min(n, V - 1));
       l[j] = n < V ? x : __builtin_nanf("");
@@ -333,7 +340,7 @@ __device__ __forceinline__ int find_row(const VerifyArgs& a, int t) {
   return -1;
 }
 
-template <typename L, bool VEC>
+template <typename L, bool VEC, int PER>
 __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs a) {
   __shared__ float sv[kWaves];
   __shared__ int si[kWaves];
@@ -341,9 +348,9 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int slice = blockIdx.x, row = blockIdx.y, which = blockIdx.z;
   const void* src = static_cast<const L*>(which ? a.draft : a.logits) + (size_t)row * a.V;
-  const int n0 = slice * kSlice + wave * kSub;
-  float l[kPer];
-  load_sub<L, VEC>(src, n0, a.V, l);               // on its way while the row's sequence is found
+  const int n0 = slice * kSlice<PER> + wave * kSub<PER>;
+  float l[PER];
+  load_sub<L, VEC, PER>(src, n0, a.V, l);               // on its way while the row's sequence is found
   if (slice == 0 && tid == 0) {
     const int d = row + 1 < a.T ? a.tokens[row + 1] : -1;
     a.drafted[(size_t)which * a.T + row] =
@@ -365,20 +372,20 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   // Each wave's maximum and sum, then the four joined.
   float top = kNegInf;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
+  for (int j = 0; j < PER; ++j) top = fmaxf(top, l[j]);
   const float wtop = reduce64(top, larger);
   int first = a.V;
   double sum = 0.0;
   const double c = 1.4426950408889634074 / (double)t;
   if (greedy) {
 #pragma unroll
-    for (int j = kPer - 1; j >= 0; --j) first = l[j] == wtop ? n0 + index_of<L, VEC>(j) : first;
+    for (int j = PER - 1; j >= 0; --j) first = l[j] == wtop ? n0 + index_of<L, VEC>(j) : first;
     first = reduce64(first, lower);
   } else {
     if (wtop < -kNegInf) {
       const double dtop = wtop;
 #pragma unroll
-      for (int j = 0; j < kPer; j += kBatch) {
+      for (int j = 0; j < PER; j += kBatch) {
         double w[kBatch];
         finite_weights<false>(l + j, dtop, c, w);
 #pragma unroll
@@ -386,7 +393,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) sum += l[j] == wtop ? 1.0 : 0.0;
+      for (int j = 0; j < PER; ++j) sum += l[j] == wtop ? 1.0 : 0.0;
     }
     sum = reduce64(sum, plus);
   }
@@ -480,8 +487,9 @@ __device__ __forceinline__ void residuals(const Stop& st, double c, const float*
   }
 }
 
-template <typename L, bool VEC>
+template <typename L, bool VEC, int PER>
 __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs a) {
+  constexpr int kFind = kSub<PER> / kThreads;        // entries of a thread in the last search
   __shared__ Stop stops[kWaves];
   __shared__ int is_last, found, positive;
   __shared__ double wsum[kWaves];
@@ -574,13 +582,13 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
     const int subs = a.slices * kWaves;
     unsigned long long* words = a.weight + (size_t)s * subs;
     {
-      float lp[kPer], lq[kPer];
-      const int n0 = (slice * kWaves + wave) * kSub;
-      load_sub<L, VEC>(lp_row, n0, a.V, lp);
-      load_sub<L, VEC>(lq_row, n0, a.V, lq);         // without q, lp again
+      float lp[PER], lq[PER];
+      const int n0 = (slice * kWaves + wave) * kSub<PER>;
+      load_sub<L, VEC, PER>(lp_row, n0, a.V, lp);
+      load_sub<L, VEC, PER>(lq_row, n0, a.V, lq);         // without q, lp again
       double w = 0.0;
 #pragma unroll
-      for (int j = 0; j < kPer; j += kBatch) {
+      for (int j = 0; j < PER; j += kBatch) {
         int n[kBatch];
         double x[kBatch];
 #pragma unroll
@@ -601,7 +609,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
     __syncthreads();
     if (!is_last) return;
 
-    // The kSub entries where the running sum passes u times the total; without
+    // The wave's share where the running sum passes u times the total; without
     // any weight (p nowhere above q), the same over p itself, slice by slice.
     if (wave == 0) {
       const Stat* ps = a.stats + (size_t)row * a.slices;
@@ -692,7 +700,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
     const bool plain = plain_s;
     double before = before_s;
     for (int k = 0; k < (plain ? kWaves : 1); ++k) {
-      const int m0 = (sub_s + k) * kSub + tid * kFind;
+      const int m0 = (sub_s + k) * kSub<PER> + tid * kFind;
       double x[kFind], sum = 0.0;
       float lp[kFind], lq[kFind];
       int n[kFind], some = -1;
@@ -744,7 +752,17 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
 // ---------------------------------------------------------------------------
 // Host side.
 
-int slices_of(int vocab) { return (vocab + kSlice - 1) / kSlice; }
+constexpr int kShortSlices = 64, kShortGroups = 1024;   // of a row, of all rows
+
+int slices_of(int vocab, int per) {
+  const int slice = kThreads * per;
+  return (vocab + slice - 1) / slice;
+}
+// Logits per lane of a step, by the rule above.
+int per_of(int rows, int vocab) {
+  const int slices = slices_of(vocab, kPerShort);
+  return slices <= kShortSlices && rows <= kShortGroups / slices ? kPerShort : kPerLong;
+}
 
 size_t up(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -752,12 +770,16 @@ struct Layout {
   size_t stats, weight, drafted, arrived, total;
 };
 
+// Room for either length of slices, so that more rows, sequences or entries
+// never need less than fewer.
 Layout layout(int rows, int seqs, int vocab) {
-  const size_t sl = slices_of(vocab);
+  const size_t sl = slices_of(vocab, kPerLong);
+  const size_t few = std::min(slices_of(vocab, kPerShort), kShortSlices);
+  const size_t stats = std::max(rows * sl, std::min(rows * few, (size_t)kShortGroups));
   Layout w;
   w.stats = 0;
-  w.weight = up((size_t)2 * rows * sl * sizeof(Stat));
-  w.drafted = w.weight + up((size_t)seqs * sl * kWaves * sizeof(double));
+  w.weight = up(2 * stats * sizeof(Stat));
+  w.drafted = w.weight + up((size_t)seqs * std::max(sl, few) * kWaves * sizeof(double));
   w.arrived = w.drafted + up((size_t)2 * rows * sizeof(float));
   w.total = w.arrived + up((size_t)seqs * sizeof(int));
   return w;
@@ -771,21 +793,22 @@ skinny_status check_sizes(int rows, int seqs, int vocab) {
   return SKINNY_OK;
 }
 
-template <typename L, bool VEC>
+template <typename L, bool VEC, int PER>
 skinny_status launch(const VerifyArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((skinny_verify_stats<L, VEC>), dim3(a.slices, a.T, a.draft ? 2 : 1),
+  hipLaunchKernelGGL((skinny_verify_stats<L, VEC, PER>), dim3(a.slices, a.T, a.draft ? 2 : 1),
                      dim3(kThreads), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
-  hipLaunchKernelGGL((skinny_verify_pick<L, VEC>), dim3(a.slices, a.S), dim3(kThreads), 0, stream,
-                     a);
+  hipLaunchKernelGGL((skinny_verify_pick<L, VEC, PER>), dim3(a.slices, a.S), dim3(kThreads), 0,
+                     stream, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 
 template <typename L>
 skinny_status launch_as(const VerifyArgs& a, hipStream_t stream) {
-  if (a.V % kVec<L> == 0 && aligned(a.logits, 16) && (!a.draft || aligned(a.draft, 16)))
-    return launch<L, true>(a, stream);
-  return launch<L, false>(a, stream);
+  const bool vec = a.V % kVec<L> == 0 && aligned(a.logits, 16) && (!a.draft || aligned(a.draft, 16));
+  if (per_of(a.T, a.V) == kPerShort)
+    return vec ? launch<L, true, kPerShort>(a, stream) : launch<L, false, kPerShort>(a, stream);
+  return vec ? launch<L, true, kPerLong>(a, stream) : launch<L, false, kPerLong>(a, stream);
 }
 
 }  // namespace
@@ -856,7 +879,7 @@ skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
   a.T = v.rows;
   a.S = v.seqs;
   a.V = v.vocab;
-  a.slices = slices_of(v.vocab);
+  a.slices = slices_of(v.vocab, per_of(v.rows, v.vocab));
   return v.dtype == SKINNY_LOGITS_BF16 ? launch_as<__bf16>(a, (hipStream_t)stream)
                                        : launch_as<float>(a, (hipStream_t)stream);
 }

@@ -61,3 +61,23 @@ def test_binding_checks_tensors():
             (dict(accepted=torch.zeros(2)), "accepted: dtype"), (dict(), "on the GPU")):
         with pytest.raises(ValueError, match=what):
             sg.verify_draft(**{**good, **kw})
+
+
+def test_workspace_of_a_larger_step_holds_a_smaller_one():
+    """Sized once for the most rows, sequences and entries, it does for less."""
+    sizes = [1, 2, 3, 16, 51, 52, 102, 103, 170, 171, 512, 1024, 1025, 4000]
+    vocabs = [1, 2048, 2049, 4096, 4097, 12288, 12289, 20480, 32003, 131072, 131073, 152064]
+    for most in (sizes, vocabs):
+        got = [sg.verify_workspace_bytes(*((n, 5, 20480) if most is sizes else (7, 5, n)))
+               for n in most]
+        assert got == sorted(got) and got[0] > 0
+    got = [sg.verify_workspace_bytes(40, n, 32003) for n in sizes]
+    assert got == sorted(got)
+    # Either length of slices fits: statistics (16 bytes) of each row's slices,
+    # the target's and the draft's, and four sums of each sequence's.
+    for rows in sizes:
+        for vocab in vocabs:
+            short = -(-vocab // 2048)
+            slices = short if short <= 64 and rows * short <= 1024 else -(-vocab // 4096)
+            need = 2 * rows * slices * 16 + 5 * slices * 32 + 8 * rows + 20
+            assert sg.verify_workspace_bytes(rows, 5, vocab) >= need

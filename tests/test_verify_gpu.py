@@ -138,6 +138,14 @@ def test_vocabularies(dtype, draft, V):
         check(case([6, 1, 3], V, dtype, draft, seed=seed, temps=[0.8, 1.0, 0.0]), what=str(seed))
 
 
+@pytest.mark.parametrize("V,rows", [(2047, 3), (2048, 3), (2049, 3), (131072, 16), (131073, 3),
+                                    (131080, 3), (20480, 102), (20480, 103)])
+def test_slices(V, rows):
+    """Vocabularies around a slice's end, and both sides of each bound of the
+    short slices' rule: 64 of a row, 1024 of all rows."""
+    check(case([rows - 2, 2], V, seed=V + rows), what=f"{V} {rows}")
+
+
 @pytest.mark.parametrize("dtype,offset", [("bf16", 1), ("bf16", 4), ("f32", 1)])
 def test_unaligned(dtype, offset):
     check(case([4, 2], 5000, dtype, seed=3, temps=[0.7]), offset=offset)
