@@ -435,8 +435,7 @@ skinny_status skinny_moe_mlp_plan_query(const skinny_experts* gate_up, const ski
 
 /* ------------------------------------------------------------------------
  * The step's operators between the QKV linear and the O linear: the paged
- * key/value cache and the attention over it (grouped query heads, flash
- * decoding: "Developing a custom Qwen2.5 72B inference engine from scratch -
+ * key/value cache and the attention over it (grouped query heads: "Developing a custom Qwen2.5 72B inference engine from scratch -
  * what is the real bottleneck?", section 6.3).
  *
  * A pool of `pages` pages of `page_tokens` tokens holds the keys and values of
@@ -512,8 +511,8 @@ typedef struct skinny_kv_batch {
  * their positions (and, as above, earlier codes in the same page), nothing
  * else: positions below 0 or past the page table have no slot.  A page that
  * receives rows must belong to one sequence only (shared full pages are fine:
- * they receive none); if two sequences write one page, its contents are
- * undefined.  A second call with the same inputs changes nothing.
+ * they receive none); if two sequences, or two places of one, write one
+ * page, its contents are undefined.  A second call with the same inputs changes nothing.
  * q_heads is a multiple of kv_heads.  No buffer that is written may overlap
  * another operand.  No workspace; one launch. */
 skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_batch* batch,
