@@ -435,8 +435,9 @@ skinny_status skinny_moe_mlp_plan_query(const skinny_experts* gate_up, const ski
 
 /* ------------------------------------------------------------------------
  * The step's operators between the QKV linear and the O linear: the paged
- * key/value cache and the attention over it (grouped query heads: "Developing a custom Qwen2.5 72B inference engine from scratch -
- * what is the real bottleneck?", section 6.3).
+ * key/value cache and the attention over it (grouped query heads: "Developing
+ * a custom Qwen2.5 72B inference engine from scratch - what is the real
+ * bottleneck?", section 6.3).
  *
  * A pool of `pages` pages of `page_tokens` tokens holds the keys and values of
  * all sequences, one layer's at a time; all pointers are device pointers:
@@ -533,7 +534,9 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
  * Results are reproducible bitwise for the same lengths, shapes and device.
  *   workspace  >= skinny_kv_attention_workspace_bytes(cache, batch, q_heads)
  *              bytes (0 for invalid arguments; pure host arithmetic on the
- *              shapes), 16-byte aligned; contents undefined afterwards
+ *              shapes, for which a step of fewer sequences can need more: its
+ *              sequences have more rows), 16-byte aligned; contents undefined
+ *              before and after, so calls that may overlap need their own
  * out must not overlap q, the cache, the batch's arrays or the workspace, nor
  * the workspace any of them. */
 size_t skinny_kv_attention_workspace_bytes(const skinny_kv_cache* cache,
@@ -574,7 +577,9 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
  *   logits, draft_logits [rows][vocab] bf16 or fp32, aligned to their type (read
  *     16 bytes at a time when 16-byte aligned and rows are multiples of 16 bytes)
  *   workspace >= skinny_verify_workspace_bytes(rows, seqs, vocab) bytes (0 for
- *     invalid arguments), 16-byte aligned, contents undefined before and after
+ *     invalid arguments; more rows, sequences or entries never need less),
+ *     16-byte aligned, contents undefined before and after, so calls that may
+ *     overlap need their own
  * out_tokens, accepted and the workspace must not overlap anything else. */
 enum skinny_logits_dtype { SKINNY_LOGITS_BF16 = 0, SKINNY_LOGITS_F32 = 1 };
 #define SKINNY_VERIFY_MAX_ROWS 65535
