@@ -627,7 +627,7 @@ class _Torch:
     def __init__(self):
         import torch
         self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
-        self.device = torch.cuda.current_device
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         # The stream's handle without a Stream object around it (a microsecond
         # of the host's time per call), where this torch has that.
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -671,10 +671,12 @@ def _call_stream(tt, dev, stream, cache=None, batch=None):
 
 def _space(workspace, dev):
     """A call's workspace as the library takes it, on the call's GPU."""
-    wp, wb = _ws(workspace)
-    if workspace is not None and not isinstance(workspace, tuple) and workspace.get_device() != dev:
+    if workspace is None or isinstance(workspace, tuple):
+        return _ws(workspace)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _ptr(workspace)
         raise ValueError(f"workspace is on {workspace.device}, the call's other tensors on GPU {dev}")
-    return wp, wb
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _one_gpu(struct, *tensors):
@@ -723,10 +725,11 @@ def make_batch(q_start, kv_len, page_table, tokens: int) -> KvBatch:
 
 def _heads(cache: KvCache, batch: KvBatch, t, what: str, extra: int = 0) -> int:
     """Query heads of a [tokens][(q_heads + extra) * head_dim] tensor."""
-    width = t.shape[-1]
-    heads = width // cache.head_dim - extra
-    if t.shape != (batch.tokens, (heads + extra) * cache.head_dim):
-        _need(t, (batch.tokens, (heads + extra) * cache.head_dim), _BF16, what)
+    dim = cache.head_dim
+    shape = t.shape
+    heads = shape[-1] // dim - extra
+    if shape != (batch.tokens, (heads + extra) * dim):
+        _need(t, (batch.tokens, (heads + extra) * dim), _BF16, what)
     return heads
 
 
