@@ -751,9 +751,9 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 // barrier in the loop; e4m3 codes become bf16 exactly, and a page's scale is
 // folded into the scores (k) and the probabilities (v).
 //
-// The blocks of 32 KW keys of all items, in order, are cut into equal shares,
-// one per workgroup (every workgroup computes the cut from the batch's device
-// arrays); each wave takes an equal run of a segment's keys.  A segment that is
+// Short items stay whole, each in one workgroup (stays_whole).  Else the blocks
+// of 32 KW keys of all items, in order, are cut into equal shares, one per
+// workgroup (every workgroup computes the cut from the batch's device arrays); each wave takes an equal run of a segment's keys.  A segment that is
 // not a whole item leaves its m, l and O in the workspace, and a second launch
 // joins an item's segments in order: no atomics, so a result depends on the
 // lengths and the grid only.  (Joining in the first launch, by the last segment
@@ -805,6 +805,7 @@ struct AttnArgs {
   float* part;             // [2 grid] segments: [ROWS][D] sums, [ROWS] m, [ROWS] l
   float scale;             // softmax scale * log2 e
   int groups;              // workgroups
+  int whole;               // each item is one block of one workgroup: nothing to join
 };
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
@@ -822,9 +823,10 @@ __device__ __forceinline__ unsigned e4m3x2_to_bf16(unsigned v) {
 struct Cut {
   int rows;       // of a row group
   int keys;       // of a block
+  int whole;      // each item is one block
 };
 __device__ __forceinline__ int seq_blocks(const Seq& q, Cut cut) {
-  return max(1, (q.cap + cut.keys - 1) / cut.keys);
+  return cut.whole ? 1 : max(1, (q.cap + cut.keys - 1) / cut.keys);
 }
 __device__ __forceinline__ int seq_row_groups(const Seq& q, int group, Cut cut) {
   return (q.n * group + cut.rows - 1) / cut.rows;
@@ -1084,7 +1086,8 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
   constexpr int ROWS = kWaveRows * RW;
   constexpr int kAll = 64 * NW;                      // threads
   constexpr int kStride = D + 4;                     // LDS row of the waves' sums, padded
-  constexpr Cut cut{ROWS, 32 * KW};
+  constexpr int kKeys = 32 * KW;                     // keys of a block
+  const Cut cut{ROWS, kKeys, a.whole};
   // Keys that one wave reads come in whole 128-byte lines: lane (c, g) loads
   // 16-byte part g + 4 (c % 2) of a line of key c & ~1, then of c | 1.  Products
   // with both halves of q leave each score in two neighbouring rows, in one lane.
@@ -1113,8 +1116,11 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
   while (pos < end) {
     const Place pl = place_of(kv, cut, work, pos);
     const int h = pl.rgs == 1 ? pl.item : pl.item / pl.rgs, rg = pl.item - h * pl.rgs;
-    const int blocks = min(pl.nb - pl.blk, end - pos);
     const Seq q = pl.q;
+    const int steps = min(pl.nb - pl.blk, end - pos);
+    const bool whole = steps == pl.nb;
+    // 32-key tiles of each wave.
+    const int blocks = a.whole ? (q.cap + kKeys - 1) / kKeys : steps;
     const int row_count = min(q.n * kv.group - rg * ROWS, ROWS);
     // This wave's rows, and the keys seen by the first and the last of them.
     const int row0 = rg * ROWS + rw * kWaveRows;
@@ -1377,7 +1383,6 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 
     // The waves' sums, 16 rows of each row wave at a time.
     settle(o);
-    const bool whole = blocks == pl.nb;
     float* part = a.part + (size_t)(2 * blockIdx.x + (pl.blk == 0 ? 1 : 0)) * part_floats<D>(ROWS);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -1429,7 +1434,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
     }
     if (pl.blk == 0 && !whole)
       split = Split{shares.of(pos + pl.nb - 1) - (int)blockIdx.x + 1, row_count, rg * ROWS, q.q0, h};
-    pos += blocks;
+    pos += steps;
   }
   if (tid == 0) a.splits[blockIdx.x] = split;
 }
@@ -1670,6 +1675,25 @@ size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, i
 
 constexpr int kGroupsPerCU = 1;
 
+// Whether a call's items stay whole, one workgroup each and no second launch: at
+// most four tiles and 32 KB of keys and values per wave by the page table's
+// width, and no more items than workgroups (or one tile, which has no parts).
+// Whole against split, us: e4m3, 5 sequences, 32 heads on 8 of 64: 6.6 / 7.6 at
+// 256 keys, 8.3 / 9.4 at 777, 9.5 / 9.6 at 1500 (6 tiles: split), 11.9 / 9.6 at
+// 2048; bf16, 16 sequences, 64 on 8 of 128: 7.9 / 9.5 at 256, 11.2 / 12.4 at 512,
+// 13.6 / 12.6 at 777 (split); 48 such sequences, 384 items: 15.0 / 16.7 at 256 (one
+// tile), 19.7 / 17.7 at 512 (split).
+constexpr int kWholeTiles = 4;
+constexpr int kWholeBytes = 32 * 1024;
+bool stays_whole(const skinny_kv_cache& c, const skinny_kv_batch& b, RowCut r, long long items,
+                 long long groups) {
+  const long long keys = (long long)b.max_pages * c.page_tokens;
+  const int block = 32 * (waves_of(c.head_dim) / r.rw);
+  const long long tiles = (keys + block - 1) / block;
+  const int bytes = 32 * 2 * c.head_dim * (c.dtype == SKINNY_KV_BF16 ? 2 : 1);
+  return tiles <= kWholeTiles && tiles * bytes <= kWholeBytes && (tiles == 1 || items <= groups);
+}
+
 template <int DT, int D, int RT, int RW>
 skinny_status launch_attention(const AttnArgs& a, int rows, hipStream_t stream) {
   constexpr int NW = waves_of(D);
@@ -1677,7 +1701,7 @@ skinny_status launch_attention(const AttnArgs& a, int rows, hipStream_t stream) 
   hipLaunchKernelGGL((skinny_kv_attention_k<DT, D, RT, RW, NW>), dim3(a.groups), dim3(64 * NW), 0,
                      stream, a);
   if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
-  if (a.groups == 1) return SKINNY_OK;               // nothing is split
+  if (a.groups == 1 || a.whole) return SKINNY_OK;    // nothing is split
   if (rows > ROWS) rows = ROWS;
   hipLaunchKernelGGL((skinny_kv_attention_join<D>),
                      dim3(a.groups - 1, (rows + kJoinRows<D> - 1) / kJoinRows<D>),
@@ -1831,7 +1855,10 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   a.scale = scale * 1.44269504088896340736f;         // log2 e: the kernel's softmax is in exp2
   long long groups = (long long)d.cus * kGroupsPerCU;
   if (groups > kMaxGroups) groups = kMaxGroups;
-  if (groups > work) groups = work;
+  const long long items = max_items(c, b, q_heads, r);
+  a.whole = stays_whole(c, b, r, items, groups);
+  const long long parts = a.whole ? items : work;
+  if (groups > parts) groups = parts;
   a.groups = (int)groups;
   const long long rows = (long long)b.tokens * (q_heads / c.kv_heads);
   const int most = rows < 128 ? (int)rows : 128;     // rows of an item at most

@@ -68,6 +68,20 @@ def test_prompt(dtype):
     check(kv.Case([(70, 100)], hq=8, hkv=1, D=128, dtype=dtype, seed=24))
 
 
+@pytest.mark.parametrize("seqs", [3, 70])
+@pytest.mark.parametrize("wider", [0, 1])
+@pytest.mark.parametrize("dtype,D,tiles", [("fp8", 64, 4), ("fp8", 128, 4), ("fp8", 256, 2),
+                                           ("bf16", 64, 4), ("bf16", 128, 2), ("bf16", 256, 1)])
+def test_whole_items(dtype, D, tiles, wider, seqs):
+    """Both sides of the page table's width up to which items stay whole, and
+    more items than workgroups."""
+    keys = tiles * 32 * (4 if D == 256 else 8)
+    lens = [(1, keys), (2, 3), (1, keys - 37)]
+    lens += [(int(i % 7 > 0), 1 + 7 * i % keys) for i in range(seqs - 3)]
+    check(kv.Case(lens, P=16, hq=8, hkv=4, D=D, dtype=dtype, seed=D + seqs,
+                  max_pages=keys // 16 + wider))
+
+
 def test_many_sequences():
     rng = np.random.default_rng(5)
     seqs = [(int(n), int(n + rng.integers(0, 200))) for n in rng.integers(0, 3, 150)]
