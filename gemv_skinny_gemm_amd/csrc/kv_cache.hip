@@ -17,6 +17,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "host_util.h"
 #include "skinny_gemm.h"
 
@@ -1149,13 +1151,6 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 
     f32x4 o[RT][Sh::kTiles];
     float m[RT], l[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      m[rt] = kNegInf;
-      l[rt] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] = f32x4{0, 0, 0, 0};
-    }
 
     // This wave's keys: as many tiles of 32 as the segment has blocks.
     const int key0 = (pl.blk * KW + kw * blocks) * 32;
@@ -1225,9 +1220,22 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 
     // The next tile's keys load behind this tile's scores, its values behind
     // this tile's output; the last tile loads itself once more.
+    //   Values that are no finite numbers leave the products, and come back behind
+    // the loop for the rows that see their keys: in tiles with a mask, where 0 * inf
+    // and 0 * NaN would reach rows that do not, and, once sums have turned out not
+    // to be finite, in a second run over all tiles, where a probability that
+    // vanishes in fp32 would make a NaN of an infinity.
     Half now[2];
-    bool dirty = false;                              // a masked tile had such values
-    if (tiles > 0) {
+    bool dirty = false;                              // such values were found
+    const auto run = [&](auto clean) {               // whether this is the second run
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = kNegInf;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < Sh::kTiles; ++j) o[rt][j] = f32x4{0, 0, 0, 0};
+      }
+      if (tiles <= 0) return;
       look(key0);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
@@ -1327,9 +1335,7 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 #pragma unroll
           for (int i = 0; i < 4; ++i) pf[rt][i] = pack_bf16(p[2 * i], p[2 * i + 1]);
         }
-        if (masked) {
-          // 0 * inf and 0 * NaN are NaN: values that are no finite numbers leave
-          // the product, and come back below for the rows that do see their keys.
+        if (clean.value || masked) {
           unsigned any = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -1351,14 +1357,26 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
         }
         load_v(now);
       } while (++t < tiles);
-    }
+      settle(o);
+    };
+    run(std::false_type{});
+    // 0 as long as every sum is finite; one chain per register of a tile.
+    f32x4 zero{0, 0, 0, 0};
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int j = 0; j < Sh::kTiles; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) zero[r] = fmaf(o[rt][j][r], 0.0f, zero[r]);
+    const bool clean = __any((zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f);
+    if (__builtin_expect(clean, 0)) run(std::true_type{});
 
     for (int t = dirty ? 0 : tiles; t < tiles; ++t) {
       const int key = key0 + 32 * t;
       look(key);
       now[0] = half_of(key);
       now[1] = half_of(key + 16);
-      if (now[0].there && now[1].there && key + 32 <= lim_lo) continue;
+      if (!clean && now[0].there && now[1].there && key + 32 <= lim_lo) continue;
       load_v(now);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -1382,7 +1400,6 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
     }
 
     // The waves' sums, 16 rows of each row wave at a time.
-    settle(o);
     float* part = a.part + (size_t)(2 * blockIdx.x + (pl.blk == 0 ? 1 : 0)) * part_floats<D>(ROWS);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {

@@ -529,7 +529,8 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
  *   scale   finite, usually 1 / sqrt(head_dim)
  * Scores, the softmax's statistics and sums are fp32; the probabilities are
  * rounded to bf16 for the product with v.  Keys and values of positions that a
- * row does not see do not reach it, whatever they hold.  A row that sees no
+ * row does not see do not reach it, whatever they hold; an infinite value that
+ * it sees gives that infinity, however small its probability.  A row that sees no
  * position gets zeros; rows that belong to no sequence are left as they were.
  * Results are reproducible bitwise for the same lengths, shapes and device.
  *   workspace  >= skinny_kv_attention_workspace_bytes(cache, batch, q_heads)
