@@ -781,6 +781,9 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 constexpr int kMaxGroups = 512;          // workgroups of the grid at most
 constexpr size_t kSplitBytes = kMaxGroups * 32;
 constexpr float kNegInf = -__builtin_inff();
+// The maximum of a row that sees keys, but with scores of -inf (or NaN) only: lower
+// than another share's, and at the end 0 / 0, where -inf, no key seen, is zeros.
+constexpr float kAllNegInf = -__FLT_MAX__;
 // m need not be the maximum itself, only near it: sums are scaled again when a
 // score passes it by more than this (probabilities then reach 2^8, far from
 // fp32's and bf16's ends).  A wave's first tiles would otherwise do so nearly
@@ -1078,6 +1081,12 @@ __device__ __forceinline__ u32x4 v_marks(const unsigned (&raw)[8][Shape<DT, D>::
     r[p] = v_bf16<DT>(bad, j);
   }
   return r;
+}
+
+// 1 / the sum of a row's weights.
+__device__ __forceinline__ float inverse(float top, float sum) {
+  if (top == kAllNegInf) return __builtin_nanf("");
+  return top == kNegInf ? 0.0f : 1.0f / sum;
 }
 
 template <int DT, int D, int RT, int RW, int NW>
@@ -1399,6 +1408,21 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
       }
     }
 
+    bool none = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) none = none || (m[rt] == kNegInf && key0 < lim[rt]);
+    for (int t = __any(none) ? 0 : tiles; t < tiles; ++t) {
+      const int key = key0 + 32 * t;
+      look(key);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool there = half_of(key + 16 * u).there;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          if (there && key + 16 * u < lim[rt] && m[rt] == kNegInf) m[rt] = kAllNegInf;
+      }
+    }
+
     // The waves' sums, 16 rows of each row wave at a time.
     float* part = a.part + (size_t)(2 * blockIdx.x + (pl.blk == 0 ? 1 : 0)) * part_floats<D>(ROWS);
 #pragma unroll
@@ -1427,13 +1451,12 @@ __global__ __launch_bounds__(64 * NW) void skinny_kv_attention_k(const AttnArgs 
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
             const float mw = sm[w * RW + w0][rr], lw2 = sl[w * RW + w0][rr];
-            // Without a maximum l is 0 (no key seen) or NaN (a score was).
-            const float f = mw == kNegInf ? lw2 : __builtin_amdgcn_exp2f(mw - top);
+            const float f = mw == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw - top);
             sum += f * lw2;
             x += f * *reinterpret_cast<const f32x4*>(&sums[w * RW + w0][rr][d]);
           }
           if (whole) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = inverse(top, sum);
             const int r = rg * ROWS + row, tok = by_group(kv, r), head = r - tok * kv.group;
             *reinterpret_cast<u32x2*>(a.out +
                 ((size_t)(q.q0 + tok) * q_heads + h * kv.group + head) * D + d) =
@@ -1505,8 +1528,7 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
 #pragma unroll
     for (int e = 0; e < kJoinAhead; ++e)
       if (k0 + e * kJoinSets < n) {
-        // Without a maximum l is 0 (no key seen) or NaN (a score was).
-        const float f = mk[e] == kNegInf ? lk[e] : __builtin_amdgcn_exp2f(mk[e] - top);
+        const float f = mk[e] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk[e] - top);
         sum += f * lk[e];
         x += f * y[e];
       }
@@ -1525,11 +1547,11 @@ __global__ __launch_bounds__(kJoinThreads) void skinny_kv_attention_join(const A
 #pragma unroll
   for (int k = 0; k < kJoinSets; ++k) {
     const float tk = st[k][slot], lk = sl[k][slot];
-    const float f = tk == kNegInf ? lk : __builtin_amdgcn_exp2f(tk - top);
-    sum += tk == kNegInf ? lk : f * lk;
+    const float f = tk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(tk - top);
+    sum += f * lk;
     x += f * sx[k][slot][d];
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = inverse(top, sum);
   const int group = a.kv.group, r = sp.row0 + row;
   *reinterpret_cast<u32x2*>(a.out + ((size_t)(sp.q0 + r / group) * a.kv.kv_heads * group +
                                      sp.h * group + r % group) * D + 4 * d) =

@@ -531,7 +531,8 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
  * rounded to bf16 for the product with v.  Keys and values of positions that a
  * row does not see do not reach it, whatever they hold; an infinite value that
  * it sees gives that infinity, however small its probability.  A row that sees no
- * position gets zeros; rows that belong to no sequence are left as they were.
+ * position gets zeros, one that sees scores of -inf only NaN (0 / 0); rows that
+ * belong to no sequence are left as they were.
  * Results are reproducible bitwise for the same lengths, shapes and device.
  *   workspace  >= skinny_kv_attention_workspace_bytes(cache, batch, q_heads)
  *              bytes (0 for invalid arguments; pure host arithmetic on the

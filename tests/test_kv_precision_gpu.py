@@ -57,3 +57,30 @@ def test_infinite_values_of_small_probability(D, rows, length):
         assert np.array_equal(got[inf], want[inf]), f"infinities, {back} back"
         ok = np.isfinite(want)
         assert (np.abs(got - want)[ok] <= tol[ok]).all(), f"the rest, {back} back"
+
+
+@pytest.mark.parametrize("rows,length,finite", [(1, 20, []), (1, 300, []), (7, 300, []), (1, 9000, []),
+                                                (1, 300, [5]), (1, 300, [299]), (1, 9000, [4500]),
+                                                (3, 9000, [8998])])
+def test_scores_of_minus_infinity(rows, length, finite):
+    """Scores of -inf take no part where a row has a finite one; a row with no
+    other scores is 0 / 0 (zeros are for rows that see no position)."""
+    c = kv.Case([(rows, length), (2, 33)], hq=4, hkv=2, D=64, dtype="bf16", seed=61)
+    aligned_queries(c, 1.0)
+    first_key_values(c, 0, 0, length, -np.inf)
+    for pos in finite:
+        first_key_values(c, 0, pos, pos + 1, 0.5)
+    got = attend(c)
+    v = c.values("v")
+    for r in range(rows):
+        end = length - rows + r + 1
+        seen = [p for p in finite if p < end]
+        for h in range(c.hq):
+            row = got[r, h * c.D:(h + 1) * c.D]
+            if not seen:
+                assert np.isnan(row).all(), f"row {r}"
+            else:
+                pos = seen[0]
+                assert np.array_equal(row, v[c.table[0, pos // c.P], h // 2, pos % c.P]), f"row {r}"
+    want, tol, _ = kv.attention_oracle(c)                # the other sequence
+    assert (np.abs(got - want) <= tol)[rows:].all()
