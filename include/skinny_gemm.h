@@ -527,8 +527,8 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
  * head head / (q_heads / kv_heads).
  *   q, out  [tokens][q_heads head_dim] bf16, 16-byte aligned; out is written
  *   scale   finite, usually 1 / sqrt(head_dim)
- * Scores, the softmax's statistics and sums are fp32; the probabilities are
- * rounded to bf16 for the product with v.  Keys and values of positions that a
+ * Scores, the softmax's statistics and sums are fp32; the probabilities go into
+ * the product with v as two bf16 numbers each, within 2^-16.  Keys and values of positions that a
  * row does not see do not reach it, whatever they hold; an infinite value that
  * it sees gives that infinity, however small its probability.  A row that sees no
  * position gets zeros, one that sees scores of -inf only NaN (0 / 0); rows that

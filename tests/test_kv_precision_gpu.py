@@ -84,3 +84,45 @@ def test_scores_of_minus_infinity(rows, length, finite):
                 assert np.array_equal(row, v[c.table[0, pos // c.P], h // 2, pos % c.P]), f"row {r}"
     want, tol, _ = kv.attention_oracle(c)                # the other sequence
     assert (np.abs(got - want) <= tol)[rows:].all()
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "bf16"])
+@pytest.mark.parametrize("seqs,hq,hkv,D", [([(1, 3), (1, 7), (2, 40)], 8, 2, 64),
+                                           ([(6, 9), (6, 500)], 16, 2, 128),
+                                           ([(12, 12), (3, 6000)], 8, 1, 256),
+                                           ([(1, 20000)], 8, 1, 128)])
+def test_probabilities_keep_16_bits(dtype, seqs, hq, hkv, D):
+    """The output's own rounding is the only one to 8 bits.  With p held to 2^-16
+    of itself (bf16 of p and of the rest), scores as in the oracle's bound, and A
+    = sum p |v|: |err| <= 2^-8 |out| + (2^-16 + 4 (D + 4) 2^-24 max|q||k| + 2 (L +
+    64) 2^-24) A, and 1e-3 of the rounding for what it does to a rounded error."""
+    c = kv.Case(seqs, hq=hq, hkv=hkv, D=D, P=32, dtype=dtype, seed=62)
+    # Short keys and queries: what the scores' fp32 sums may lose stays below 2^-14.
+    c.q = kv.bf16_round(0.25 * kv.bf16_values(c.q))
+    if dtype == "bf16":
+        k = kv.bf16_values(c.codes["k"])
+        c.codes["k"] = np.where(np.isnan(k), c.codes["k"], kv.bf16_round(0.25 * k)).astype(np.uint16)
+    else:
+        c.scales["k"] *= np.float32(0.25)
+    got = attend(c)
+    want, rough, _ = kv.attention_oracle(c)
+    vals = {n: c.values(n) for n in ("k", "v")}
+    G, worst = hq // hkv, 0.0
+    for s in range(len(seqs)):
+        n, length = seqs[s]
+        ids = c.table[s, :-(-length // c.P)]
+        kk, vv = (vals[x][ids].transpose(1, 0, 2, 3).reshape(hkv, -1, D)[:, :length] for x in ("k", "v"))
+        q = kv.bf16_values(c.q).reshape(c.T, hq, D)
+        for r in range(n):
+            end = length - n + r + 1
+            for h in range(hq):
+                row, k, v = q[c.q_start[s] + r, h], kk[h // G][:end], vv[h // G][:end]
+                p = np.exp(D ** -0.5 * (k @ row))
+                p /= p.sum()
+                big = D ** -0.5 * (np.abs(k) @ np.abs(row)).max()
+                rel = 2.0 ** -16 + 4 * (D + 4) * kv.ULP32 * big + 2 * (end + 64) * kv.ULP32
+                at = slice(h * D, (h + 1) * D)
+                out = want[c.q_start[s] + r, at]
+                tol = 1.001 * kv.HALF_BF16 * np.abs(out) + 1.01 * rel * (p @ np.abs(v)) + 1e-30
+                worst = max(worst, np.max(np.abs(got[c.q_start[s] + r, at] - out) / tol))
+    assert worst <= 1.0, worst
