@@ -350,12 +350,17 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   const void* src = static_cast<const L*>(which ? a.draft : a.logits) + (size_t)row * a.V;
   const int n0 = slice * kSlice<PER> + wave * kSub<PER>;
   float l[PER];
-  load_sub<L, VEC, PER>(src, n0, a.V, l);               // on its way while the row's sequence is found
-  if (slice == 0 && tid == 0) {
-    const int d = row + 1 < a.T ? a.tokens[row + 1] : -1;
-    a.drafted[(size_t)which * a.T + row] =
-        d >= 0 && d < a.V ? logit<L>(src, d) : __builtin_nanf("");
-  }
+  const auto load = [&] {
+    load_sub<L, VEC, PER>(src, n0, a.V, l);
+    if (slice == 0 && tid == 0) {
+      const int d = row + 1 < a.T ? a.tokens[row + 1] : -1;
+      a.drafted[(size_t)which * a.T + row] =
+          d >= 0 && d < a.V ? logit<L>(src, d) : __builtin_nanf("");
+    }
+  };
+  // The target's are on their way while the row's sequence is found.  The draft's
+  // wait until it is known that they are asked: those of other rows need not be there.
+  if (which == 0) load();
   if (row == 0 && which == 0) {
     for (int i = tid; i < a.S * kWaves; i += kThreads)
       a.weight[((size_t)(i / kWaves) * a.slices + slice) * kWaves + i % kWaves] = kNotYet;
@@ -368,7 +373,10 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_stats(const VerifyArgs
   const float t = temperature_of(a, s);
   const bool greedy = !(t > 0.0f);
   // The draft's last row drafted nothing, and a greedy sequence asks only the target.
-  if (which == 1 && (greedy || row + 1 == r.q0 + r.n)) return;
+  if (which == 1) {
+    if (greedy || row + 1 == r.q0 + r.n) return;
+    load();
+  }
   // Each wave's maximum and sum, then the four joined.
   float top = kNegInf;
 #pragma unroll

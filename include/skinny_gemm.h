@@ -556,8 +556,8 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
  * skinny_kv_batch, values not trusted); tokens[row] is the token that the step
  * read at that row: a sequence's first one is its last sure token, the others
  * are drafted.  logits[row] are the target's for the place after it, and
- * draft_logits[row] those that the token at row + 1 was drawn from (a sequence's
- * last row is not read).  With p = softmax(logits[row] / t), q =
+ * draft_logits[row] those that the token at row + 1 was drawn from (the rows of a
+ * greedy sequence, a sequence's last row and rows of none are not read).  With p = softmax(logits[row] / t), q =
  * softmax(draft_logits[row] / t), t = temperature[s] and d = tokens[row + 1]:
  *   row by row, d is kept while accept_u[row] * q(d) < p(d);
  *   at the first row that keeps none, the next token is drawn from max(0, p - q)
