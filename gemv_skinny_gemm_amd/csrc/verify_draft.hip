@@ -13,7 +13,9 @@
 // distribution that moves by 2^-24 of the total gives another token once in a
 // few hundred calls at 150 thousand entries.  Exponentials and sums are
 // therefore fp64 throughout (one wave instruction of fp64 FMA costs what an fp32
-// one does on this GPU), which puts the boundaries within about 2^-50.
+// one does on this GPU).  2^y is within 2^-47 of itself by its series and |y| 2^-52
+// by y's own rounding; entries far below the largest add little to a sum, so
+// boundaries are within about 2^-46 of the total (1.4e-14).
 //
 // Two launches:
 //   skinny_verify_stats   workgroup (slice, row, target or draft): the largest

@@ -573,8 +573,11 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
  *     token, then -1; rows of no sequence are left as they were
  *   accepted [seqs] int32: drafts kept, so accepted + 1 tokens are new (0, and
  *     none, for a sequence without rows)
- * Probabilities and sums are fp64: the tokens are those of exact arithmetic
- * unless a random number lies within about 1e-13 of a boundary.
+ * Probabilities and sums are fp64, and an entry below 2^-1000 of its row's largest
+ * probability has none: it is neither drawn nor kept (so masks of the type's lowest
+ * value hold for a random number of 0, too).  The tokens are then those of exact
+ * arithmetic unless a random number lies within about 2e-13 of a boundary,
+ * relative to it.
  *   accept_u [rows], sample_u [seqs] fp32, uniform on [0, 1)
  *   logits, draft_logits [rows][vocab] bf16 or fp32, aligned to their type (read
  *     16 bytes at a time when 16-byte aligned and rows are multiples of 16 bytes)

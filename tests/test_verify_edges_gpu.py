@@ -2,12 +2,13 @@
 ask for, drafts of vanishing probability, vocabularies of many trips."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import gemv_skinny_gemm_amd as sg
 from tests.gpu_util import need_gpu
-from tests.test_verify_gpu import case, compare, upload
+from tests.test_verify_gpu import BELOW_ONE, case, compare, run, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -22,7 +23,7 @@ def _gpu():
                                               ([4], [1.0], 3), ([5, 1, 1], [0.8], 4)])
 def test_rows_of_the_draft_that_are_not_asked(dtype, rows, temps, asked):
     """The last row of a sequence, greedy sequences' rows and rows of no sequence
-    need no draft logits: there are none behind the last row that is asked."""
+    need no draft logits; here there are none behind the last row that is asked."""
     c = case(rows, 100003, dtype, seed=40, tail=2, temps=temps)
     d = upload(c)
     T, V = c["logits"].shape
@@ -36,3 +37,30 @@ def test_rows_of_the_draft_that_are_not_asked(dtype, rows, temps, asked):
     assert sg.lib().skinny_verify_draft(v, d["ws"].data_ptr(), d["ws"].numel(), None) == 0
     torch.cuda.synchronize()
     compare(c, d)
+
+
+@pytest.mark.parametrize("p_at,q_at,au,kept", [
+    (-900, -901, BELOW_ONE, 1), (-901, -900, 0.499, 1), (-901, -900, 0.501, 0), (-999, -999, 0.999, 1),
+    (-1001, -900, 0.0, 0), (-1001, -1002, 0.5, 0), (-999, -1002, BELOW_ONE, 1), (-20, -900, 0.5, 1)])
+def test_drafts_far_below_the_largest(p_at, q_at, au, kept):
+    """u q(d) < p(d) at a low temperature, by the ratio of two probabilities of
+    2^p_at and 2^q_at; what lies below 2^-1000 is no probability, and is not kept."""
+    t = np.float32(2e-3)
+    c = case([2], 5000, "f32", seed=30, temps=[t])
+    c["logits"][0], c["draft"][0] = -3.0, -3.0           # 2^-2164 and less
+    c["logits"][0, 7] = c["draft"][0, 9] = 0.0           # p is 1 at 7, q is 1 at 9
+    c["tokens"][1], c["accept_u"][0] = 4321, au
+    for name, at in (("logits", p_at), ("draft", q_at)):
+        c[name][0, 4321] = at * np.log(2.0) * np.float64(t)
+    d = upload(c)
+    run(d)
+    torch.cuda.synchronize()
+    assert d["accepted"].tolist() == [kept]
+    assert d["out"].tolist()[0] == (4321 if kept else 7)
+    # The same draft, given instead of drawn: q is 1, only a random number of 0 keeps it.
+    for u in (0.0, 2.0 ** -22):
+        d["accept_u"].fill_(u)
+        d["draft"] = None
+        run(d)
+        torch.cuda.synchronize()
+        assert d["accepted"].tolist() == [int(p_at > -1000 and u * 2.0 ** 500 < 2.0 ** (p_at + 500))]
