@@ -24,7 +24,7 @@ __all__ = [
     "MOE_X_PER_ROUTE", "MOE_SWIGLU", "MAX_TOPK", "KERNEL_NAMES",
     "KV_BF16", "KV_FP8", "KvCache", "KvBatch", "make_kv_cache", "make_batch", "kv_append",
     "kv_attention", "kv_attention_workspace_bytes", "LOGITS_BF16", "LOGITS_F32", "Verify",
-    "verify_draft", "verify_workspace_bytes",
+    "verify_draft", "verify_workspace_bytes", "verify_set_spin_limit",
 ]
 
 BF16 = 0
@@ -196,6 +196,8 @@ def _bind(path: str):
     L.skinny_verify_workspace_bytes.argtypes = [i, i, i]
     L.skinny_verify_draft.restype = i
     L.skinny_verify_draft.argtypes = [ctypes.POINTER(Verify), vp, sz, vp]
+    L.skinny_verify_set_spin_limit.restype = None
+    L.skinny_verify_set_spin_limit.argtypes = [ctypes.c_longlong]
     L.skinny_status_string.restype = ctypes.c_char_p
     L.skinny_status_string.argtypes = [i]
     L.skinny_abi_version.restype = i
@@ -784,7 +786,7 @@ def verify_draft(q_start, logits, tokens, accept_u, sample_u, out_tokens, accept
     (the step's input tokens), q_start int32 [seqs + 1], accept_u float32 [rows],
     sample_u and temperature float32 [seqs]; out_tokens int32 [rows] gets each
     sequence's kept drafts, its next token, then -1, and accepted int32 [seqs]
-    the number kept."""
+    the number kept (-1 if a wait inside the launch gave up)."""
     tt, dev = _call_device(logits)
     rows, vocab = _shape2(logits)
     seqs = sample_u.shape[0]
@@ -808,3 +810,9 @@ def verify_draft(q_start, logits, tokens, accept_u, sample_u, out_tokens, accept
     _check(lib().skinny_verify_draft(v, wp, wb, _call_stream(tt, dev, stream)),
            "skinny_verify_draft")
     return out_tokens
+
+
+def verify_set_spin_limit(polls: int) -> None:
+    """Polls before a sampling sequence's wait for another workgroup's sums gives
+    up (< 0: it does not wait); for tests of that path."""
+    lib().skinny_verify_set_spin_limit(int(polls))

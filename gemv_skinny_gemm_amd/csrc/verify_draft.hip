@@ -28,7 +28,8 @@
 //     quarter, then the entry, where the running sum passes u times the
 //     total; sums are added in index order, so it does not matter who came last.
 // The sums pass between workgroups as relaxed device-scope words that the first
-// launch set to a mark: a word read before it arrived is read again.  Fences in
+// launch set to a mark: a word read before it arrived is read again, up to a limit
+// of polls, behind which the sequence gets -1 in the place of its results.  Fences in
 // their place cost about 8 us a call here (they write back and invalidate an
 // XCD's whole L2).
 //
@@ -47,6 +48,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "host_util.h"
 #include "skinny_gemm.h"
@@ -78,7 +80,7 @@ constexpr int kRowsAtOnce = kThreads / kRowLanes;
 constexpr int kBatch = 4;                          // exponentials at a time
 constexpr float kNegInf = -__builtin_inff();
 constexpr unsigned long long kNotYet = ~0ull;      // a NaN that no sum is
-constexpr int kMaxPolls = 1 << 16;
+std::atomic<long long> g_polls{1 << 16};
 
 struct Stat {
   double sum;            // sum over the slice of exp((l - max) / t)
@@ -101,6 +103,7 @@ struct VerifyArgs {
   float* drafted;        // [2][T] logit of the token drafted at each row (NaN: none)
   int* arrived;          // [S]
   int T, S, V, slices;
+  long long polls;       // of a word that has not arrived, before giving up; < 0: at once
 };
 
 struct Rows {
@@ -504,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
   __shared__ int is_last, found, positive;
   __shared__ double wsum[kWaves];
   __shared__ double goal_s, before_s;
-  __shared__ int sub_s, plain_s;
+  __shared__ int sub_s, plain_s, gave_up;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int slice = blockIdx.x, s = blockIdx.y;
   const Rows r = rows_of(a, s);
@@ -582,6 +585,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
   const bool final = st.row == r.n - 1;
 
   int token = 0;
+  bool failed = false;
   if (greedy) {
     token = st.greedy_token;
   } else {
@@ -628,6 +632,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
       // The lane's run of words from i0 on.  With `plain` a slice's sum counts
       // at its first word, and the slice is searched as a whole.
       static_assert(kRun == kWaves, "a lane's run is a slice");
+      bool missing = a.polls < 0;
       const auto fetch = [&](int i0, bool plain) {
         const int i = i0 + lane * kRun;
         double x = 0.0;
@@ -639,7 +644,7 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
         } else {
           unsigned long long y[kRun];
           bool all = false;
-          for (int k = 0; !all && k < kMaxPolls; ++k) {
+          for (long long k = 0; !all && k <= a.polls; ++k) {
             all = true;
 #pragma unroll
             for (int e = 0; e < kRun; ++e)
@@ -648,9 +653,10 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
 #pragma unroll
             for (int e = 0; e < kRun; ++e) all = all && y[e] != kNotYet;
           }
+          missing = missing || !all;
 #pragma unroll
           for (int e = 0; e < kRun; ++e) {
-            w[e] = i < subs && y[e] != kNotYet ? __builtin_bit_cast(double, y[e]) : 0.0;
+            w[e] = all && i < subs ? __builtin_bit_cast(double, y[e]) : 0.0;
             x += w[e];
           }
         }
@@ -696,7 +702,9 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
         }
         before += lane_of(incl, 63);
       }
+      const bool any_missing = __any(missing);
       if (lane == 0) {
+        gave_up = any_missing;
         sub_s = max(at, 0);
         before_s = at_before;
         goal_s = goal;
@@ -750,13 +758,14 @@ __global__ __launch_bounds__(kThreads) void skinny_verify_pick(const VerifyArgs 
       if (found < a.V) break;
     }
     token = found < a.V ? found : positive;
+    failed = gave_up;
   }
 
   for (int i = tid; i < r.n; i += kThreads) {
     const int next = i == tid ? kept : i + 1 < r.n ? a.tokens[r.q0 + i + 1] : -1;
-    a.out_tokens[r.q0 + i] = i < st.row ? next : i == st.row ? token : -1;
+    a.out_tokens[r.q0 + i] = failed ? -1 : i < st.row ? next : i == st.row ? token : -1;
   }
-  if (tid == 0) a.accepted[s] = st.row;
+  if (tid == 0) a.accepted[s] = failed ? -1 : st.row;
 }
 
 // ---------------------------------------------------------------------------
@@ -890,8 +899,11 @@ skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
   a.S = v.seqs;
   a.V = v.vocab;
   a.slices = slices_of(v.vocab, per_of(v.rows, v.vocab));
+  a.polls = g_polls.load();
   return v.dtype == SKINNY_LOGITS_BF16 ? launch_as<__bf16>(a, (hipStream_t)stream)
                                        : launch_as<float>(a, (hipStream_t)stream);
 }
+
+void skinny_verify_set_spin_limit(long long polls) { g_polls.store(polls); }
 
 }  // extern "C"

@@ -572,7 +572,9 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
  *   out_tokens [rows] int32: at a sequence's rows its kept drafts, the next
  *     token, then -1; rows of no sequence are left as they were
  *   accepted [seqs] int32: drafts kept, so accepted + 1 tokens are new (0, and
- *     none, for a sequence without rows)
+ *     none, for a sequence without rows).  -1, and -1 in all of its out_tokens, if
+ *     a wait inside the launch gave up (skinny_verify_set_spin_limit; by default
+ *     after polls of many times what a launch takes): the step is to be repeated
  * Probabilities and sums are fp64, and an entry below 2^-1000 of its row's largest
  * probability has none: it is neither drawn nor kept (so masks of the type's lowest
  * value hold for a random number of 0, too).  The tokens are then those of exact
@@ -607,6 +609,10 @@ typedef struct skinny_verify {
 size_t skinny_verify_workspace_bytes(int rows, int seqs, int vocab);
 skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
                                   size_t workspace_bytes, void* stream);
+/* Polls for another workgroup's sums before a sampling sequence gives up (default
+ * 65536; a negative value makes it give up without waiting).  Process-wide; read
+ * when a call is enqueued.  For tests of that path. */
+void skinny_verify_set_spin_limit(long long polls);
 
 /* Static text for a status code; never NULL. */
 const char* skinny_status_string(int status);

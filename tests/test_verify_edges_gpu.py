@@ -8,7 +8,7 @@ import torch
 
 import gemv_skinny_gemm_amd as sg
 from tests.gpu_util import need_gpu
-from tests.test_verify_gpu import BELOW_ONE, case, compare, run, upload
+from tests.test_verify_gpu import BELOW_ONE, case, compare, oracle, run, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,26 @@ def test_drafts_far_below_the_largest(p_at, q_at, au, kept):
         run(d)
         torch.cuda.synchronize()
         assert d["accepted"].tolist() == [int(p_at > -1000 and u * 2.0 ** 500 < 2.0 ** (p_at + 500))]
+
+
+def test_a_wait_that_gives_up_says_so():
+    """A spin limit < 0, set from the host, makes every sampling sequence give up:
+    -1 for its count and in all its places, nothing else, and the next call is
+    as ever."""
+    c = case([4, 2, 0, 3], 32003, seed=41, temps=[0.9, 0.0, 1.0, 0.7], tail=1)
+    d = upload(c)
+    sg.verify_set_spin_limit(-1)
+    try:
+        run(d)
+        torch.cuda.synchronize()
+    finally:
+        sg.verify_set_spin_limit(1 << 16)
+    out, accepted = oracle(c)
+    out[[0, 1, 2, 3, 6, 7, 8]] = -1
+    assert d["out"].tolist() == out.tolist()
+    assert d["accepted"].tolist() == [-1, accepted[1], 0, -1]
+    for _ in range(3):
+        d["out"].fill_(-9)
+        run(d)
+        torch.cuda.synchronize()
+        compare(c, d)
