@@ -1724,6 +1724,7 @@ long long max_work(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_hea
 size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, int q_heads) {
   const RowCut r = row_cut(c, b, q_heads);
   const long long w = max_work(c, b, q_heads, r);
+  if (w >= kMaxCount) return 0;                      // more blocks than the kernels count
   const long long groups = w < kMaxGroups ? w : kMaxGroups;
   return kSplitBytes + (size_t)(2 * groups) * (16 * r.rt * r.rw) * (c.head_dim + 2) * sizeof(float);
 }
@@ -1867,6 +1868,7 @@ size_t skinny_kv_attention_workspace_bytes(const skinny_kv_cache* cache,
       check_heads(*cache, q_heads) != SKINNY_OK)
     return 0;
   const size_t b = attention_workspace(*cache, *batch, q_heads);
+  if (b == 0) return 0;
   return b > SKINNY_MIN_WORKSPACE_BYTES ? b : SKINNY_MIN_WORKSPACE_BYTES;
 }
 

@@ -540,7 +540,10 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
  *              sequences have more rows), 16-byte aligned; contents undefined
  *              before and after, so calls that may overlap need their own
  * out must not overlap q, the cache, the batch's arrays or the workspace, nor
- * the workspace any of them. */
+ * the workspace any of them.  A step that could be more blocks of work than 32 bits
+ * count is refused (SKINNY_ERR_UNSUPPORTED, and 0 for its workspace); none is while
+ * kv_heads * (tokens * q_heads / kv_heads / 16 + seqs) * (max_pages * page_tokens
+ * / 32 + 1) stays below 2^31 - 1. */
 size_t skinny_kv_attention_workspace_bytes(const skinny_kv_cache* cache,
                                            const skinny_kv_batch* batch, int q_heads);
 skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_batch* batch,
