@@ -211,17 +211,36 @@ __device__ __forceinline__ float page_scale(float top) {
   return __builtin_bit_cast(float, (unsigned)(max(e, kMinScaleExp) + 127) << 23);
 }
 
-// A page's older codes, four to a dword, from scale `had` to 1 / inv: exact for
-// a power of two, but for codes that become subnormal.
+// Whether a page's scale, the same for all lanes, is a power of two: then products
+// with it or its inverse are exact in fp32 (but for results that underflow, whose
+// code is 0 all the same).
+__device__ __forceinline__ bool power_of_two(float x) {
+  return (uniform(__builtin_bit_cast(int, x)) & 0x7fffff) == 0;
+}
+
+// Other scales, the user's: x / scale rounded to odd, so that the code is the only
+// rounding: a tie stays one, and nothing becomes one.  The product with the inverse
+// is put right by what it leaves of x, to the last bit where the quotient is short.
+__device__ __forceinline__ float quotient(float x, double scale, double inv) {
+  const double q = x * inv;
+  return to_odd(fma(fma(-q, scale, (double)x), inv, q));
+}
+
+// A page's older codes, four to a dword, from scale `had` to 1 / inv, a power of
+// two: exact if `had` is one, but for codes that become subnormal; else rounded
+// once, a code times both being exact in fp64.
 __device__ __forceinline__ void rescale(unsigned* codes, int n, float had, double inv, int tid) {
-  const float ratio = (float)((double)had * inv);
-  for (int i = tid; i < n; i += kThreads) {
-    const unsigned c = codes[i];
-    const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
-    const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
-    codes[i] = pack_e4m3(x[0] * ratio, x[1] * ratio) |
-               pack_e4m3(y[0] * ratio, y[1] * ratio) << 16;
-  }
+  const double ratio = (double)had * inv;
+  const auto every = [&](auto times) {
+    for (int i = tid; i < n; i += kThreads) {
+      const unsigned c = codes[i];
+      const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
+      const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+      codes[i] = pack_e4m3(times(x[0]), times(x[1])) | pack_e4m3(times(y[0]), times(y[1])) << 16;
+    }
+  };
+  if (__builtin_expect(power_of_two(had), 1)) every([r = (float)ratio](float x) { return x * r; });
+  else every([&](float x) { return to_odd(x * ratio); });
 }
 
 // A quad is four values of a head: two neighbours at pa and two at pb that
@@ -473,15 +492,20 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_few(const AppendArg
     const float need = page_scale(top);
     const float now = had >= need ? had : need;
     const double inv = 1.0 / (double)now;
+    const bool exact = power_of_two(now);
     if (older && now != had) rescale(reinterpret_cast<unsigned*>(block), older * upr, had, inv, tid);
-    for (int i = tid; i < count * upr; i += kThreads) {
-      const int r = i / upr, j = i % upr;
-      const Quad u = quad_of(j, rot, a.interleaved);
-      const f32x4 w = rows[i];
-      unsigned short* dst = reinterpret_cast<unsigned short*>(block + (size_t)(older + r) * D);
-      dst[u.pa / 2] = (unsigned short)pack_e4m3((float)(w[0] * inv), (float)(w[1] * inv));
-      dst[u.pb / 2] = (unsigned short)pack_e4m3((float)(w[2] * inv), (float)(w[3] * inv));
-    }
+    const auto every = [&](auto scaled) {
+      for (int i = tid; i < count * upr; i += kThreads) {
+        const int r = i / upr, j = i % upr;
+        const Quad u = quad_of(j, rot, a.interleaved);
+        const f32x4 w = rows[i];
+        unsigned short* dst = reinterpret_cast<unsigned short*>(block + (size_t)(older + r) * D);
+        dst[u.pa / 2] = (unsigned short)pack_e4m3(scaled(w[0]), scaled(w[1]));
+        dst[u.pb / 2] = (unsigned short)pack_e4m3(scaled(w[2]), scaled(w[3]));
+      }
+    };
+    if (__builtin_expect(exact, 1)) every([f = (float)inv](float x) { return x * f; });
+    else every([&](float x) { return quotient(x, now, inv); });
     if (tid == 0) *scale = now;
   }
 }
@@ -702,16 +726,19 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
     const float need = page_scale(top);
     const float now = had >= need ? had : need;
     const double inv = 1.0 / (double)now;
+    const bool exact = power_of_two(now);
     if (older && now != had) rescale(reinterpret_cast<unsigned*>(block), older * D / 4, had, inv, tid);
-    // A power of two divides exactly in fp32; another scale (the user's) in fp64.
-    const bool exact = (__builtin_bit_cast(unsigned, now) & 0x7fffffu) == 0;
-    const float finv = (float)inv;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int r = p * step + tid / upr;
       if (r >= count) break;
+      if (__builtin_expect(exact, 1)) {
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) w[p][e] = exact ? w[p][e] * finv : (float)(w[p][e] * inv);
+        for (int e = 0; e < kUnit; ++e) w[p][e] *= (float)inv;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) w[p][e] = quotient(w[p][e], now, inv);
+      }
       unsigned c[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -505,7 +505,8 @@ typedef struct skinny_kv_batch {
  * for all of this step's rows in the page; rows that continue a page set it to
  * the larger of that and the scale the page has, and where it grows the
  * sequence's earlier codes in the page are rounded again to the new scale
- * (exact but for codes that become subnormal).  Codes are x / scale to nearest
+ * (exact but for codes that become subnormal, unless the caller had set a scale
+ * that is no power of two; that one is kept while it is large enough).  Codes are x / scale to nearest
  * even; infinities become the largest code and take no part in the scale, NaN
  * stays NaN.
  *   Written are q_out's rows that belong to a sequence and the cache's slots of

@@ -126,3 +126,65 @@ def test_probabilities_keep_16_bits(dtype, seqs, hq, hkv, D):
                 tol = 1.001 * kv.HALF_BF16 * np.abs(out) + 1.01 * rel * (p @ np.abs(v)) + 1e-30
                 worst = max(worst, np.max(np.abs(got[c.q_start[s] + r, at] - out) / tol))
     assert worst <= 1.0, worst
+
+
+def odd_scale(seqs, count, seed, scale, codes, row):
+    """`seqs` sequences of `count` rows each behind 8 older ones in their pages;
+    scale(s, h), codes(s, h) and row(s, h) give a page's scale, its older codes
+    and its new values (for k and v alike)."""
+    c = kv.Case([(count, 8 + count)] * seqs, D=64, hq=2, hkv=2, seed=seed, x_sigma=0.5)
+    x = c.qkv.reshape(c.T, 6, 64)
+    for s in range(seqs):
+        page = c.table[s, 0]
+        for h in range(2):
+            for n, lo in (("k", 2), ("v", 4)):
+                c.scales[n][page, h] = scale(s, h)
+                c.codes[n][page, h, :8] = codes(s, h)
+                x[s * count:(s + 1) * count, lo + h] = kv.bf16_round(row(s, h))
+    return c
+
+
+MIDDLES = (kv.E4M3[8:126] + kv.E4M3[9:127]) / 2         # half way between two codes
+
+
+@pytest.mark.parametrize("count", [1, 3])
+@pytest.mark.parametrize("seqs", [15, 100])               # the kernels of few and of many rows
+def test_older_codes_of_any_scale_are_rounded_once(seqs, count):
+    """A page's scale that is no power of two grows: older codes land next to the
+    middle between two codes, nearer to it than fp32 can tell."""
+    rng = np.random.default_rng(63)
+    code = rng.integers(32, 127, (seqs, 2))
+    middle = np.empty((seqs, 2))
+    for i in np.ndindex(seqs, 2):
+        r = MIDDLES / kv.E4M3[code[i]]
+        middle[i] = rng.choice(MIDDLES[(r > 0.3) & (r < 0.99)])
+    had = (middle / kv.E4M3[code]).astype(np.float32)
+    c = odd_scale(seqs, count, 63, lambda s, h: had[s, h],
+                  lambda s, h: np.where(rng.random((8, 64)) < 0.7, code[s, h],
+                                        rng.integers(0, 127, (8, 64))).astype(np.uint8),
+                  lambda s, h: np.full(64, 448.0))        # needs a scale of 1
+    c.upload()
+    c.append(None)
+    torch.cuda.synchronize()
+    kv.assert_append(c, None)
+    assert (c.dev["k_scale"].cpu().numpy()[c.table[:, 0]] == 1.0).all()
+
+
+@pytest.mark.parametrize("count", [1, 3])
+@pytest.mark.parametrize("seqs", [15, 100])
+def test_new_codes_of_any_scale_are_rounded_once(seqs, count):
+    """A page's scale that is no power of two stays: values next to the middle
+    between two codes after the division, and exactly there."""
+    rng = np.random.default_rng(64)
+    x = kv.bf16_values(rng.integers(0x3F80, 0x4080, (seqs, 2)).astype(np.uint16))      # 1 .. 4
+    middle = rng.choice(MIDDLES[(MIDDLES > 0.02) & (MIDDLES < 200)], (seqs, 2))
+    had = (x / middle).astype(np.float32)
+    for s in range(0, seqs, 3):                           # exact ties: 3 * middle is a bf16 number
+        had[s], x[s] = 3.0, 3 * middle[s]
+    c = odd_scale(seqs, count, 64, lambda s, h: had[s, h], lambda s, h: np.full((8, 64), 0x30, np.uint8),
+                  lambda s, h: x[s, h] * rng.choice([-1.0, 1.0, 0.5], 64))
+    c.upload()
+    c.append(None)
+    torch.cuda.synchronize()
+    kv.assert_append(c, None)
+    assert np.array_equal(c.dev["v_scale"].cpu().numpy()[c.table[:, 0]], had)
