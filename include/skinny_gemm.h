@@ -506,9 +506,10 @@ typedef struct skinny_kv_batch {
  * the larger of that and the scale the page has, and where it grows the
  * sequence's earlier codes in the page are rounded again to the new scale
  * (exact but for codes that become subnormal, unless the caller had set a scale
- * that is no power of two; that one is kept while it is large enough).  Codes are x / scale to nearest
- * even; infinities become the largest code and take no part in the scale, NaN
- * stays NaN.
+ * that is no power of two; that one is kept while it is large enough).  Codes are
+ * x / scale to nearest even; infinities, and values that the rotation takes past
+ * fp32's largest number, become the largest code and take no part in the scale,
+ * NaN stays NaN.
  *   Written are q_out's rows that belong to a sequence and the cache's slots of
  * their positions (and, as above, earlier codes in the same page), nothing
  * else: positions below 0 or past the page table have no slot.  A page that

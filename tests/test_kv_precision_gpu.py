@@ -188,3 +188,34 @@ def test_new_codes_of_any_scale_are_rounded_once(seqs, count):
     torch.cuda.synchronize()
     kv.assert_append(c, None)
     assert np.array_equal(c.dev["v_scale"].cpu().numpy()[c.table[:, 0]], had)
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "bf16"])
+@pytest.mark.parametrize("seqs", [1, 80])                 # the kernels of few and of many rows
+def test_rotations_past_the_largest_number(seqs, dtype):
+    """Two values of bf16's largest number turned by 3 pi / 4: one becomes 1.41
+    times that, which is an infinity like any other."""
+    freq = np.zeros(32, np.float32)
+    freq[5] = np.pi / 4
+    c = kv.Case([(1, 4)] * seqs, D=64, hq=2, hkv=1, dtype=dtype, seed=65)
+    x = c.qkv.reshape(c.T, 4, 64)
+    x[:, :3, 5] = x[:, :3, 37] = 0x7F7F
+    c.upload()
+    q = c.append(freq).float().cpu().double().numpy().reshape(c.T, 2, 64)
+    torch.cuda.synchronize()
+    assert (q[:, :, 5] == -np.inf).all() and np.isfinite(np.delete(q, 5, axis=2)).all()
+    k = kv.bf16_values(x[:, 2])
+    top = 0.0
+    for r in range(c.T):
+        turned = kv.rotate(k[r], 3, freq, False)
+        assert turned[5] < -np.finfo(np.float32).max
+        top = max(top, np.abs(np.delete(turned, 5)).max())
+    got = c.dev["k"].cpu().view(torch.int16 if dtype == "bf16" else torch.uint8).numpy()
+    got = got.astype(np.int64)[c.table[:, 0], 0, 3]
+    if dtype == "bf16":
+        assert (got[:, 5] & 0xFFFF == kv.BF16_INF | 0x8000).all()
+        return
+    assert (got[:, 5] == 0xFE).all()                      # -448
+    scale = c.dev["k_scale"].cpu().numpy()[c.table[:, 0], 0]
+    old = c.scales["k"][c.table[:, 0], 0]
+    assert np.array_equal(scale, np.maximum(old, np.float32(kv.pow2_scale(top))))
