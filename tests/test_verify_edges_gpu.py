@@ -8,7 +8,7 @@ import torch
 
 import gemv_skinny_gemm_amd as sg
 from tests.gpu_util import need_gpu
-from tests.test_verify_gpu import BELOW_ONE, case, compare, oracle, run, upload
+from tests.test_verify_gpu import BELOW_ONE, case, check, compare, oracle, run, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,65 @@ def test_a_wait_that_gives_up_says_so():
         run(d)
         torch.cuda.synchronize()
         compare(c, d)
+
+
+def check_rows(V, seed, **kw):
+    c = case([3, 2, 1, 1], V, "f32", seed=seed, temps=[0.9, 0.7, 1.0, 0.0], **kw)
+    check(c, what=f"{V}")
+    return c
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("V", [262144, 262145, 600001])
+def test_vocabularies_of_several_trips(V, draft):
+    """From 65 slices of 4096 entries on, a row's sums and a sequence's words take
+    more than one trip."""
+    c = check_rows(V, 50, draft=draft)
+    for su in (0.0, 0.5, BELOW_ONE):
+        c["sample_u"][:] = su
+        check(c, what=f"{V} {su}")
+        c["accept_u"][:] = 0.0 if su == 0.5 else BELOW_ONE
+        check(c, what=f"{V} {su}")
+
+
+@pytest.mark.parametrize("at", [0, 5, 262143, 262144, 400000, 524287, 524288, 600000])
+def test_every_trip_gives_its_entry(at):
+    """A flat row's entry at `at`; one that alone is above -inf, or infinite, there;
+    and an infinity each in two trips."""
+    V = 600001
+    c = case([1, 1, 1, 1], V, "f32", seed=51, draft=False)
+    l = c["logits"]
+    l[0] = 1.0
+    l[1] = -np.inf
+    l[1, at] = -4.0
+    l[2, at] = np.inf
+    l[3, [7, at]] = np.inf
+    c["sample_u"][:] = (at + 0.5) / V, 0.5, 0.5, 0.75
+    d = check(c)
+    assert d["out"].tolist() == [at, at, at, max(7, at)]
+
+
+def test_several_trips_without_a_residual():
+    """p = q, and a draft where both are 0: rejected, then drawn from p itself."""
+    c = case([2, 2, 2], 600001, "f32", seed=52, close=0.0)
+    for x in ("logits", "draft"):
+        c[x][[0, 2, 4], 17] = -np.inf
+    c["tokens"][[1, 3, 5]] = 17
+    for su in (0.0, 0.3, 0.999, BELOW_ONE):
+        c["sample_u"][:] = su
+        d = check(c, what=str(su))
+        assert d["accepted"].tolist() == [0, 0, 0]
+
+
+def test_the_largest_vocabulary():
+    c = case([1], 5, "f32", seed=53, draft=False)
+    V = 1 << 24
+    row = np.full((1, V), -np.inf, np.float32)
+    for at in (0, 9000000, V - 1):
+        row[:] = -np.inf
+        row[0, at] = 1.5
+        c["logits"] = row
+        d = upload(c)
+        run(d)
+        torch.cuda.synchronize()
+        assert d["out"].tolist() == [at] and d["accepted"].tolist() == [0]
