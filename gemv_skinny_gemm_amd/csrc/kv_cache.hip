@@ -377,6 +377,38 @@ __device__ __forceinline__ int touched(const Seq& q, int log2p, int& first) {
   return lo < hi ? ((hi - 1) >> log2p) - first + 1 : 0;
 }
 
+// The unit-th page that receives rows, sequences in order.
+struct NewRows {
+  int page;       // -1: there is none, or not in the pool
+  int lo;         // position of the first
+  int count;      // 1 .. page_tokens
+  int older;      // rows of the sequence before them in the page
+  size_t row;     // the first one's, in the batch
+};
+__device__ __forceinline__ NewRows find_page(const KvArgs& kv, int unit) {
+  const int lane = threadIdx.x & 63;
+  int s = -1, page_no = 0, before = 0;
+  for (int s0 = 0; s0 < kv.S && s < 0; s0 += 64) {
+    int first = 0, c = 0;
+    if (s0 + lane < kv.S) c = touched(load_seq(kv, s0 + lane), kv.log2p, first);
+    const int incl = add_count(wave_scan(c), before);
+    int idx;
+    const int at = scan_find(incl, before, unit, idx);
+    if (at >= 0) {
+      s = s0 + at;
+      page_no = lane_of(first, at) + idx;
+    }
+    before = lane_of(incl, 63);
+  }
+  if (s < 0) return NewRows{-1, 0, 0, 0, 0};
+  const Seq q = uniform(load_seq(kv, s));
+  const int lo = max(max(q.base, 0), page_no << kv.log2p);
+  const int hi = min(min(q.base + q.n, q.cap), (page_no + 1) << kv.log2p);
+  const int page = kv.table[(size_t)s * kv.max_pages + page_no];
+  return NewRows{page < kv.pages ? page : -1, lo, hi - lo, lo & ((1 << kv.log2p) - 1),
+                 (size_t)(q.q0 + (lo - q.base))};
+}
+
 // One workgroup per (page that receives rows, KV head, k or v), which alone
 // reads and writes that page's block and scale, then one per token and
 // kQHeadsPerBlock query heads.  The rotated rows wait in LDS (as fp32 rounded
@@ -425,35 +457,15 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_few(const AppendArg
 
   const bool is_v = blockIdx.x & 1;
   const int h = (blockIdx.x >> 1) % kv.kv_heads;
-  const int unit = (blockIdx.x >> 1) / kv.kv_heads;
-  // The unit-th page touched, sequences in order.
-  int s = -1, page_no = 0, before = 0;
-  for (int s0 = 0; s0 < kv.S && s < 0; s0 += 64) {
-    int first = 0, c = 0;
-    if (s0 + lane < kv.S) c = touched(load_seq(kv, s0 + lane), kv.log2p, first);
-    const int incl = add_count(wave_scan(c), before);
-    int idx;
-    const int at = scan_find(incl, before, unit, idx);
-    if (at >= 0) {
-      s = s0 + at;
-      page_no = lane_of(first, at) + idx;
-    }
-    before = lane_of(incl, 63);
-  }
-  if (s < 0) return;
-  const Seq q = uniform(load_seq(kv, s));
-  const int P = 1 << kv.log2p;
-  const int lo = max(max(q.base, 0), page_no << kv.log2p);
-  const int hi = min(min(q.base + q.n, q.cap), (page_no + 1) << kv.log2p);
-  const int count = hi - lo;                         // new rows, 1 .. P
-  const int older = lo & (P - 1);                    // rows of this sequence before them
-  const int page = kv.table[(size_t)s * kv.max_pages + page_no];
-  if (page < 0 || page >= kv.pages) return;
+  const NewRows fresh = find_page(kv, (blockIdx.x >> 1) / kv.kv_heads);
+  if (fresh.page < 0) return;
+  const int P = 1 << kv.log2p, lo = fresh.lo, count = fresh.count, older = fresh.older,
+            page = fresh.page;
   constexpr int kEsize = DT == kBF16 ? 2 : 1;
   unsigned char* block = (is_v ? kv.v : kv.k) + ((size_t)page * kv.kv_heads + h) * P * D * kEsize;
   const int rot = is_v ? 0 : a.rot;
   const unsigned* src = reinterpret_cast<const unsigned*>(
-      a.qkv + (size_t)(q.q0 + (lo - q.base)) * row_elems +
+      a.qkv + fresh.row * row_elems +
       (size_t)(a.q_heads + (is_v ? kv.kv_heads : 0) + h) * D);
 
   float top = 0.0f;
@@ -607,34 +619,14 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 
   const bool is_v = blockIdx.x & 1;
   const int h = (blockIdx.x >> 1) % kv.kv_heads;
-  const int unit = (blockIdx.x >> 1) / kv.kv_heads;
-  // The unit-th page touched, sequences in order.
-  int s = -1, page_no = 0, before = 0;
-  for (int s0 = 0; s0 < kv.S && s < 0; s0 += 64) {
-    int first = 0, c = 0;
-    if (s0 + lane < kv.S) c = touched(load_seq(kv, s0 + lane), kv.log2p, first);
-    const int incl = add_count(wave_scan(c), before);
-    int idx;
-    const int at = scan_find(incl, before, unit, idx);
-    if (at >= 0) {
-      s = s0 + at;
-      page_no = lane_of(first, at) + idx;
-    }
-    before = lane_of(incl, 63);
-  }
-  if (s < 0) return;
-  const Seq q = uniform(load_seq(kv, s));
-  const int P = 1 << kv.log2p;
-  const int lo = max(max(q.base, 0), page_no << kv.log2p);
-  const int hi = min(min(q.base + q.n, q.cap), (page_no + 1) << kv.log2p);
-  const int count = hi - lo;                         // new rows, 1 .. P
-  const int older = lo & (P - 1);                    // rows of this sequence before them
-  const int page = kv.table[(size_t)s * kv.max_pages + page_no];
-  if (page < 0 || page >= kv.pages) return;
+  const NewRows fresh = find_page(kv, (blockIdx.x >> 1) / kv.kv_heads);
+  if (fresh.page < 0) return;
+  const int P = 1 << kv.log2p, lo = fresh.lo, count = fresh.count, older = fresh.older,
+            page = fresh.page;
   constexpr int kEsize = DT == kBF16 ? 2 : 1;
   unsigned char* block = (is_v ? kv.v : kv.k) + ((size_t)page * kv.kv_heads + h) * P * D * kEsize;
   const int rot = is_v ? 0 : a.rot;
-  const __bf16* src = a.qkv + (size_t)(q.q0 + (lo - q.base)) * row_elems +
+  const __bf16* src = a.qkv + fresh.row * row_elems +
                       (size_t)(a.q_heads + (is_v ? kv.kv_heads : 0) + h) * D;
   float* scale = nullptr;
   float had = 0.0f;
