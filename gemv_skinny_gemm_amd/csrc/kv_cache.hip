@@ -798,7 +798,7 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 // spills).  One workgroup per CU, not two: 35.6 against 45.0 us there, 51.7
 // against 59.6 on the long sequence.
 
-constexpr int kMaxGroups = 512;          // workgroups of the grid at most
+constexpr int kMaxGroups = 256;          // workgroups of the grid, one per CU, at most
 constexpr size_t kSplitBytes = kMaxGroups * 32;
 constexpr float kNegInf = -__builtin_inff();
 // The maximum of a row that sees keys, but with scores of -inf (or NaN) only: lower
@@ -1748,8 +1748,6 @@ size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, i
   return kSplitBytes + (size_t)(2 * groups) * (16 * r.rt * r.rw) * (c.head_dim + 2) * sizeof(float);
 }
 
-constexpr int kGroupsPerCU = 1;
-
 // Whether a call's items stay whole, one workgroup each and no second launch: at
 // most four tiles and 32 KB of keys and values per wave by the page table's
 // width, and no more items than workgroups (or one tile, which has no parts).
@@ -1929,8 +1927,7 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   a.splits = (Split*)workspace;
   a.part = (float*)((unsigned char*)workspace + kSplitBytes);
   a.scale = scale * 1.44269504088896340736f;         // log2 e: the kernel's softmax is in exp2
-  long long groups = (long long)d.cus * kGroupsPerCU;
-  if (groups > kMaxGroups) groups = kMaxGroups;
+  long long groups = d.cus < kMaxGroups ? d.cus : kMaxGroups;
   const long long items = max_items(c, b, q_heads, r);
   a.whole = stays_whole(c, b, r, items, groups);
   const long long parts = a.whole ? items : work;
