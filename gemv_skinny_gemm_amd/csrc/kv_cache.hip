@@ -1898,7 +1898,8 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   if (st != SKINNY_OK) return st;
   const skinny_kv_cache& c = *cache;
   const skinny_kv_batch& b = *batch;
-  if (!q || !out || !(scale - scale == 0.0f)) return SKINNY_ERR_INVALID_ARG;
+  const float log2_scale = scale * 1.44269504088896340736f;   // the kernel's softmax is in exp2
+  if (!q || !out || !(log2_scale - log2_scale == 0.0f)) return SKINNY_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return SKINNY_ERR_UNSUPPORTED;
   const RowCut r = row_cut(c, b, q_heads);
   const long long work = max_work(c, b, q_heads, r);
@@ -1926,7 +1927,7 @@ skinny_status skinny_kv_attention(const skinny_kv_cache* cache, const skinny_kv_
   a.out = (__bf16*)out;
   a.splits = (Split*)workspace;
   a.part = (float*)((unsigned char*)workspace + kSplitBytes);
-  a.scale = scale * 1.44269504088896340736f;         // log2 e: the kernel's softmax is in exp2
+  a.scale = log2_scale;
   long long groups = d.cus < kMaxGroups ? d.cus : kMaxGroups;
   const long long items = max_items(c, b, q_heads, r);
   a.whole = stays_whole(c, b, r, items, groups);

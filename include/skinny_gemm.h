@@ -528,7 +528,7 @@ skinny_status skinny_kv_append(const skinny_kv_cache* cache, const skinny_kv_bat
  * over the positions j <= kv_len - n + i of row i, query head `head` reading KV
  * head head / (q_heads / kv_heads).
  *   q, out  [tokens][q_heads head_dim] bf16, 16-byte aligned; out is written
- *   scale   finite, usually 1 / sqrt(head_dim)
+ *   scale   usually 1 / sqrt(head_dim); finite, and times log2 e too
  * Scores, the softmax's statistics and sums are fp32; the probabilities go into
  * the product with v as two bf16 numbers each, within 2^-16.  Keys and values of positions that a
  * row does not see do not reach it, whatever they hold; an infinite value that

@@ -2,7 +2,7 @@
 call agree (no GPU; the addresses are never touched)."""
 import pytest
 
-from tests.test_kv_abi import UNSUPPORTED, WORKSPACE, attend, batch, cache
+from tests.test_kv_abi import INVALID, UNSUPPORTED, WORKSPACE, attend, batch, cache
 import gemv_skinny_gemm_amd as sg
 
 FAR = dict(q=1 << 44, out=2 << 44, ws=3 << 44)
@@ -37,3 +37,9 @@ def test_steps_below_the_stated_bound_have_one(seqs, tokens, kv_heads, q_heads, 
     n = sg.kv_attention_workspace_bytes(c, b, heads)
     assert n > 0
     assert attend(c=c, b=b, q_heads=heads, n=n - 1, **FAR) == WORKSPACE
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_scales_that_log2_e_takes_past_the_largest_number(scale):
+    assert attend(scale=scale) == INVALID
+    assert attend(scale=2.3e38, n=255) == WORKSPACE         # the next check
