@@ -775,7 +775,8 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 //
 // Short items stay whole, each in one workgroup (stays_whole).  Else the blocks
 // of 32 KW keys of all items, in order, are cut into equal shares, one per
-// workgroup (every workgroup computes the cut from the batch's device arrays); each wave takes an equal run of a segment's keys.  A segment that is
+// workgroup (every workgroup computes the cut from the batch's device arrays);
+// each wave takes an equal run of a segment's keys.  A segment that is
 // not a whole item leaves its m, l and O in the workspace, and a second launch
 // joins an item's segments in order: no atomics, so a result depends on the
 // lengths and the grid only.  (Joining in the first launch, by the last segment
@@ -784,19 +785,20 @@ __global__ __launch_bounds__(kThreads) void skinny_kv_append_many(const AppendAr
 // other waves stream through.)
 //
 // What bounds it, measured: long contexts the reads (bf16, 16 sequences, 64
-// query and 8 KV heads of 128: 538 MB of pages in 99.5 us = 5.4 TB/s, six
-// times the pages 6.3; e4m3, one sequence of 131072 keys: 51.7 us = 5.2 TB/s,
-// where 4 us are the second launch and about 5 the start and the waves' join);
-// a short call the chain start - page numbers - keys - join - second launch
-// (4000 keys under one KV head: 9.8 us, of which 3.3 the second launch).  Rows of
-// several tokens share the keys' bytes but not the work on them: 131072 keys under
-// 8, 16, 32, 48, 64 and 96 rows per KV head take 53, 53, 58, 75, 77 and 112 us (32
-// keys by 32 rows are 1700 to 2100 cycles of a wave's instructions), two sequences
-// of 12 verified tokens between them read 77 MB in 35 us.  Tried there and no
-// faster: three row tiles per wave with q in LDS (36.6 us), four row waves
-// (45.9), a second tile of keys and values in flight in registers (82; it
-// spills).  One workgroup per CU, not two: 35.6 against 45.0 us there, 51.7
-// against 59.6 on the long sequence.
+// query and 8 KV heads of 128: 538 MB of pages in 99.0 us = 5.4 TB/s, 2167 MB in
+// 346 = 6.3; e4m3, one sequence of 131072 keys: 51.8 us = 5.2 TB/s, where 4 us
+// are the second launch and about 5 the start and the waves' join); a short call
+// the chain start - page numbers - keys - join - second launch (4000 keys under
+// one KV head: 10.0 us, of which 3.2 the second launch).  Rows of several tokens
+// share the keys' bytes but not the work on them: 131072 keys under 8, 16, 32, 48,
+// 64 and 96 rows per KV head take 52, 53, 57, 78, 78 and 126 us (32 keys by 32 rows
+// are some 2000 cycles of a wave's instructions), two sequences of 12 verified
+// tokens between them read 77 MB in 38.6 us, prompts of 4099 rows in three sequences
+// of up to 9001 keys take 1364 us (504 TFLOP/s; bf16 3376, 204).  Tried on the two
+// sequences when a probability was one bf16 number, against 35.6 us then, and no
+// faster: three row tiles per wave with q in LDS (36.6 us), four row waves (45.9),
+// a second tile of keys and values in flight in registers (82; it spills), two
+// workgroups per CU (45.0; 59.6 against 51.7 on the long sequence).
 
 constexpr int kMaxGroups = 256;          // workgroups of the grid, one per CU, at most
 constexpr size_t kSplitBytes = kMaxGroups * 32;
@@ -1751,11 +1753,11 @@ size_t attention_workspace(const skinny_kv_cache& c, const skinny_kv_batch& b, i
 // Whether a call's items stay whole, one workgroup each and no second launch: at
 // most four tiles and 32 KB of keys and values per wave by the page table's
 // width, and no more items than workgroups (or one tile, which has no parts).
-// Whole against split, us: e4m3, 5 sequences, 32 heads on 8 of 64: 6.6 / 7.6 at
-// 256 keys, 8.3 / 9.4 at 777, 9.5 / 9.6 at 1500 (6 tiles: split), 11.9 / 9.6 at
-// 2048; bf16, 16 sequences, 64 on 8 of 128: 7.9 / 9.5 at 256, 11.2 / 12.4 at 512,
-// 13.6 / 12.6 at 777 (split); 48 such sequences, 384 items: 15.0 / 16.7 at 256 (one
-// tile), 19.7 / 17.7 at 512 (split).
+// Whole against split, us: e4m3, 5 sequences, 32 heads on 8 of 64: 6.2 / 7.7 at
+// 256 keys, 8.4 / 9.5 at 777, 10.3 / 9.8 at 1500 (6 tiles: split), 12.1 / 9.7 at
+// 2048; bf16, 16 sequences, 64 on 8 of 128: 8.7 / 10.4 at 256, 11.4 / 12.4 at 512,
+// 13.6 / 12.7 at 777 (split); 48 such sequences, 384 items: 15.1 / 16.7 at 256 (one
+// tile), 19.8 / 17.9 at 512 (split).
 constexpr int kWholeTiles = 4;
 constexpr int kWholeBytes = 32 * 1024;
 bool stays_whole(const skinny_kv_cache& c, const skinny_kv_batch& b, RowCut r, long long items,

@@ -33,11 +33,14 @@
 // their place cost about 8 us a call here (they write back and invalidate an
 // XCD's whole L2).
 //
-// What bounds it, measured: one exponential per logit in fp64 (11 FMA and some
-// ten instructions around them) in the first launch, instruction issue there, and
-// the latency of the second one's chain: 37 rows of 152064 bf16 logits with as
-// many of the draft's take 26.5 us (15.4 + 11.2), where reading them would take 3.
-// A few rows are the two launches' latency: 11.1 us for 2 rows of 32003, 14.1 for
+// What bounds it, measured on 37 rows of 152064 bf16 logits with as many of the
+// draft's: 26.0 us (15.0 + 11.4), where reading them would take 3.  The first launch
+// issues 30 vector instructions per logit (11 FMA of the exponential, the rest around
+// them), 18.4 thousand cycles per SIMD or 7.7 us at 2.4 GHz, and without the
+// exponentials takes 9.4: what is not issue is the launch and the chains of some
+// eleven workgroups per CU (row's sequence - logits - maximum - sum - join).  The
+// second one is the latency of its chain.  A few rows are the two launches' latency:
+// 11.0 us for 2 rows of 32003, 14.2 for
 // 6 of 152064.  Slices are 4096 entries, or 2048 where that makes at most 64 of a
 // row (what one trip of the second launch reads) and 1024 of all rows: 32003
 // entries 11.8 against 13.2 us at 4 rows, 13.5 against 14.2 at 32; beyond the
