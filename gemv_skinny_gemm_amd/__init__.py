@@ -25,6 +25,8 @@ __all__ = [
     "KV_BF16", "KV_FP8", "KvCache", "KvBatch", "make_kv_cache", "make_batch", "kv_append",
     "kv_attention", "kv_attention_workspace_bytes", "LOGITS_BF16", "LOGITS_F32", "Verify",
     "verify_draft", "verify_workspace_bytes", "verify_set_spin_limit",
+    "VALUES_BF16", "VALUES_F32", "NORM_RMS", "NORM_LAYER", "Norm", "block_norm", "Lora", "make_lora",
+    "lora_workspace_bytes", "lora_linear", "ROUTE_SOFTMAX", "ROUTE_SIGMOID", "Route", "moe_route",
 ]
 
 BF16 = 0
@@ -48,6 +50,13 @@ LOGITS_BF16 = 0
 LOGITS_F32 = 1
 KV_BF16 = 0
 KV_FP8 = 1
+VALUES_BF16 = 0
+VALUES_F32 = 1
+NORM_RMS = 0
+NORM_LAYER = 1
+ROUTE_SOFTMAX = 0
+ROUTE_SIGMOID = 1
+MAX_LORA_SLICES = 4
 MOE_MLP_COUNTER_BYTES = 256   # moe_mlp_swiglu's workspace: counter and flag, then gate_up outputs
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -109,6 +118,34 @@ class Verify(ctypes.Structure):
                 ("temperature", ctypes.c_void_p), ("accept_u", ctypes.c_void_p),
                 ("sample_u", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p),
                 ("accepted", ctypes.c_void_p)]
+
+
+class Norm(ctypes.Structure):
+    """struct skinny_norm"""
+    _fields_ = [(n, ctypes.c_int) for n in ("kind", "rows", "width", "routes", "residual_dtype",
+                                            "weight_dtype", "gate_rows", "reserved")] + \
+               [(n, ctypes.c_float) for n in ("eps", "residual_scale", "block_scale",
+                                              "weight_offset")] + \
+               [(n, ctypes.c_void_p) for n in ("block", "route_weights", "post_weight", "post_bias",
+                                               "gate", "residual", "residual_out", "weight", "bias",
+                                               "out")]
+
+
+class Lora(ctypes.Structure):
+    """struct skinny_lora"""
+    _fields_ = [("adapters", ctypes.c_int), ("rank", ctypes.c_int), ("K", ctypes.c_int),
+                ("slices", ctypes.c_int), ("n", ctypes.c_int * MAX_LORA_SLICES),
+                ("a", ctypes.c_void_p * MAX_LORA_SLICES), ("b", ctypes.c_void_p * MAX_LORA_SLICES),
+                ("ranks", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+    gpu = None                 # of the tensors that make_lora was given
+
+
+class Route(ctypes.Structure):
+    """struct skinny_route"""
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "scoring", "rows", "experts", "topk", "groups",
+                                            "top_groups", "renormalize")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int)] + \
+               [(n, ctypes.c_void_p) for n in ("logits", "bias", "ids", "weights")]
 
 
 class Plan(ctypes.Structure):
@@ -198,6 +235,14 @@ def _bind(path: str):
     L.skinny_verify_draft.argtypes = [ctypes.POINTER(Verify), vp, sz, vp]
     L.skinny_verify_set_spin_limit.restype = None
     L.skinny_verify_set_spin_limit.argtypes = [ctypes.c_longlong]
+    L.skinny_block_norm.restype = i
+    L.skinny_block_norm.argtypes = [ctypes.POINTER(Norm), vp]
+    L.skinny_lora_workspace_bytes.restype = sz
+    L.skinny_lora_workspace_bytes.argtypes = [ctypes.POINTER(Lora), i]
+    L.skinny_lora_linear.restype = i
+    L.skinny_lora_linear.argtypes = [ctypes.POINTER(Lora), vp, vp, i, vp, vp, vp, sz, vp]
+    L.skinny_moe_route.restype = i
+    L.skinny_moe_route.argtypes = [ctypes.POINTER(Route), vp]
     L.skinny_status_string.restype = ctypes.c_char_p
     L.skinny_status_string.argtypes = [i]
     L.skinny_abi_version.restype = i
@@ -816,3 +861,147 @@ def verify_set_spin_limit(polls: int) -> None:
     """Polls before a sampling sequence's wait for another workgroup's sums gives
     up (< 0: it does not wait); for tests of that path."""
     lib().skinny_verify_set_spin_limit(int(polls))
+
+
+def _values(t, tt, what) -> int:
+    """VALUES_BF16 or VALUES_F32 of a tensor."""
+    if t.dtype is tt.bf16:
+        return VALUES_BF16
+    if t.dtype is not tt.f32:
+        _need(t, t.shape, _BF16 | _F32, what)
+    return VALUES_F32
+
+
+def block_norm(out, weight, residual=None, block=None, residual_out=None, bias=None,
+               post_weight=None, post_bias=None, gate=None, route_weights=None,
+               kind: int = NORM_RMS, eps: float = 1e-6, residual_scale: float = 1.0,
+               block_scale: float = 1.0, weight_offset: float = 0.0, stream=None):
+    """h = residual_scale * residual + block_scale * gate * norm(block) into
+    residual_out, and norm(h) * weight + bias into out [rows][width] bf16, the
+    next linear's x.  block [rows * routes][width] bf16 is a linear's y, or the
+    experts' routes, summed with route_weights float32 [rows][routes]; its norm is
+    taken only with a post_weight.  residual and residual_out (which may be the
+    same tensor) are bf16 or float32; weights and biases [width], and gate
+    [width] or [rows][width], are all bf16 or all float32, weights counting as
+    weight_offset + weight.  What is None takes no part; out None only updates
+    the residual."""
+    first = out if out is not None else residual_out
+    if first is None:
+        raise ValueError("one of out and residual_out is needed")
+    tt, dev = _call_device(first)
+    rows, width = _shape2(first)
+    shape, one = (rows, width), (width,)
+    y = None if out is None else _operand(out, shape, tt.bf16, "out", dev)
+    rt, routes, gate_rows, wt = VALUES_BF16, 1, 0, None
+    h = r = b = rw = g = None
+    if residual is not None:
+        rt = _values(residual, tt, "residual")
+        h = _operand(residual, shape, residual.dtype, "residual", dev)
+    if residual_out is not None:
+        kept = residual_out if residual is None else residual
+        rt = _values(kept, tt, "residual_out")
+        r = _operand(residual_out, shape, kept.dtype, "residual_out", dev)
+    if block is not None:
+        if route_weights is not None:
+            routes = _shape2(route_weights)[1]
+            rw = _operand(route_weights, (rows, routes), tt.f32, "route_weights", dev)
+        elif rows:
+            routes = max(1, block.shape[0] // rows)
+        b = _operand(block, (rows * routes, width), tt.bf16, "block", dev)
+    elif route_weights is not None or gate is not None or post_weight is not None:
+        raise ValueError("route_weights, gate and post_weight need a block")
+    vectors = []
+    for t, what in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"),
+                    (post_bias, "post_bias")):
+        if t is None:
+            vectors.append(None)
+            continue
+        wt = t.dtype if wt is None else wt
+        vectors.append(_operand(t, one, wt, what, dev))
+    if gate is not None:
+        wt = gate.dtype if wt is None else wt
+        gate_rows = int(gate.dim() == 2)
+        g = _operand(gate, shape if gate_rows else one, wt, "gate", dev)
+    for t in (weight, bias, post_weight, post_bias, gate):
+        if t is not None:
+            _values(t, tt, "weight")
+    w, wb, pw, pb = vectors
+    n = Norm(kind, rows, width, routes, rt, VALUES_F32 if wt is tt.f32 else VALUES_BF16, gate_rows, 0,
+             eps, residual_scale, block_scale, weight_offset, b, rw, pw, pb, g, h, r, w, wb, y)
+    _check(lib().skinny_block_norm(n, _call_stream(tt, dev, stream)), "skinny_block_norm")
+    return out if out is not None else residual_out
+
+
+def make_lora(a, b, scale=None, ranks=None) -> Lora:
+    """A skinny_lora from lists of GPU tensors a [adapters][rank][K] and b
+    [adapters][n][rank], bf16, one of each per slice of the projection (or one
+    tensor each for a projection of one); a slice without adapters has None in a
+    and its width in b.  scale float32 and ranks int32 [adapters]."""
+    a, b = ([t] if not isinstance(t, (list, tuple)) else list(t) for t in (a, b))
+    if len(a) != len(b) or not 1 <= len(a) <= MAX_LORA_SLICES:
+        raise ValueError(f"a and b need the same number of slices, 1 to {MAX_LORA_SLICES}")
+    used = [t for t in a if t is not None]
+    if not used or any(t.dim() != 3 for t in used):
+        raise ValueError("a must be 3-D tensors [adapters][rank][K], and one at least")
+    E, R, K = (int(v) for v in used[0].shape)
+    for i, (p, q) in enumerate(zip(a, b)):
+        if p is None:
+            if not isinstance(q, int):
+                raise ValueError(f"b[{i}] must be the width of a slice without adapters")
+            continue
+        _need(p, (E, R, K), _BF16, f"a[{i}]")
+        if isinstance(q, int) or q is None or q.dim() != 3:
+            raise ValueError(f"b[{i}] must be a 3-D tensor [adapters][n][rank]")
+        _need(q, (E, int(q.shape[1]), R), _BF16, f"b[{i}]")
+    _need(ranks, (E,), _I32, "ranks")
+    _need(scale, (E,), _F32, "scale")
+    lora = Lora(E, R, K, len(a))
+    for i, (p, q) in enumerate(zip(a, b)):
+        lora.n[i] = q if p is None else int(q.shape[1])
+        if p is not None:
+            lora.a[i], lora.b[i] = _ptr(p), _ptr(q)
+    lora.ranks, lora.scale = _ptr(ranks), _ptr(scale)
+    kept = [t for t in (*a, *b, ranks, scale) if t is not None and not isinstance(t, int)]
+    lora.width = sum(lora.n[:len(a)])
+    return _one_gpu(lora, *kept)
+
+
+def lora_workspace_bytes(lora: Lora, rows: int) -> int:
+    return lib().skinny_lora_workspace_bytes(lora, rows)
+
+
+def lora_linear(lora: Lora, x, ids, y, workspace, base=None, stream=None):
+    """y[t] = base[t] + scale[e] * B_e (A_e x[t]) for e = ids[t] (int32 [rows] on
+    the GPU; rows with an id that is no adapter's keep base): x [rows][K] and y
+    [rows][sum of the slices' n] bf16.  base None adds to y in place."""
+    tt, dev = _call_device(x)
+    rows = x.shape[0]
+    xp = _operand(x, (rows, lora.K), tt.bf16, "x", dev)
+    ip = _operand(ids, (rows,), tt.i32, "ids", dev)
+    shape = (rows, lora.width)
+    yp = _operand(y, shape, tt.bf16, "y", dev)
+    bp = None if base is None else _operand(base, shape, tt.bf16, "base", dev)
+    wp, wb = _space(workspace, dev)
+    if lora.gpu not in (None, dev) and dev >= 0:
+        raise ValueError(f"lora on GPU {lora.gpu}, the call's tensors on GPU {dev}")
+    _check(lib().skinny_lora_linear(lora, xp, ip, rows, bp, yp, wp, wb,
+                                    _call_stream(tt, dev, stream)), "skinny_lora_linear")
+    return y
+
+
+def moe_route(logits, ids, weights, scoring: int = ROUTE_SOFTMAX, bias=None, groups: int = 1,
+              top_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """The topk experts of each row of logits [rows][experts] (bf16 or float32)
+    into ids int32 [rows][topk], for moe_linear and moe_mlp_swiglu, and their
+    weights into weights float32 [rows][topk], for block_norm's sum of the routes."""
+    tt, dev = _call_device(logits)
+    rows, experts = _shape2(logits)
+    kind = _values(logits, tt, "logits")
+    topk = _shape2(ids)[1]
+    r = Route(kind, scoring, rows, experts, topk, groups, top_groups, int(renormalize), scale, 0,
+              _operand(logits, (rows, experts), logits.dtype, "logits", dev),
+              None if bias is None else _operand(bias, (experts,), tt.f32, "bias", dev),
+              _operand(ids, (rows, topk), tt.i32, "ids", dev),
+              _operand(weights, (rows, topk), tt.f32, "weights", dev))
+    _check(lib().skinny_moe_route(r, _call_stream(tt, dev, stream)), "skinny_moe_route")
+    return ids

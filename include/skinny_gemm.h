@@ -619,6 +619,161 @@ skinny_status skinny_verify_draft(const skinny_verify* verify, void* workspace,
  * when a call is enqueued.  For tests of that path. */
 void skinny_verify_set_spin_limit(long long polls);
 
+/* ------------------------------------------------------------------------
+ * What a layer computes between and beside its linears.  Values of two types
+ * share one enum; arrays need the alignment of their type only. */
+enum skinny_values_dtype { SKINNY_VALUES_BF16 = 0, SKINNY_VALUES_F32 = 1 };
+
+/* The residual's update with a block's output, and the norm that makes the next
+ * linear's x, for every row t of a step (each layer's attention and MLP blocks
+ * add to the residual between their linears: "Developing a custom Qwen2.5 72B
+ * inference engine from scratch - what is the real bottleneck?", section 3):
+ *   b  = sum_j route_weights[t][j] * block[t * routes + j]
+ *   b  = norm(b) * (weight_offset + post_weight) + post_bias    (post_weight given)
+ *   b  = gate * b                                               (gate given)
+ *   h  = residual_scale * residual[t] + block_scale * b
+ *   residual_out[t] = h
+ *   out[t] = norm(h) * (weight_offset + weight) + bias
+ *   norm(v) = v / sqrt(mean(v^2) + eps)                         SKINNY_NORM_RMS
+ *           = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) SKINNY_NORM_LAYER
+ * What is NULL takes no part: no block (b = 0), no residual (h = block_scale * b),
+ * weights of norm(h) and route_weights 1, biases 0; residual_out or out NULL: not
+ * written.  One of block and residual, and one of residual_out and out, are needed;
+ * post_weight, post_bias, gate and route_weights need a block, post_bias a
+ * post_weight, bias an out.
+ *   block         [rows * routes][width] bf16: the O linear's, mlp_swiglu's (routes
+ *                 1) or moe_mlp_swiglu's y; routes 1 .. SKINNY_MAX_TOPK
+ *   route_weights [rows][routes] fp32
+ *   residual, residual_out  [rows][width] of residual_dtype; residual_out may be
+ *                 residual itself (same address), and overlaps nothing else
+ *   gate          [width], or [rows][width] with gate_rows = 1; weights, biases
+ *                 [width]; all of weight_dtype
+ *   out           [rows][width] bf16, overlaps nothing else
+ * Values are fp32 from the load on (out is made of h before residual_out's
+ * rounding), means and sums of squares fp64, so they neither overflow nor vanish;
+ * outputs are rounded once, to nearest even.  A value or sum that passes fp32's
+ * largest number is infinite.  A row whose mean of squares plus eps is 0 gives NaN
+ * (0 / 0); a row with a NaN or an infinity does not touch other rows.
+ * Bitwise reproducible.  No workspace; one launch.  reserved must be 0; eps >= 0
+ * and finite, the scales and the offset finite. */
+enum skinny_norm_kind { SKINNY_NORM_RMS = 0, SKINNY_NORM_LAYER = 1 };
+#define SKINNY_NORM_MAX_ROWS 1048576
+#define SKINNY_NORM_MAX_WIDTH 32768
+typedef struct skinny_norm {
+  int kind;             /* enum skinny_norm_kind          */
+  int rows;             /* 1 .. SKINNY_NORM_MAX_ROWS      */
+  int width;            /* 1 .. SKINNY_NORM_MAX_WIDTH     */
+  int routes;           /* 1 .. SKINNY_MAX_TOPK           */
+  int residual_dtype;   /* enum skinny_values_dtype       */
+  int weight_dtype;     /* enum skinny_values_dtype       */
+  int gate_rows;        /* 0 or 1                         */
+  int reserved;
+  float eps;
+  float residual_scale;
+  float block_scale;
+  float weight_offset;
+  const void* block;
+  const float* route_weights;
+  const void* post_weight;
+  const void* post_bias;
+  const void* gate;
+  const void* residual;
+  void* residual_out;
+  const void* weight;
+  const void* bias;
+  void* out;
+} skinny_norm;
+skinny_status skinny_block_norm(const skinny_norm* norm, void* stream);
+
+/* The low-rank adapters of many requests beside a shared projection ("Multi-GPU
+ * Inference and Serving at Scale", Example 15: several adapters over one model's
+ * weights).  Row t has adapter e = ids[t]:
+ *   y[t] = base[t] + scale[e] * B_e (A_e x[t]),
+ * and y[t] = base[t] for every t whose e is outside [0, adapters).  A projection
+ * of several parts (q, k and v; gate and up) has an A and a B for each: slice i
+ * covers the n[i] columns of y behind those of the slices before it.
+ *   x         [rows][K] bf16, the projection's x; K % 8 == 0, 16-byte aligned
+ *   base, y   [rows][N] bf16, N = n[0] + .. + n[slices - 1]: the projection's y and
+ *             the result; base NULL: y itself (added in place; rows without an
+ *             adapter are then left as they were); base overlaps y in no other way
+ *   a[i]      [adapters][rank][K] bf16, b[i] [adapters][n[i]][rank] bf16, 16-byte
+ *             aligned; both NULL: a slice without adapters
+ *   rank      of the pool, a multiple of 8 up to SKINNY_LORA_MAX_RANK
+ *   ranks     [adapters] int32 or NULL: adapter e uses its first ranks[e] (cut to
+ *             0 .. rank) rows of A and columns of B; the others are not used,
+ *             whatever they hold
+ *   scale     [adapters] fp32, or NULL: 1
+ *   ids       [rows] int32, device, read by the kernels; any values
+ * Each adapter's weights are read once for all of its rows among 64 neighbouring
+ * ones.  Sums are fp32; A x, as fp32, enters the product with B as two bf16 numbers, within
+ * 2^-16; y is rounded once.  A row's result does not depend on the other rows'
+ * values; results are bitwise reproducible for the same sizes.
+ *   workspace >= skinny_lora_workspace_bytes(lora, rows) bytes (0 for invalid
+ *             arguments), 16-byte aligned, contents undefined before and after, so
+ *             calls that may overlap need their own
+ * y and the workspace must not overlap anything else. */
+#define SKINNY_LORA_MAX_ROWS 1048576
+#define SKINNY_LORA_MAX_RANK 256
+#define SKINNY_LORA_MAX_SLICES 4
+typedef struct skinny_lora {
+  int adapters;         /* 1 .. 65536                     */
+  int rank;             /* 8 .. SKINNY_LORA_MAX_RANK      */
+  int K;
+  int slices;           /* 1 .. SKINNY_LORA_MAX_SLICES    */
+  int n[SKINNY_LORA_MAX_SLICES];
+  const void* a[SKINNY_LORA_MAX_SLICES];
+  const void* b[SKINNY_LORA_MAX_SLICES];
+  const int* ranks;
+  const float* scale;
+} skinny_lora;
+size_t skinny_lora_workspace_bytes(const skinny_lora* lora, int rows);
+skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const int* ids, int rows,
+                                 const void* base, void* y, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* A router's choice: the ids that skinny_moe_linear and skinny_moe_mlp_swiglu
+ * take, and the weights with which skinny_block_norm sums their outputs ("Multi-GPU
+ * Inference and Serving at Scale", Example 8: each token goes to its top experts).
+ * For row t with logits l:
+ *   s = softmax(l), or 1 / (1 + e^-l) with SKINNY_ROUTE_SIGMOID
+ *   c = s + bias (bias [experts] fp32; only the choice sees it); without a bias
+ *       the choice goes by l itself, whose order s shares
+ *   with groups > 1, the experts are `groups` equal runs; those of the top_groups
+ *       best groups are chosen from, a group being worth its largest c (with a
+ *       bias the sum of its two largest)
+ *   ids[t]     = the topk largest c, descending; equal ones (and groups) by the lowest
+ *                index
+ *   weights[t] = scale * s[ids], over their sum first with renormalize = 1 (where
+ *                that sum is 0, they are 0)
+ * A NaN logit counts as -inf, +inf as fp32's largest number.  A row of -inf alone
+ * has s = 0.  A c or a sum of two that is NaN (by its bias) counts as -inf.
+ * s, c and sums are fp64; weights are rounded once.
+ *   logits  [rows][experts] bf16 or fp32;  ids [rows][topk] int32 and weights
+ *           [rows][topk] fp32, written, neither overlapping anything else
+ * experts % groups == 0, topk <= top_groups * (experts / groups).  No workspace;
+ * one launch.  reserved must be 0; scale finite. */
+enum skinny_route_scoring { SKINNY_ROUTE_SOFTMAX = 0, SKINNY_ROUTE_SIGMOID = 1 };
+#define SKINNY_ROUTE_MAX_ROWS 1048576
+#define SKINNY_ROUTE_MAX_EXPERTS 1024
+#define SKINNY_ROUTE_MAX_GROUPS 64
+typedef struct skinny_route {
+  int dtype;            /* enum skinny_values_dtype, of the logits */
+  int scoring;          /* enum skinny_route_scoring               */
+  int rows;             /* 1 .. SKINNY_ROUTE_MAX_ROWS              */
+  int experts;          /* 1 .. SKINNY_ROUTE_MAX_EXPERTS           */
+  int topk;             /* 1 .. SKINNY_MAX_TOPK                    */
+  int groups;           /* 1 .. SKINNY_ROUTE_MAX_GROUPS            */
+  int top_groups;       /* 1 .. groups                             */
+  int renormalize;      /* 0 or 1                                  */
+  float scale;
+  int reserved;
+  const void* logits;
+  const float* bias;
+  int* ids;
+  float* weights;
+} skinny_route;
+skinny_status skinny_moe_route(const skinny_route* route, void* stream);
+
 /* Static text for a status code; never NULL. */
 const char* skinny_status_string(int status);
 

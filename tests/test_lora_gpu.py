@@ -1,0 +1,179 @@
+"""lora_linear against its 64-bit form: whole numbers, whose sums hold no
+rounding, bitwise; other values within what fp32 sums leave."""
+import numpy as np
+import pytest
+import torch
+
+import gemv_skinny_gemm_amd as sg
+from tests import layer_util as lu
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF, NAN = torch.bfloat16, float("nan")
+
+
+class Call:
+    def __init__(self, rows, K, n, adapters, rank, ids=None, ranks=None, scaled=True, whole=False,
+                 bare=(), seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def rnd(*s, most=2, k=1.0):
+            if whole:
+                return torch.randint(-most, most + 1, s, generator=g, device="cuda").to(BF)
+            return (k * torch.randn(*s, generator=g, device="cuda")).to(BF)
+
+        self.rows, self.N = rows, sum(n)
+        self.x, self.base = rnd(rows, K), rnd(rows, sum(n), most=100)
+        self.a = [None if i in bare else rnd(adapters, rank, K, k=K ** -0.5) for i in range(len(n))]
+        self.b = [w if i in bare else rnd(adapters, w, rank) for i, w in enumerate(n)]
+        if ids is None:
+            ids = torch.randint(-1, adapters, (rows,), generator=g, device="cuda")
+        self.ids = torch.as_tensor(ids, device="cuda").to(torch.int32)
+        self.ranks = None if ranks is None else torch.tensor(ranks, dtype=torch.int32, device="cuda")
+        self.scale = None
+        if scaled:
+            self.scale = torch.randint(-2, 3, (adapters,), generator=g, device="cuda").float() if whole \
+                else torch.randn(adapters, generator=g, device="cuda")
+        self.lora = sg.make_lora(self.a, self.b, scale=self.scale, ranks=self.ranks)
+        self.ws = torch.full((sg.lora_workspace_bytes(self.lora, rows),), 0xFF, dtype=torch.uint8,
+                             device="cuda")
+
+    def want(self):
+        part = lambda v: v if v is None or isinstance(v, int) else lu.host(v)
+        return lu.lora(lu.host(self.x), self.ids.tolist(), lu.host(self.base),
+                       [part(v) for v in self.a], [part(v) for v in self.b],
+                       None if self.ranks is None else self.ranks.tolist(), lu.host(self.scale))
+
+    def run(self, in_place=False):
+        guard = 40
+        y = torch.full((self.rows * self.N + 2 * guard,), 7.0, dtype=BF, device="cuda")
+        inner = y[guard:guard + self.rows * self.N].view(self.rows, self.N)
+        if in_place:
+            inner.copy_(self.base)
+        else:
+            inner.fill_(NAN)
+        sg.lora_linear(self.lora, self.x, self.ids, inner, self.ws,
+                       base=None if in_place else self.base)
+        torch.cuda.synchronize()
+        assert (y[:guard] == 7).all() and (y[guard + self.rows * self.N:] == 7).all()
+        return inner
+
+    def check(self, whole=False):
+        want, bound = self.want()
+        for in_place in (False, True):
+            got = self.run(in_place)
+            if whole:                  # every sum is a whole number below 2^24
+                rounded = torch.from_numpy(want).to(torch.float32).to(BF)
+                assert np.abs(want).max() < 2 ** 24
+                assert torch.equal(got.cpu(), rounded)
+            else:
+                lu.near(lu.values(got), want, bound)
+        return got
+
+
+SIZES = [
+    (1, 8, [1], 1, 8), (1, 8192, [1024], 3, 16), (2, 64, [64], 2, 8), (3, 72, [65], 2, 24),
+    (16, 1000, [256, 100, 31], 5, 32), (17, 520, [257], 1, 64), (33, 128, [300], 40, 40),
+    (64, 256, [70], 64, 16), (65, 256, [70, 3], 3, 72), (200, 328, [513], 9, 128),
+    (300, 64, [40], 2, 256), (1000, 136, [96, 17], 70, 8), (2500, 72, [130], 4, 48),
+]
+
+
+@pytest.mark.parametrize("rows,K,n,adapters,rank", SIZES)
+def test_whole_numbers(rows, K, n, adapters, rank):
+    need_gpu()
+    Call(rows, K, n, adapters, rank, whole=True, seed=rows).check(whole=True)
+
+
+@pytest.mark.parametrize("rows,K,n,adapters,rank", SIZES)
+def test_values(rows, K, n, adapters, rank):
+    need_gpu()
+    ranks = [(7 * e + 3) % (rank + 1) for e in range(adapters)]
+    Call(rows, K, n, adapters, rank, seed=rows).check()
+    Call(rows, K, n, adapters, rank, ranks=ranks, scaled=False, seed=rows + 1).check()
+
+
+def test_ranks_hide_what_is_behind_them():
+    need_gpu()
+    ranks = [0, 1, 15, 16, 17, 40, 99, -3]
+    c = Call(50, 136, [90, 33], 8, 40, ranks=ranks, whole=True)
+    for e, r in enumerate(ranks):
+        r = min(max(r, 0), 40)
+        for a, b in zip(c.a, c.b):
+            a[e, r:] = NAN
+            b[e, :, r:] = float("inf")
+    c.check(whole=True)
+
+
+def test_slices_without_adapters():
+    need_gpu()
+    for bare in ((0,), (1,), (2,), (0, 2), (1, 2)):
+        for rows in (3, 90):
+            Call(rows, 64, [33, 300, 8], 4, 16, whole=True, bare=bare).check(whole=True)
+
+
+@pytest.mark.parametrize("ids", [[-1] * 70, [9, -5, 1 << 30, -(1 << 31)] * 20, [0] * 130,
+                                 list(range(3)) * 22, [2] * 15 + [-1] * 34 + [1] * 81])
+def test_ids(ids):
+    need_gpu()
+    Call(len(ids), 128, [100], 3, 16, ids=ids, whole=True).check(whole=True)
+
+
+def test_values_that_are_no_numbers_stay_in_their_row():
+    need_gpu()
+    c = Call(40, 128, [70], 3, 16, whole=True)
+    c.ids.copy_(torch.arange(40) % 4 - 1)
+    c.x[5, 3], c.x[6, 127], c.base[9, 0] = NAN, float("inf"), NAN
+    c.scale.fill_(1.0)
+    c.a[0][:, :, 127] = 1.0
+    c.b[0][c.b[0] == 0] = 1.0
+    c.b[0][:, :35].abs_()
+    rows = [t for t in range(40) if t not in (5, 6)]
+    want = torch.from_numpy(c.want()[0]).to(torch.float32).to(BF)
+    got = c.run().cpu()
+    same = (got[rows] == want[rows]) | (got[rows].isnan() & want[rows].isnan())
+    assert same.all() and got[5].isnan().all()
+    # An infinite A x gives infinities where B has one sign, NaN where both meet.
+    infinite = want[6].isinf()
+    assert infinite[:35].all()
+    assert torch.equal(got[6][infinite], want[6][infinite])
+
+
+def test_largest_numbers():
+    """A x beyond bf16's largest number and within fp32's keeps its value."""
+    need_gpu()
+    c = Call(4, 64, [16], 1, 8, ids=[0] * 4, scaled=False, whole=True)
+    top = float(torch.finfo(torch.float32).max)
+    c.x.zero_()
+    c.a[0].zero_()
+    c.x[:, 0], c.x[:, 1] = 2.0 ** 64, 2.0 ** 64
+    c.a[0][0, :, 0], c.a[0][0, :, 1] = 2.0 ** 63, 2.0 ** 62 * 1.9921875     # sum below 2^128
+    c.b[0].zero_()
+    c.b[0][0, :, 0] = 2.0 ** -100
+    v = 2.0 ** 127 + 2.0 ** 126 * 1.9921875
+    assert float(torch.finfo(BF).max) < v < top
+    c.base.zero_()
+    got = c.run()
+    want = torch.full_like(c.base, v * 2.0 ** -100)
+    assert torch.equal(got, want)
+
+
+def test_long_offsets():
+    """More than 2^31 values of y."""
+    need_gpu()
+    rows, N = 110000, 20001
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").to(BF)
+    x, a, b = ints(rows, 8), ints(2, 8, 8), ints(2, N, 8)
+    ids = torch.randint(-1, 2, (rows,), generator=g, device="cuda").to(torch.int32)
+    y = torch.ones(rows, N, dtype=BF, device="cuda")
+    lora = sg.make_lora(a, b)
+    ws = torch.empty(sg.lora_workspace_bytes(lora, rows), dtype=torch.uint8, device="cuda")
+    sg.lora_linear(lora, x, ids, y, ws)
+    for t in (0, 1, 53687, 107368, 107369, rows - 2, rows - 1):
+        e = int(ids[t])
+        want = torch.ones(N, device="cuda")
+        if e >= 0:
+            want = want + b[e].float() @ (a[e].float() @ x[t].float())
+        assert torch.equal(y[t], want.to(BF))
