@@ -38,9 +38,9 @@ struct NormArgs {
   __bf16* out;
   int rows, width, routes;
   int layer;                           // SKINNY_NORM_LAYER
-  int residual_f32, weight_f32, gate_rows;
+  int gate_rows;
   float residual_scale, block_scale, weight_offset;
-  double eps;
+  double eps, inv_width;
 };
 
 __device__ __forceinline__ float bf16_lo(unsigned u) { return __builtin_bit_cast(float, u << 16); }
@@ -52,67 +52,71 @@ __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
   return __builtin_bit_cast(unsigned, bf16x2{(__bf16)a, (__bf16)b});
 }
 
-// Values i .. i + 7 of an array, zeros from `width` on.
-__device__ __forceinline__ void load_bf16(const __bf16* p, int i, int width, float (&v)[kUnit]) {
-  if (i + kUnit <= width) {
-    const u32x4 x = *reinterpret_cast<const u32x4_any*>(p + i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = bf16_lo(x[e]);
-      v[2 * e + 1] = bf16_hi(x[e]);
+// A unit as it lies in memory, and its values.
+template <bool F32>
+struct Raw {
+  u32x4 x[F32 ? 2 : 1];
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (F32) {
+      const unsigned u = x[e / 4][e % 4];
+      return __builtin_bit_cast(float, u);
+    } else {
+      const unsigned u = x[0][e / 2];
+      return e % 2 ? bf16_hi(u) : bf16_lo(u);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kUnit; ++e) v[e] = i + e < width ? (float)p[i + e] : 0.0f;
   }
-}
-__device__ __forceinline__ void load_f32(const float* p, int i, int width, float (&v)[kUnit]) {
-  if (i + kUnit <= width) {
-    const u32x4 x = *reinterpret_cast<const u32x4_any4*>(p + i);
-    const u32x4 y = *reinterpret_cast<const u32x4_any4*>(p + i + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned a = x[e], b = y[e];
-      v[e] = __builtin_bit_cast(float, a);
-      v[4 + e] = __builtin_bit_cast(float, b);
-    }
+};
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load(const void* p, size_t at) {
+  Raw<F32> r;
+  if constexpr (F32) {
+    const float* q = (const float*)p + at;
+    r.x[0] = *reinterpret_cast<const u32x4_any4*>(q);
+    r.x[1] = *reinterpret_cast<const u32x4_any4*>(q + 4);
   } else {
-#pragma unroll
-    for (int e = 0; e < kUnit; ++e) v[e] = i + e < width ? p[i + e] : 0.0f;
+    r.x[0] = *reinterpret_cast<const u32x4_any*>((const __bf16*)p + at);
   }
+  return r;
 }
-__device__ __forceinline__ void load(const void* p, int f32, size_t at, int i, int width,
-                                     float (&v)[kUnit]) {
-  if (f32) load_f32((const float*)p + at, i, width, v);
-  else load_bf16((const __bf16*)p + at, i, width, v);
+// Rows of fewer values than a unit: lane 0 has them all.
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_few(const void* p, size_t at, int width) {
+  Raw<F32> r{};
+#pragma unroll
+  for (int e = 0; e < kUnit; ++e) {
+    if (e >= width) continue;
+    if constexpr (F32) r.x[e / 4][e % 4] = __builtin_bit_cast(unsigned, ((const float*)p)[at + e]);
+    else r.x[0][e / 2] |= (unsigned)((const unsigned short*)p)[at + e] << (16 * (e % 2));
+  }
+  return r;
 }
 
-__device__ __forceinline__ void store_bf16(__bf16* p, int i, int width, const float (&v)[kUnit]) {
-  if (i + kUnit <= width) {
-    u32x4 x;
+// Values from `skip` up to `end` of a unit.
+template <bool F32>
+__device__ __forceinline__ void store(void* p, size_t at, const float (&v)[kUnit], int skip, int end) {
+  if (skip == 0 && end == kUnit) {
+    if constexpr (F32) {
+      u32x4 x, y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-    *reinterpret_cast<u32x4_any*>(p + i) = x;
-  } else {
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __builtin_bit_cast(unsigned, v[e]);
+        y[e] = __builtin_bit_cast(unsigned, v[4 + e]);
+      }
+      *reinterpret_cast<u32x4_any4*>((float*)p + at) = x;
+      *reinterpret_cast<u32x4_any4*>((float*)p + at + 4) = y;
+    } else {
+      u32x4 x;
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e)
-      if (i + e < width) p[i + e] = (__bf16)v[e];
-  }
-}
-__device__ __forceinline__ void store_f32(float* p, int i, int width, const float (&v)[kUnit]) {
-  if (i + kUnit <= width) {
-    u32x4 x, y;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = __builtin_bit_cast(unsigned, v[e]);
-      y[e] = __builtin_bit_cast(unsigned, v[4 + e]);
+      for (int e = 0; e < 4; ++e) x[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+      *reinterpret_cast<u32x4_any*>((__bf16*)p + at) = x;
     }
-    *reinterpret_cast<u32x4_any4*>(p + i) = x;
-    *reinterpret_cast<u32x4_any4*>(p + i + 4) = y;
-  } else {
+    return;
+  }
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e)
-      if (i + e < width) p[i + e] = v[e];
+  for (int e = 0; e < kUnit; ++e) {
+    if (e < skip || e >= end) continue;
+    if constexpr (F32) ((float*)p)[at + e] = v[e];
+    else ((__bf16*)p)[at + e] = (__bf16)v[e];
   }
 }
 
@@ -125,13 +129,17 @@ __device__ __forceinline__ double from_lane(double x) {
   return __builtin_bit_cast(double, (unsigned long long)(unsigned)lo |
                                         (unsigned long long)(unsigned)hi << 32);
 }
-// The sum over the wave, in every lane: neighbours, pairs, then the mirrored
-// halves and rows of 16 lanes (whose lanes agree by then), rows, halves.
+// The sums over runs of 2, 4, 8 and 16 neighbouring lanes, in all of them.
+template <int N>
+__device__ __forceinline__ double lanes_sum(double x) {
+  if constexpr (N > 1) x += from_lane<0xb1>(x);      // quad_perm 1 0 3 2
+  if constexpr (N > 2) x += from_lane<0x4e>(x);      // quad_perm 2 3 0 1
+  if constexpr (N > 4) x += from_lane<0x141>(x);     // row_half_mirror: quads agree by now
+  if constexpr (N > 8) x += from_lane<0x140>(x);     // row_mirror
+  return x;
+}
 __device__ __forceinline__ double wave_sum(double x) {
-  x += from_lane<0xb1>(x);             // quad_perm 1 0 3 2
-  x += from_lane<0x4e>(x);             // quad_perm 2 3 0 1
-  x += from_lane<0x141>(x);            // row_half_mirror
-  x += from_lane<0x140>(x);            // row_mirror
+  x = lanes_sum<16>(x);
 #pragma unroll
   for (int off = 16; off < 64; off *= 2) {
     const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
@@ -149,138 +157,207 @@ __device__ __forceinline__ double wave_sum(double x) {
 }
 
 // The sum over a row's threads, in every one of them; `part` is used once only.
-template <int TPR>
 __device__ __forceinline__ double row_sum(double x, double* part) {
   x = wave_sum(x);
-  if constexpr (TPR == 64) return x;
-  constexpr int kWaves = TPR / 64;
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return x;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
   __syncthreads();
-  x = 0.0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) x += part[w];
-  return x;
+  const int w = threadIdx.x & 15;
+  return lanes_sum<16>(w < waves ? part[w] : 0.0);
 }
 
-// norm(v) over the row, in place, times (offset + weight) plus bias.
-template <int TPR, int CH>
-__device__ __forceinline__ void normalise(const NormArgs& a, float (&v)[CH][kUnit], int lane,
-                                          const void* weight, const void* bias, double* part) {
-  const double n = (double)a.width;
+// 1 / sqrt(x) within 2^-44: the instruction's number (within 2^-22) after one step
+// of Newton's method; 0 and infinity as it has them.
+__device__ __forceinline__ double inverse_root(double x) {
+  const double r = __builtin_amdgcn_rsq(x);
+  const double y = fma(r * 0.5, fma(-x * r, r, 1.0), r);
+  return x > 0.0 && x < __builtin_inf() ? y : r;
+}
+
+// Where a thread's units lie.  A row's last unit ends with the row: it begins
+// `skip` values early, which belong to the unit before it and take no part here,
+// so that every load is one of whole units within the row.
+template <int CH>
+struct Units {
+  int at[CH], skip[CH], end;
+  __device__ __forceinline__ Units(int lane, int width) {
+    end = min(width, kUnit);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * (int)blockDim.x + lane) * kUnit;
+      at[c] = max(min(i, width - kUnit), 0);
+      skip[c] = i - at[c];
+    }
+  }
+  __device__ __forceinline__ bool has(int c) const { return skip[c] < kUnit; }
+  __device__ __forceinline__ bool has(int c, int e) const { return e >= skip[c] && e < end; }
+  template <bool F32>
+  __device__ __forceinline__ Raw<F32> get(const void* p, size_t row, int c) const {
+    if (__builtin_expect(end < kUnit, 0)) return has(c) ? load_few<F32>(p, row, end) : Raw<F32>{};
+    return load<F32>(p, row + at[c]);
+  }
+};
+
+// norm(v) over the row, in place, times (offset + weight) plus bias.  Values that
+// take no part are zeros before, and no matter after.
+template <int CH, bool WF>
+__device__ __forceinline__ void normalise(const NormArgs& a, float (&v)[CH][kUnit],
+                                          const Units<CH>& u, const void* weight,
+                                          const void* bias, double* part) {
   double mean = 0.0;
   if (a.layer) {
     double s = 0.0;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e)
-        if ((c * TPR + lane) * kUnit + e < a.width) s += (double)v[c][e];
-    mean = row_sum<TPR>(s, part) / n;
+      for (int e = 0; e < kUnit; ++e) s += (double)v[c][e];
+    mean = row_sum(s, part) / (double)a.width;       // a row of one value has exactly that mean
+    // In two parts, so that fp32 differences are rounded relative to themselves.
+    const float hi = (float)mean, lo = (float)(mean - (double)hi);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) v[c][e] = u.has(c, e) ? (v[c][e] - hi) - lo : 0.0f;
   }
-  double s = 0.0;
+  double s[2] = {0.0, 0.0};
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e) {
-      const double d = (double)v[c][e] - mean;
-      if ((c * TPR + lane) * kUnit + e < a.width) s = fma(d, d, s);
-    }
-  const double r = 1.0 / sqrt(row_sum<TPR>(s, part + 16) / n + a.eps);
+    for (int e = 0; e < kUnit; ++e) s[e % 2] = fma((double)v[c][e], (double)v[c][e], s[e % 2]);
+  const double r = inverse_root(fma(row_sum(s[0] + s[1], part + 16), a.inv_width, a.eps));
+  // The product in fp32 wherever r is far from its ends.
+  const float rf = (float)r;
+  const bool mild = rf > 1e-30f && rf < 1e30f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i = (c * TPR + lane) * kUnit;
-    if (i >= a.width) continue;
-    float w[kUnit];
-    if (weight) {
-      load(weight, a.weight_f32, 0, i, a.width, w);
+    Raw<WF> w, b;
+    if (weight) w = u.template get<WF>(weight, 0, c);
+    if (bias) b = u.template get<WF>(bias, 0, c);
+    if (__builtin_expect(mild, 1)) {
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) w[e] += a.weight_offset;
+      for (int e = 0; e < kUnit; ++e) v[c][e] *= rf;
     } else {
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) w[e] = 1.0f;
+      for (int e = 0; e < kUnit; ++e) v[c][e] = (float)((double)v[c][e] * r);
     }
+    if (weight)
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e) v[c][e] = (float)(((double)v[c][e] - mean) * r) * w[e];
-    if (bias) {
-      load(bias, a.weight_f32, 0, i, a.width, w);
+      for (int e = 0; e < kUnit; ++e) v[c][e] *= a.weight_offset + w[e];
+    if (bias)
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) v[c][e] += w[e];
-    }
+      for (int e = 0; e < kUnit; ++e) v[c][e] += b[e];
   }
 }
 
-// TPR threads hold a row in registers, CH runs of kUnit neighbouring values each.
-template <int TPR, int CH>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void skinny_block_norm_k(const NormArgs a) {
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;   // of a workgroup
+// A workgroup holds a row in registers, CH units of 8 neighbouring values per
+// thread and as many threads as the row has units for; every value is read and
+// written once.
+//
+// What bounds it: many rows the memory.  Rows of 8192 in bf16, block and residual in,
+// residual and x out: 16384 of them 180 us = 5.96 TB/s (a plain copy of 2 GiB
+// reaches 4.9 in sum), 1024 13.7; with a norm behind the block, too, 213 us = 5.0.
+// Few rows the chain launch - loads - sum over the waves - store: 2.4 us at a width
+// of 128, 3.3 at 8192, 6.5 with four sums (two LAYER norms).
+//   One unit per thread, against rows of 8192 in 512 threads of two units and 256 of
+// four: 180 / 190 / 194 us (16384 rows), 3.2 / 3.5 / 5.0 (one); rows of 4096 in
+// 512, 1024 (half of them idle) and 256 threads: 91 / 108 / 93.  Two units from 8193
+// values on, four from 16385, whose registers spill (fp32 residual and weights, two
+// LAYER norms, 16384 rows of 32768: 2.7 ms, 3.2 TB/s; bf16 RMS 850 us, 5.0).
+//   A kernel of 64 registers has two workgroups of 16 waves on a CU; 65 had one, and
+// 16384 rows of 8192 with two LAYER norms in fp32 took 481 us instead of 422.
+// Loading weights before the sums, to have them at hand behind, costs those
+// registers and gained nothing at one row.  Several one-wave rows per workgroup gain
+// nothing either (16384 rows of 512: 12.4 us alone, 12.9 by fours).
+template <int CH, bool RF, bool WF>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(CH == 1 ? 8 : 4)))
+void skinny_block_norm_k(const NormArgs a) {
   __shared__ double part[2][32];
-  const int lane = threadIdx.x % TPR;
-  const int row = blockIdx.x * kRows + threadIdx.x / TPR;
-  if (row >= a.rows) return;                         // whole waves, and only without a barrier
+  constexpr bool kAhead = CH <= 2;     // registers are left for loads ahead of their use
+  const int row = blockIdx.x;
   const size_t at = (size_t)row * a.width;
+  const Units<CH> u(threadIdx.x, a.width);
 
-  float h[CH][kUnit], b[CH][kUnit];
+  float v[CH][kUnit];
+  Raw<RF> res[CH];
+  if (a.residual && (kAhead || !a.block))
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int i = (c * TPR + lane) * kUnit;
-#pragma unroll
-    for (int e = 0; e < kUnit; ++e) h[c][e] = b[c][e] = 0.0f;
-    if (i >= a.width) continue;
-    if (a.residual) load(a.residual, a.residual_f32, at, i, a.width, h[c]);
-    if (!a.block) continue;
-    const __bf16* src = a.block + at * a.routes;
-    if (!a.route_weights && a.routes == 1) {
-      load_bf16(src, i, a.width, b[c]);
-      continue;
-    }
-    for (int j = 0; j < a.routes; ++j) {
-      float x[kUnit];
-      load_bf16(src + (size_t)j * a.width, i, a.width, x);
-      const float w = a.route_weights ? a.route_weights[(size_t)row * a.routes + j] : 1.0f;
-#pragma unroll
-      for (int e = 0; e < kUnit; ++e) b[c][e] = fmaf(w, x[e], b[c][e]);
-    }
-  }
+    for (int c = 0; c < CH; ++c) res[c] = u.template get<RF>(a.residual, at, c);
   if (a.block) {
-    if (a.post_weight) normalise<TPR, CH>(a, b, lane, a.post_weight, a.post_bias, part[0]);
+    const size_t first = at * a.routes;
+    Raw<false> x[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * TPR + lane) * kUnit;
-      if (i >= a.width) continue;
-      float g[kUnit];
-      if (a.gate) {
-        load(a.gate, a.weight_f32, a.gate_rows ? at : 0, i, a.width, g);
+    for (int c = 0; c < CH; ++c) x[c] = u.template get<false>(a.block, first, c);
+    if (a.routes == 1 && !a.route_weights) {
 #pragma unroll
-        for (int e = 0; e < kUnit; ++e) b[c][e] *= g[e];
-      }
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) {
-        const float x = a.block_scale * b[c][e];
-        h[c][e] = a.residual ? fmaf(a.residual_scale, h[c][e], x) : x;
+        for (int e = 0; e < kUnit; ++e) v[c][e] = x[c][e];
+    } else {
+      const float* rw = a.route_weights ? a.route_weights + (size_t)row * a.routes : nullptr;
+      for (int j = 0; j < a.routes; ++j) {
+        Raw<false> next[CH];
+        const int k = min(j + 1, a.routes - 1);
+        if constexpr (kAhead)
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            next[c] = u.template get<false>(a.block, first + (size_t)k * a.width, c);
+        const float w = rw ? rw[j] : 1.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < kUnit; ++e) v[c][e] = j ? fmaf(w, x[c][e], v[c][e]) : w * x[c][e];
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          x[c] = kAhead ? next[c] : u.template get<false>(a.block, first + (size_t)k * a.width, c);
       }
     }
+    if (a.post_weight) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e)
+          if (!u.has(c, e)) v[c][e] = 0.0f;
+      normalise<CH, WF>(a, v, u, a.post_weight, a.post_bias, part[0]);
+    }
+    if (a.gate)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const Raw<WF> g = u.template get<WF>(a.gate, a.gate_rows ? at : 0, c);
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) v[c][e] *= g[e];
+      }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) v[c][e] *= a.block_scale;
+    if (a.residual)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if constexpr (!kAhead) res[c] = u.template get<RF>(a.residual, at, c);
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) v[c][e] = fmaf(a.residual_scale, res[c][e], v[c][e]);
+      }
   } else {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) h[c][e] *= a.residual_scale;
+      for (int e = 0; e < kUnit; ++e) v[c][e] = a.residual_scale * res[c][e];
   }
-  if (a.residual_out) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * TPR + lane) * kUnit;
-      if (i >= a.width) continue;
-      if (a.residual_f32) store_f32((float*)a.residual_out + at, i, a.width, h[c]);
-      else store_bf16((__bf16*)a.residual_out + at, i, a.width, h[c]);
-    }
-  }
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e)
+      if (!u.has(c, e)) v[c][e] = 0.0f;
+  if (a.residual_out)
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (u.has(c)) store<RF>(a.residual_out, at + u.at[c], v[c], u.skip[c], u.end);
   if (!a.out) return;
-  normalise<TPR, CH>(a, h, lane, a.weight, a.bias, part[1]);
+  normalise<CH, WF>(a, v, u, a.weight, a.bias, part[1]);
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int i = (c * TPR + lane) * kUnit;
-    if (i < a.width) store_bf16(a.out + at, i, a.width, h[c]);
-  }
+  for (int c = 0; c < CH; ++c)
+    if (u.has(c)) store<false>(a.out, at + u.at[c], v[c], u.skip[c], u.end);
 }
 
 // ---------------------------------------------------------------------------
@@ -288,11 +365,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void skinny_block_norm_k(con
 
 bool finite(float x) { return x - x == 0.0f; }
 
-template <int TPR, int CH>
-skinny_status launch(const NormArgs& a, hipStream_t stream) {
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-  hipLaunchKernelGGL((skinny_block_norm_k<TPR, CH>), dim3((a.rows + kRows - 1) / kRows),
-                     dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
+template <int CH>
+skinny_status launch(const NormArgs& a, bool rf, bool wf, hipStream_t stream) {
+  const int units = (a.width + CH * kUnit - 1) / (CH * kUnit);
+  const dim3 grid(a.rows), threads((units + 63) / 64 * 64);
+  if (rf && wf) hipLaunchKernelGGL((skinny_block_norm_k<CH, true, true>), grid, threads, 0, stream, a);
+  else if (rf) hipLaunchKernelGGL((skinny_block_norm_k<CH, true, false>), grid, threads, 0, stream, a);
+  else if (wf) hipLaunchKernelGGL((skinny_block_norm_k<CH, false, true>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((skinny_block_norm_k<CH, false, false>), grid, threads, 0, stream, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 
@@ -372,19 +452,17 @@ skinny_status skinny_block_norm(const skinny_norm* norm, void* stream) {
   a.width = n.width;
   a.routes = n.routes;
   a.layer = n.kind == SKINNY_NORM_LAYER;
-  a.residual_f32 = n.residual_dtype == SKINNY_VALUES_F32;
-  a.weight_f32 = n.weight_dtype == SKINNY_VALUES_F32;
   a.gate_rows = n.gate_rows;
   a.residual_scale = n.residual_scale;
   a.block_scale = n.block_scale;
   a.weight_offset = n.weight_offset;
   a.eps = (double)n.eps;
+  a.inv_width = 1.0 / n.width;
   const hipStream_t hs = (hipStream_t)stream;
-  if (n.width <= 512) return launch<64, 1>(a, hs);
-  if (n.width <= 2048) return launch<256, 1>(a, hs);
-  if (n.width <= 8192) return launch<1024, 1>(a, hs);
-  if (n.width <= 16384) return launch<1024, 2>(a, hs);
-  return launch<1024, 4>(a, hs);
+  const bool rf = n.residual_dtype == SKINNY_VALUES_F32, wf = n.weight_dtype == SKINNY_VALUES_F32;
+  if (a.width <= 1024 * kUnit) return launch<1>(a, rf, wf, hs);
+  if (a.width <= 2048 * kUnit) return launch<2>(a, rf, wf, hs);
+  return launch<4>(a, rf, wf, hs);
 }
 
 }  // extern "C"
