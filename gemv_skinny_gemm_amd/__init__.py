@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "BF16", "FP8_BS128", "VARIANT_AUTO", "VARIANT_VECTOR", "VARIANT_MFMA", "MAX_M",
@@ -243,6 +244,11 @@ def _bind(path: str):
     L.skinny_lora_linear.argtypes = [ctypes.POINTER(Lora), vp, vp, i, vp, vp, vp, sz, vp]
     L.skinny_moe_route.restype = i
     L.skinny_moe_route.argtypes = [ctypes.POINTER(Route), vp]
+    # The same entry points for structures packed as bytes.
+    L.norm_of_bytes, L.route_of_bytes = L["skinny_block_norm"], L["skinny_moe_route"]
+    for f in (L.norm_of_bytes, L.route_of_bytes):
+        f.restype = i
+        f.argtypes = [ctypes.c_char_p, vp]
     L.skinny_status_string.restype = ctypes.c_char_p
     L.skinny_status_string.argtypes = [i]
     L.skinny_abi_version.restype = i
@@ -872,6 +878,12 @@ def _values(t, tt, what) -> int:
     return VALUES_F32
 
 
+# struct skinny_norm and struct skinny_route as bytes: a ctypes structure of as many
+# fields takes three times as long to make (2 us of a call's host time).
+_NORM = struct.Struct("8i4f10P")
+_ROUTE = struct.Struct("8ifi4P")
+
+
 def block_norm(out, weight, residual=None, block=None, residual_out=None, bias=None,
                post_weight=None, post_bias=None, gate=None, route_weights=None,
                kind: int = NORM_RMS, eps: float = 1e-6, residual_scale: float = 1.0,
@@ -889,11 +901,14 @@ def block_norm(out, weight, residual=None, block=None, residual_out=None, bias=N
     if first is None:
         raise ValueError("one of out and residual_out is needed")
     tt, dev = _call_device(first)
-    rows, width = _shape2(first)
-    shape, one = (rows, width), (width,)
-    y = None if out is None else _operand(out, shape, tt.bf16, "out", dev)
+    shape = first.shape
+    if len(shape) != 2:
+        raise ValueError("expected a 2-D tensor")
+    rows, width = shape
     rt, routes, gate_rows, wt = VALUES_BF16, 1, 0, None
-    h = r = b = rw = g = None
+    y = h = r = b = rw = g = 0
+    if out is not None:
+        y = _operand(out, shape, tt.bf16, "out", dev)
     if residual is not None:
         rt = _values(residual, tt, "residual")
         h = _operand(residual, shape, residual.dtype, "residual", dev)
@@ -905,31 +920,36 @@ def block_norm(out, weight, residual=None, block=None, residual_out=None, bias=N
         if route_weights is not None:
             routes = _shape2(route_weights)[1]
             rw = _operand(route_weights, (rows, routes), tt.f32, "route_weights", dev)
-        elif rows:
+        elif block.shape != shape and rows:
             routes = max(1, block.shape[0] // rows)
         b = _operand(block, (rows * routes, width), tt.bf16, "block", dev)
     elif route_weights is not None or gate is not None or post_weight is not None:
         raise ValueError("route_weights, gate and post_weight need a block")
-    vectors = []
-    for t, what in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"),
-                    (post_bias, "post_bias")):
-        if t is None:
-            vectors.append(None)
-            continue
-        wt = t.dtype if wt is None else wt
-        vectors.append(_operand(t, one, wt, what, dev))
+    w = wb = pw = pb = 0
+    if weight is not None:
+        wt = weight.dtype
+        w = _operand(weight, (width,), wt, "weight", dev)
+    if bias is not None:
+        wt = wt or bias.dtype
+        wb = _operand(bias, (width,), wt, "bias", dev)
+    if post_weight is not None:
+        wt = wt or post_weight.dtype
+        pw = _operand(post_weight, (width,), wt, "post_weight", dev)
+    if post_bias is not None:
+        wt = wt or post_bias.dtype
+        pb = _operand(post_bias, (width,), wt, "post_bias", dev)
     if gate is not None:
-        wt = gate.dtype if wt is None else wt
+        wt = wt or gate.dtype
         gate_rows = int(gate.dim() == 2)
-        g = _operand(gate, shape if gate_rows else one, wt, "gate", dev)
-    for t in (weight, bias, post_weight, post_bias, gate):
-        if t is not None:
-            _values(t, tt, "weight")
-    w, wb, pw, pb = vectors
-    n = Norm(kind, rows, width, routes, rt, VALUES_F32 if wt is tt.f32 else VALUES_BF16, gate_rows, 0,
-             eps, residual_scale, block_scale, weight_offset, b, rw, pw, pb, g, h, r, w, wb, y)
-    _check(lib().skinny_block_norm(n, _call_stream(tt, dev, stream)), "skinny_block_norm")
-    return out if out is not None else residual_out
+        g = _operand(gate, shape if gate_rows else (width,), wt, "gate", dev)
+    if wt is not None and wt is not tt.bf16 and wt is not tt.f32:
+        raise ValueError(f"weights, biases and gate: dtype {str(wt).replace('torch.', '')}, expected "
+                         "bfloat16 or float32")
+    n = _NORM.pack(kind, rows, width, routes, rt, VALUES_F32 if wt is tt.f32 else VALUES_BF16,
+                   gate_rows, 0, eps, residual_scale, block_scale, weight_offset, b, rw, pw, pb, g,
+                   h, r, w, wb, y)
+    _check(lib().norm_of_bytes(n, _call_stream(tt, dev, stream)), "skinny_block_norm")
+    return first
 
 
 def make_lora(a, b, scale=None, ranks=None) -> Lora:
@@ -995,13 +1015,17 @@ def moe_route(logits, ids, weights, scoring: int = ROUTE_SOFTMAX, bias=None, gro
     into ids int32 [rows][topk], for moe_linear and moe_mlp_swiglu, and their
     weights into weights float32 [rows][topk], for block_norm's sum of the routes."""
     tt, dev = _call_device(logits)
-    rows, experts = _shape2(logits)
-    kind = _values(logits, tt, "logits")
-    topk = _shape2(ids)[1]
-    r = Route(kind, scoring, rows, experts, topk, groups, top_groups, int(renormalize), scale, 0,
-              _operand(logits, (rows, experts), logits.dtype, "logits", dev),
-              None if bias is None else _operand(bias, (experts,), tt.f32, "bias", dev),
-              _operand(ids, (rows, topk), tt.i32, "ids", dev),
-              _operand(weights, (rows, topk), tt.f32, "weights", dev))
-    _check(lib().skinny_moe_route(r, _call_stream(tt, dev, stream)), "skinny_moe_route")
+    shape, chosen = logits.shape, ids.shape
+    if len(shape) != 2 or len(chosen) != 2:
+        raise ValueError("expected 2-D tensors")
+    rows, experts = shape
+    topk = chosen[1]
+    each = (rows, topk)
+    r = _ROUTE.pack(_values(logits, tt, "logits"), scoring, rows, experts, topk, groups, top_groups,
+                    bool(renormalize), scale, 0,
+                    _operand(logits, shape, logits.dtype, "logits", dev),
+                    0 if bias is None else _operand(bias, (experts,), tt.f32, "bias", dev),
+                    _operand(ids, each, tt.i32, "ids", dev),
+                    _operand(weights, each, tt.f32, "weights", dev))
+    _check(lib().route_of_bytes(r, _call_stream(tt, dev, stream)), "skinny_moe_route")
     return ids
