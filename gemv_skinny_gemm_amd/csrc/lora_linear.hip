@@ -17,6 +17,7 @@ using skinny_host::range_of;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));   // y's rows of an odd width
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -34,15 +35,21 @@ struct LoraArgs {
   const int* ids;
   const int* ranks;
   const float* scale;
-  float* part;                         // [splits][slices][rows][rank]
+  // In the workspace:
+  float* part;                         // [splits][slices][rows][rank]: A x over a split's K
+  __bf16* low;                         // joined: [slices][rows][2][padded], A x in two parts
+  int4* blocks;                        // [most_blocks]: up to 64 rows of one adapter (-1: of
+                                       // none): adapter, first place in order, rows, its rank
+  int* order;                          // row numbers
+  int most_blocks;
   const __bf16* a[kMaxSlices];
   const __bf16* b[kMaxSlices];
   int n[kMaxSlices], col[kMaxSlices];  // columns of a slice, and the first one's number in y
   int tile[kMaxSlices + 1];            // first column tile of a slice
   int rows, adapters, rank, K, N, slices;
   int splits, pieces;                  // of K, and pieces of a split
-  int rank_groups;                     // of 16 MT ranks
-  int ordinals;                        // workgroups that share a row block's adapters
+  int rank_groups;                     // few rows: of 16 MT ranks; many: passes over A's tiles
+  int ordinals;                        // few rows: adapters at most
   int copy;                            // base is not y: rows without an adapter are copied
 };
 
@@ -61,6 +68,31 @@ __device__ __forceinline__ float bf16_hi(unsigned u) {
   return __builtin_bit_cast(float, u & 0xffff0000u);
 }
 
+// 128 bytes of each of 16 rows in two registers' worth of 16 bytes per lane: as the
+// products take them, lane (c, g) has parts g and g + 4 of row c; as they are loaded
+// and stored, in whole lines, parts g + 4 (c / 8) of rows c % 8 and c % 8 + 8.  A load
+// of half lines costs the L1 cache as much as one of whole lines (an instruction of
+// 16 half lines 66 cycles of a CU, one of 8 whole ones 23).
+struct Lines {
+  u32x4 x[2];
+  template <int BANKS>
+  static __device__ __forceinline__ u32x4 exchange(u32x4 own, u32x4 other) {
+    u32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)        // lane c ^ 8's, in lanes 8 .. 15 or 0 .. 7 of each 16
+      r[e] = __builtin_amdgcn_update_dpp((int)own[e], (int)other[e], 0x128, 0xf, BANKS, false);
+    return r;
+  }
+  // From one form to the other, either way.
+  __device__ __forceinline__ Lines turned() const {
+    return Lines{{exchange<0xc>(x[0], x[1]), exchange<0x3>(x[1], x[0])}};
+  }
+};
+__device__ __forceinline__ int line_row() { return threadIdx.x & 7; }
+__device__ __forceinline__ int line_part() {
+  return ((threadIdx.x & 63) >> 4) + ((threadIdx.x & 8) >> 1);
+}
+
 __device__ __forceinline__ unsigned upper_halves(float a, float b) {
   return __builtin_amdgcn_perm(__builtin_bit_cast(unsigned, b), __builtin_bit_cast(unsigned, a),
                                0x07060302u);
@@ -71,313 +103,758 @@ __device__ __forceinline__ float rest_of(float x, float part) {
   return r - r == 0.0f ? r : 0.0f;
 }
 
-// The rows of a block that share an adapter.
-struct Group {
-  int adapter;                         // -1: the rows without one
-  unsigned long long lanes;            // bit l: row l of the block
-};
-
-// The adapters of a row block, one after the other: lane l holds row l's.
-struct Adapters {
-  int id;                              // of the lane's row; -1: none
-  unsigned long long rest;             // rows with an adapter that has not come yet
-  unsigned long long none;             // rows without one
-  __device__ __forceinline__ Adapters(const LoraArgs& a, int block) {
-    const int t = block * kRowBlock + (threadIdx.x & 63);
-    id = t < a.rows ? a.ids[t] : -1;
-    if (id < 0 || id >= a.adapters) id = -1;
-    rest = __ballot(id >= 0);
-    none = __ballot(id < 0 && t < a.rows);
-  }
-  __device__ __forceinline__ Group next() {
-    const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(rest));
-    const unsigned long long same = __ballot(id == e);
-    rest &= ~same;
-    return Group{e, same};
-  }
-};
-
-__device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
-  return a.ranks ? min(max(uniform(a.ranks[adapter]), 0), a.rank) : a.rank;
-}
-
-// Row numbers of a group's rows, side by side, the last one again behind them.
-__device__ __forceinline__ void list_rows(const Group& g, int block, int (&list)[kRowBlock]) {
+// The numbers of `rows`, side by side, the last one again behind them (one wave).
+__device__ __forceinline__ void list_rows(unsigned long long rows, int* list) {
   const int lane = threadIdx.x & 63;
-  const int count = __popcll(g.lanes);
-  const int at = __popcll(g.lanes & ((1ull << lane) - 1));
-  if (threadIdx.x < 64) {
-    if (g.lanes >> lane & 1) list[at] = block * kRowBlock + lane;
-    if (lane >= count) list[lane] = block * kRowBlock + 63 - __builtin_clzll(g.lanes);
-  }
+  const int count = __popcll(rows);
+  if (rows >> lane & 1) list[__popcll(rows & ((1ull << lane) - 1))] = lane;
+  if (lane >= count && count) list[lane] = 63 - __builtin_clzll(rows);
 }
 
-// A x for RT tiles of 16 rows and MT tiles of 16 ranks over a split's share of K:
-// the waves take pieces of K in turn, and their sums are added in order.
+// Few rows (one block): A x for RT tiles of 16 rows and MT tiles of 16 ranks over a
+// split's share of K: the waves take pieces of K in turn, and their sums are added
+// in order.
+constexpr int kFewWaves = 8;
+constexpr int kSumTiles = 4;           // tiles that the waves add up at a time
 template <int MT, int RT>
 __device__ __forceinline__ void shrink(const LoraArgs& a, const __bf16* w, int rank, int r0,
                                        int count, int split, int slice, const int* list,
                                        float* sums) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  f32x4 acc[MT][RT];
+  f32x4 acc[MT * RT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int i = 0; i < MT * RT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+  const int lr = line_row(), lp = 8 * line_part();
+  const __bf16* xp[RT][2];
+  const __bf16* wp[MT][2];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
-  const __bf16* xp[RT];
-  const __bf16* wp[MT];
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-  for (int t = 0; t < RT; ++t) xp[t] = a.x + (size_t)list[16 * t + c] * a.K + 8 * g;
+    for (int t = 0; t < RT; ++t) xp[t][h] = a.x + (size_t)list[16 * t + 8 * h + lr] * a.K + lp;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) wp[m] = w + (size_t)min(r0 + 16 * m + c, rank - 1) * a.K + 8 * g;
+    for (int m = 0; m < MT; ++m)
+      wp[m][h] = w + (size_t)min(r0 + 16 * m + 8 * h + lr, rank - 1) * a.K + lp;
+  }
   const int end = min((split + 1) * a.pieces * kPiece, a.K);
-  for (int k = (split * a.pieces + wave) * kPiece; k < end; k += kWaves * kPiece) {
-    u32x4 xf[2][RT], wf[2][MT];
+  for (int k = (split * a.pieces + wave) * kPiece; k < end; k += kFewWaves * kPiece) {
+    Lines xf[RT], wf[MT];
+    const bool in = k + lp < end;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bool in = k + 32 * u + 8 * g < end;
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        wf[m].x[h] = in ? *reinterpret_cast<const u32x4*>(wp[m][h] + k) : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int t = 0; t < RT; ++t)
-        xf[u][t] = in ? *reinterpret_cast<const u32x4*>(xp[t] + k + 32 * u) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        wf[u][m] = in ? *reinterpret_cast<const u32x4*>(wp[m] + k + 32 * u) : u32x4{0, 0, 0, 0};
+        xf[t].x[h] = in ? *reinterpret_cast<const u32x4*>(xp[t][h] + k) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int m = 0; m < MT; ++m) wf[m] = wf[m].turned();
+#pragma unroll
+    for (int t = 0; t < RT; ++t) xf[t] = xf[t].turned();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc[m][t] = mfma_bf16(wf[u][m], xf[u][t], acc[m][t]);
+        for (int t = 0; t < RT; ++t)
+          acc[m * RT + t] = mfma_bf16(wf[m].x[h], xf[t].x[h], acc[m * RT + t]);
   }
-  // Lane (c, g), register r holds rank 4g + r of row c.
+  // Lane (c, g), register r of a tile holds rank 4g + r of row c.
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int i0 = 0; i0 < MT * RT; i0 += kSumTiles) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-      *reinterpret_cast<f32x4*>(sums + ((wave * MT + m) * RT + t) * 256 + lane * 4) = acc[m][t];
-  __syncthreads();
-  for (int i = threadIdx.x; i < MT * RT * 64; i += kThreads) {
-    const int l = i & 63, t = i / 64 % RT, m = i / 64 / RT;
-    const int row = 16 * t + (l & 15), r = r0 + 16 * m + 4 * (l >> 4);
-    if (row >= count || r >= rank) continue;
-    f32x4 s{0, 0, 0, 0};
+    for (int i = i0; i < i0 + kSumTiles && i < MT * RT; ++i)
+      *reinterpret_cast<f32x4*>(sums + (wave * kSumTiles + i - i0) * 256 + lane * 4) = acc[i];
+    __syncthreads();
+    const int i = i0 + (int)threadIdx.x / 64;
+    if (i < i0 + kSumTiles && i < MT * RT) {
+      const int row = i % RT * 16 + c, r = r0 + 16 * (i / RT) + 4 * g;
+      f32x4 s{0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v)
-      s += *reinterpret_cast<const f32x4*>(sums + ((v * MT + m) * RT + t) * 256 + l * 4);
-    *reinterpret_cast<f32x4*>(
-        a.part + ((size_t)(split * a.slices + slice) * a.rows + list[row]) * a.rank + r) = s;
+      for (int v = 0; v < kFewWaves; ++v)
+        s += *reinterpret_cast<const f32x4*>(sums + (v * kSumTiles + i - i0) * 256 + lane * 4);
+      if (row < count && r < rank)
+        *reinterpret_cast<f32x4*>(
+            a.part + ((size_t)(split * a.slices + slice) * a.rows + list[row]) * a.rank + r) = s;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 }
 
 template <int MT>
-__global__ __launch_bounds__(kThreads) void skinny_lora_shrink(const LoraArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves) void skinny_lora_shrink_few(const LoraArgs a) {
   __shared__ int list[kRowBlock];
-  __shared__ __attribute__((aligned(16))) float sums[kWaves * MT * 4 * 256];
-  // Splits of one item run on neighbouring workgroups.
+  __shared__ __attribute__((aligned(16))) float sums[kFewWaves * kSumTiles * 256];
   int i = blockIdx.x;
   const int split = i % a.splits;
   i /= a.splits;
   const int r0 = i % a.rank_groups * 16 * MT;
   i /= a.rank_groups;
   const int slice = i % a.slices;
-  i /= a.slices;
-  const int ordinal = i % a.ordinals;
-  const int block = i / a.ordinals;
-  if (!a.a[slice]) return;
-  Adapters all(a, block);
-  for (int d = 0; all.rest; ++d) {
-    const Group grp = all.next();
-    if (d % a.ordinals != ordinal) continue;
-    const int rank = rank_of(a, grp.adapter);
-    if (r0 >= rank) continue;
-    list_rows(grp, block, list);
-    __syncthreads();
-    const int count = __popcll(grp.lanes);
-    const __bf16* w = a.a[slice] + (size_t)grp.adapter * a.rank * a.K;
-    if (count <= 16) shrink<MT, 1>(a, w, rank, r0, count, split, slice, list, sums);
-    else if (count <= 32) shrink<MT, 2>(a, w, rank, r0, count, split, slice, list, sums);
-    else shrink<MT, 4>(a, w, rank, r0, count, split, slice, list, sums);
+  const int ordinal = i / a.slices;
+  // Lane l has row l's adapter; the workgroup takes the ordinal-th one that comes.
+  const int lane = threadIdx.x & 63;
+  int id = lane < a.rows ? a.ids[lane] : -1;
+  if (id < 0 || id >= a.adapters) id = -1;
+  unsigned long long rest = __ballot(id >= 0), rows = 0;
+  int adapter = -1;
+  for (int d = 0; d <= ordinal && rest; ++d) {
+    adapter = __builtin_amdgcn_readlane(id, __builtin_ctzll(rest));
+    rows = __ballot(id == adapter);
+    rest &= ~rows;
+    if (d < ordinal) rows = 0;
+  }
+  const int count = __popcll(rows);
+  const int rank = count == 0 ? 0 : a.ranks ? min(max(uniform(a.ranks[adapter]), 0), a.rank) : a.rank;
+  // What the second launch has to know; the last block has the rows without an adapter.
+  const bool tells = split == 0 && slice == 0 && r0 == 0;
+  if (threadIdx.x < 64) {
+    list_rows(rows, list);
+    if (tells) {
+      if (lane < count) a.order[ordinal * kRowBlock + lane] = list[lane];
+      if (lane == 0) a.blocks[ordinal] = int4{adapter, ordinal * kRowBlock, count, rank};
+      if (ordinal == 0) {
+        const unsigned long long none = __ballot(id < 0 && lane < a.rows);
+        const int last = a.most_blocks - 1;
+        if (none >> lane & 1)
+          a.order[last * kRowBlock + __popcll(none & ((1ull << lane) - 1))] = lane;
+        if (lane == 0) a.blocks[last] = int4{-1, last * kRowBlock, __popcll(none), 0};
+      }
+    }
+  }
+  if (!a.a[slice] || r0 >= rank) return;
+  __syncthreads();
+  const __bf16* w = a.a[slice] + (size_t)adapter * a.rank * a.K;
+  if (count <= 16) {
+    shrink<MT, 1>(a, w, rank, r0, count, split, slice, list, sums);
+  } else {
+    constexpr int H = MT > 2 ? 2 : MT;               // registers for two tiles of ranks by 64 rows
+#pragma unroll
+    for (int m = 0; m < MT; m += H)
+      if (r0 + 16 * m < rank)
+        shrink<H, 4>(a, w, rank, r0 + 16 * m, count, split, slice, list, sums);
   }
 }
 
-// y of RT tiles of 16 rows in the wave's columns.
-template <int RT>
-__device__ __forceinline__ void expand(const LoraArgs& a, const __bf16* w, int rank, int n0, int n,
-                                       int col, int count, const int* list, const unsigned* hi,
-                                       const unsigned* lo, int stride) {
-  const int lane = threadIdx.x & 63;
+// Many rows: A x for all slices and ranks of RT tiles of 16 rows.  The rows of x pass
+// through shared memory, a stage of 128 values of K ahead in registers, and each wave
+// multiplies them with MT tiles of 16 ranks of its own, whose rows of A it loads
+// itself, a stage ahead.
+constexpr int kStage = 128;            // values of K
+constexpr int kChunks = kStage / 8;    // 16-byte chunks of a row's stage
+template <int MT, int RT>
+__device__ __forceinline__ void shrink_rows(const LoraArgs& a, int adapter, int rank, int count,
+                                            int split, int pass, const int* list, u32x4* xs) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  f32x4 acc[RT][4];
+  const int per = (a.rank + 15) / 16;                // tiles of a slice
+  // The wave's tiles: of which slice, and their first rank.
+  const __bf16* wp[MT][2];
+  int slice[MT], r0[MT];
+  bool any = false;
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
-  // Product j's row i is column 16 (i / 4) + 4 j + i % 4, so that a lane ends with
-  // 16 neighbouring columns of one row of y.
-  const __bf16* wp[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = n0 + 16 * (c >> 2) + 4 * j + (c & 3);
-    wp[j] = w + (size_t)min(at, n - 1) * a.rank;
-  }
-  for (int k = 0; k < rank; k += 32) {
-    const int at = k + 8 * g;
-    u32x4 wf[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      wf[j] = at < rank ? *reinterpret_cast<const u32x4*>(wp[j] + at) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {    // columns past the adapter's own, whatever they hold
-        if (at + 2 * e >= rank) wf[j][e] = 0;
-        else if (at + 2 * e + 1 >= rank) wf[j][e] &= 0xffffu;
+  for (int m = 0; m < MT; ++m) {
+    int tile = (pass * MT + m) * kWaves + wave;
+    slice[m] = -1;
+    r0[m] = 0;
+    for (int s = 0; s < a.slices; ++s) {
+      if (!a.a[s]) continue;
+      if (tile >= 0 && tile < per) {
+        slice[m] = s;
+        r0[m] = 16 * tile;
       }
+      tile -= per;
     }
+    if (slice[m] >= 0 && r0[m] >= rank) slice[m] = -1;
+    any = any || slice[m] >= 0;
+    const int s = max(slice[m], 0);
+    const __bf16* w = nullptr;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int v = (16 * t + c) * stride + at / 2;
-      const u32x4 vh = *reinterpret_cast<const u32x4*>(hi + v);
-      const u32x4 vl = *reinterpret_cast<const u32x4*>(lo + v);
+    for (int i = 0; i < kMaxSlices; ++i)
+      if (i == s) w = a.a[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = mfma_bf16(wf[j], vh, acc[t][j]);
+    for (int h = 0; h < 2; ++h)
+      wp[m][h] = w + ((size_t)adapter * a.rank + min(r0[m] + 8 * h + line_row(), rank - 1)) * a.K +
+                 8 * line_part();
+  }
+  f32x4 acc[MT][RT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = mfma_bf16(wf[j], vl, acc[t][j]);
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
+  // Thread i moves chunk i % 16 of rows i / 16 + 16 t; a row's chunks lie turned by the
+  // row's number, so that 16 rows' equal chunks are in different banks.
+  const int row = threadIdx.x / kChunks, chunk = threadIdx.x % kChunks;
+  const __bf16* xp[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) xp[t] = a.x + (size_t)list[16 * t + row] * a.K + 8 * chunk;
+  const int begin = split * a.pieces * kPiece, end = min(begin + a.pieces * kPiece, a.K);
+  u32x4 xr[RT];
+  Lines wf[2][MT], wn[2][MT];
+  const auto load_x = [&](int k) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      xr[t] = k + 8 * chunk < end ? *reinterpret_cast<const u32x4*>(xp[t] + k) : u32x4{0, 0, 0, 0};
+  };
+  const auto load_w = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          wn[u][m].x[h] = slice[m] >= 0 && k + 64 * u + 8 * line_part() < end
+              ? *reinterpret_cast<const u32x4*>(wp[m][h] + k + 64 * u) : u32x4{0, 0, 0, 0};
+  };
+  load_x(begin);
+  load_w(begin);
+  int buf = 0;
+  for (int k = begin; k < end; k += kStage) {
+    u32x4* x = xs + buf * kRowBlock * kChunks;
+    buf ^= 1;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) x[(16 * t + row) * kChunks + (chunk ^ row)] = xr[t];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) wf[u][m] = wn[u][m].turned();
+    __syncthreads();
+    load_x(k + kStage);
+    load_w(k + kStage);
+    if (any) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const u32x4 xf = x[(16 * t + c) * kChunks + ((4 * u + g) ^ c)];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[m][t] = mfma_bf16(wf[u / 2][m].x[u % 2], xf, acc[m][t]);
+        }
     }
   }
-  const int first = n0 + 16 * g;
-  const int cols = min(n - first, 16);
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    if (16 * t + c >= count || cols <= 0) continue;
-    const size_t at = (size_t)list[16 * t + c] * a.N + col + first;
-    if (cols == 16) {
+  for (int m = 0; m < MT; ++m) {
+    const int r = r0[m] + 4 * g;
+    if (slice[m] < 0 || r >= rank) continue;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        u32x4 v = *reinterpret_cast<const u32x4_any*>(a.base + at + 8 * p);
+    for (int t = 0; t < RT; ++t)
+      if (16 * t + c < count)
+        *reinterpret_cast<f32x4*>(a.part + ((size_t)(split * a.slices + slice[m]) * a.rows +
+                                            list[16 * t + c]) * a.rank + r) = acc[m][t];
+  }
+  __syncthreads();
+}
+
+// The block that a workgroup works on.
+struct Block {
+  int adapter, first, count, rank;
+  __device__ __forceinline__ Block(const LoraArgs& a, int i) {
+    const int4 b = a.blocks[i];
+    adapter = uniform(b.x);
+    first = uniform(b.y);
+    count = uniform(b.z);
+    rank = uniform(b.w);
+  }
+  // Its rows' numbers, the last one again behind them.
+  __device__ __forceinline__ void rows(const LoraArgs& a, int* list) const {
+    if (threadIdx.x < kRowBlock) list[threadIdx.x] = a.order[first + min((int)threadIdx.x, count - 1)];
+  }
+};
+
+template <int MT>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void skinny_lora_shrink_many(const LoraArgs a) {
+  __shared__ int list[kRowBlock];
+  __shared__ __attribute__((aligned(16))) u32x4 xs[2 * kRowBlock * kChunks];
+  int i = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+  const int split = i % a.splits;
+  i /= a.splits;
+  const int pass = i % a.rank_groups;
+  i /= a.rank_groups;
+  if (i >= a.most_blocks) return;
+  const Block b(a, i);
+  if (b.count == 0 || b.rank == 0) return;
+  b.rows(a, list);
+  __syncthreads();
+  if (b.count <= 16) shrink_rows<MT, 1>(a, b.adapter, b.rank, b.count, split, pass, list, xs);
+  else shrink_rows<MT, 4>(a, b.adapter, b.rank, b.count, split, pass, list, xs);
+}
+
+// Many rows: their order by adapter, and the blocks of up to 64 that share one (the
+// blocks behind the last have no rows).  One workgroup counts in shared memory; in
+// what order the rows of one adapter come changes no result.
+constexpr int kGroupThreads = 1024;
+__global__ __launch_bounds__(kGroupThreads) void skinny_lora_group(const LoraArgs a) {
+  extern __shared__ int count[];                     // [adapters + 1], the last: without one
+  __shared__ int2 waves[kGroupThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int kinds = a.adapters + 1;
+  for (int e = tid; e < kinds; e += kGroupThreads) count[e] = 0;
+  __syncthreads();
+  const auto kind_of = [&](int t) {
+    const int e = a.ids[t];
+    return e >= 0 && e < a.adapters ? e : a.adapters;
+  };
+  // The place of the row among its kind's: one addition for a wave of one kind.
+  const auto place = [&](int e, bool live) -> int {
+    const int first = uniform(e);
+    const unsigned long long all = __ballot(live), same = __ballot(live && e == first);
+    if (all == same) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&count[first], __popcll(all));
+      return uniform(at) + __popcll(all & ((1ull << lane) - 1));
+    }
+    return live ? atomicAdd(&count[e], 1) : 0;
+  };
+  // The first rows' kinds and places stay in registers, the others' are found twice.
+  constexpr int kKept = 8;
+  int kind[kKept], at[kKept];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = pack_bf16(bf16_lo(v[e]) + acc[t][2 * p + e / 2][2 * (e % 2)],
-                           bf16_hi(v[e]) + acc[t][2 * p + e / 2][2 * (e % 2) + 1]);
-        *reinterpret_cast<u32x4_any*>(a.y + at + 8 * p) = v;
-      }
+  for (int i = 0; i < kKept; ++i) kind[i] = kind_of(min(tid + i * kGroupThreads, a.rows - 1));
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int t = tid + i * kGroupThreads;
+    at[i] = t - lane < a.rows ? place(kind[i], t < a.rows) : 0;
+  }
+  __syncthreads();                     // the kept rows come first among their kind
+  for (int t = tid + kKept * kGroupThreads; t - lane < a.rows; t += kGroupThreads)
+    place(kind_of(min(t, a.rows - 1)), t < a.rows);
+  __syncthreads();
+  // Rows and blocks of the kinds before each one's.
+  const int per = (kinds + kGroupThreads - 1) / kGroupThreads;
+  const int e0 = min(tid * per, kinds), e1 = min(e0 + per, kinds);
+  int2 own{0, 0};
+  for (int e = e0; e < e1; ++e) {
+    own.x += count[e];
+    own.y += (count[e] + kRowBlock - 1) / kRowBlock;
+  }
+  int2 incl = own;
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const int x = __shfl_up(incl.x, off), y = __shfl_up(incl.y, off);
+    if (lane >= off) {
+      incl.x += x;
+      incl.y += y;
+    }
+  }
+  if (lane == 63) waves[wave] = incl;
+  __syncthreads();
+  int2 before{incl.x - own.x, incl.y - own.y};
+  int used = 0;
+  for (int w = 0; w < kGroupThreads / 64; ++w) {
+    if (w < wave) {
+      before.x += waves[w].x;
+      before.y += waves[w].y;
+    }
+    used += waves[w].y;
+  }
+  for (int e = e0; e < e1; ++e) {
+    const int n = count[e];
+    if (n == 0) continue;
+    count[e] = before.x;                             // now the place of its first row
+    const bool one = e < a.adapters;
+    const int rank = !one ? 0 : a.ranks ? min(max(a.ranks[e], 0), a.rank) : a.rank;
+    for (int r = 0; r < n; r += kRowBlock)
+      a.blocks[before.y++] = int4{one ? e : -1, before.x + r, min(n - r, kRowBlock), rank};
+    before.x += n;
+  }
+  for (int b = used + tid; b < a.most_blocks; b += kGroupThreads) a.blocks[b] = int4{-1, 0, 0, 0};
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int t = tid + i * kGroupThreads;
+    if (t < a.rows) a.order[count[kind[i]] + at[i]] = t;
+  }
+  if (a.rows <= kKept * kGroupThreads) return;
+  __syncthreads();
+  // Places behind the kept rows': a kind's counter moves on from its first place by them.
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) place(kind[i], true);
+  __syncthreads();
+  for (int t = tid + kKept * kGroupThreads; t - lane < a.rows; t += kGroupThreads) {
+    const int e = kind_of(min(t, a.rows - 1));
+    const int p = place(e, t < a.rows);
+    if (t < a.rows) a.order[p] = t;
+  }
+}
+
+// Many rows: the splits' sums, times the scale, in the two bf16 numbers that the
+// products with B take; zeros behind the adapter's rank.
+__global__ __launch_bounds__(kThreads) void skinny_lora_join(const LoraArgs a, int padded) {
+  const int quads = padded / 4;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const int r = (int)(i % quads) * 4;
+  const long long at = i / quads;                    // slice * rows + row
+  if (at >= (long long)a.slices * a.rows) return;
+  const int slice = (int)(at / a.rows), row = (int)(at - (long long)slice * a.rows);
+  const int e = a.ids[row];
+  bool bare = true;
+#pragma unroll
+  for (int s = 0; s < kMaxSlices; ++s)
+    if (s == slice) bare = !a.a[s];
+  if (e < 0 || e >= a.adapters || bare) return;
+  const int rank = a.ranks ? min(max(a.ranks[e], 0), a.rank) : a.rank;
+  const float scale = a.scale ? a.scale[e] : 1.0f;
+  const size_t step = (size_t)a.slices * a.rows * a.rank;
+  const float* src = a.part + (size_t)at * a.rank + r;
+  f32x4 s{0, 0, 0, 0};
+  if (r < rank)
+#pragma unroll 8
+    for (int k = 0; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(src + k * step);
+  unsigned h[2], l[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const float x = r + 2 * p < rank ? s[2 * p] * scale : 0.0f;
+    const float y = r + 2 * p + 1 < rank ? s[2 * p + 1] * scale : 0.0f;
+    h[p] = upper_halves(x, y);
+    l[p] = pack_bf16(rest_of(x, bf16_lo(h[p])), rest_of(y, bf16_hi(h[p])));
+  }
+  __bf16* dst = a.low + (size_t)at * 2 * padded + r;
+  *reinterpret_cast<u32x2*>(dst) = u32x2{h[0], h[1]};
+  *reinterpret_cast<u32x2*>(dst + padded) = u32x2{l[0], l[1]};
+}
+
+// The columns of B that one wave multiplies: product j's row i is column 32 (j / 2) +
+// 8 (i / 4) + 4 (j % 2) + i % 4, so that a lane ends with two runs of 8 neighbouring
+// columns of one row of y, 32 apart, and four lanes with 32 neighbouring ones.
+template <int KS>
+struct Columns {
+  u32x4 w[KS][4];
+  __device__ __forceinline__ void load(const __bf16* b, int pool, int rank, int n0, int n) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const auto column = [&](int j, int i) {
+      return min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), n - 1);
+    };
+    if constexpr (KS == 1) {           // rows of up to 64 bytes, side by side
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[0][j] = 8 * g < rank ? *reinterpret_cast<const u32x4*>(b + (size_t)column(j, c) * pool + 8 * g)
+                               : u32x4{0, 0, 0, 0};
     } else {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (e < cols) a.y[at + e] = (__bf16)((float)a.base[at + e] + acc[t][e / 4][e % 4]);
-    }
-  }
-}
-
-// Rows that have no adapter, in the workgroup's columns.
-__device__ __forceinline__ void copy_rows(const LoraArgs& a, unsigned long long lanes, int block,
-                                          int col, int cols) {
-  while (lanes) {
-    const int l = __builtin_ctzll(lanes);
-    lanes &= lanes - 1;
-    const size_t at = (size_t)(block * kRowBlock + l) * a.N + col;
-    for (int i = threadIdx.x; i < cols; i += kThreads) a.y[at + i] = a.base[at + i];
-  }
-}
-
-__global__ __launch_bounds__(kThreads) void skinny_lora_expand(const LoraArgs a) {
-  __shared__ int list[kRowBlock];
-  extern __shared__ __attribute__((aligned(16))) unsigned low[];   // A x in two parts
-  int i = blockIdx.x;
-  const int tiles = a.tile[a.slices];
-  const int tile = i % tiles;
-  i /= tiles;
-  const int ordinal = i % a.ordinals;
-  const int block = i / a.ordinals;
-  int slice = 0;
-  while (tile >= a.tile[slice + 1]) ++slice;
-  const int n = a.n[slice], col = a.col[slice];
-  const int tile0 = (tile - a.tile[slice]) * kCols * kWaves;
-  const int lane_tile = tile0 + uniform(threadIdx.x >> 6) * kCols;
-  const int width = min(n - tile0, kCols * kWaves);
-  const bool bare = !a.a[slice];
-  const int padded = (a.rank + 31) / 32 * 32;
-  const int stride = padded / 2 + 4;                 // dwords of a row, kept off the same banks
-  unsigned* hi = low;
-  unsigned* lo = low + kRowBlock * stride;
-
-  Adapters all(a, block);
-  unsigned long long rest = all.none;
-  if (bare) rest |= all.rest;
-  if (a.copy && ordinal == 0 && rest) copy_rows(a, rest, block, col + tile0, width);
-  if (bare) return;
-  for (int d = 0; all.rest; ++d) {
-    const Group grp = all.next();
-    if (d % a.ordinals != ordinal) continue;
-    const int rank = rank_of(a, grp.adapter);
-    if (rank == 0) {
-      if (a.copy) copy_rows(a, grp.lanes, block, col + tile0, width);
-      continue;
-    }
-    list_rows(grp, block, list);
-    __syncthreads();
-    const int count = __popcll(grp.lanes);
-    const float scale = a.scale ? a.scale[grp.adapter] : 1.0f;
-    // Pairs of ranks of every row, up to a whole product of 32.
-    const int pairs = (rank + 31) / 32 * 16, tall = (count + 15) / 16 * 16;
-    for (int p = threadIdx.x; p < tall * pairs; p += kThreads) {
-      const int row = p / pairs, r = p % pairs * 2;
-      float s0 = 0.0f, s1 = 0.0f;
-      if (row < count && r < rank) {
-        const float* src = a.part + ((size_t)slice * a.rows + list[row]) * a.rank + r;
-        for (int k = 0; k < a.splits; ++k) {
-          const float2 v = *reinterpret_cast<const float2*>(
-              src + (size_t)k * a.slices * a.rows * a.rank);
-          s0 += v.x;
-          s1 += v.y;
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __bf16* row = b + (size_t)column(j, 8 * h + line_row()) * pool;
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            const int r = 32 * k + 8 * line_part();
+            w[k + h][j] = r < rank ? *reinterpret_cast<const u32x4*>(row + r) : u32x4{0, 0, 0, 0};
+          }
         }
-        s0 *= scale;
-        s1 = r + 1 < rank ? s1 * scale : 0.0f;
+    }
+  }
+  // As the products take them.
+  __device__ __forceinline__ void turn() {
+    if constexpr (KS > 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          const Lines l = Lines{{w[k][j], w[k + 1][j]}}.turned();
+          w[k][j] = l.x[0];
+          w[k + 1][j] = l.x[1];
+        }
+  }
+  // Columns past the adapter's own rank count as 0, whatever they hold.
+  __device__ __forceinline__ void cut(int rank) {
+    turn();
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 32 * k + 8 * g + 2 * e;
+          if (r >= rank) w[k][j][e] = 0;
+          else if (r + 1 >= rank) w[k][j][e] &= 0xffffu;
+        }
+  }
+};
+
+// A x of a group's rows, summed over the splits in order, times the scale, as two
+// bf16 numbers each: row t's at dwords t * stride of hi and lo, zeros behind the rank.
+constexpr int kMaxSplits = 8;
+__device__ __forceinline__ void stage(const LoraArgs& a, int slice, int rank, int padded, int count,
+                                      const int* list, float scale, f32x4* sums, unsigned* hi,
+                                      unsigned* lo, int stride) {
+  const int quads = padded / 4, items = count * quads;
+  const size_t step = (size_t)a.slices * a.rows * a.rank;
+  const auto put = [&](int row, int r, f32x4 s) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float x = r + 2 * p < rank ? s[2 * p] * scale : 0.0f;
+      const float y = r + 2 * p + 1 < rank ? s[2 * p + 1] * scale : 0.0f;
+      const unsigned h = upper_halves(x, y);
+      hi[row * stride + r / 2 + p] = h;
+      lo[row * stride + r / 2 + p] = pack_bf16(rest_of(x, bf16_lo(h)), rest_of(y, bf16_hi(h)));
+    }
+  };
+  const auto source = [&](int item, int& row, int& r) {
+    row = item / quads;
+    r = (item - row * quads) * 4;
+    return a.part + ((size_t)slice * a.rows + list[row]) * a.rank + min(r, a.rank - 4);
+  };
+  if (items > kThreads / kMaxSplits) {
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      int row, r;
+      const float* src = source(i, row, r);
+      f32x4 s = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll
+      for (int k = 1; k < kMaxSplits; ++k)
+        if (k < a.splits) s += *reinterpret_cast<const f32x4*>(src + k * step);
+      put(row, r, s);
+    }
+    return;
+  }
+  // Few items: a thread for each split.
+  constexpr int lanes = kThreads / kMaxSplits;
+  const int k = threadIdx.x / lanes, i = threadIdx.x % lanes;
+  int row = 0, r = 0;
+  f32x4 s{0, 0, 0, 0};
+  if (i < items && k < a.splits)
+    s = *reinterpret_cast<const f32x4*>(source(i, row, r) + k * step);
+  sums[threadIdx.x] = s;
+  __syncthreads();
+  if (i < items && k == 0) {
+#pragma unroll
+    for (int j = 1; j < kMaxSplits; ++j) s += sums[j * lanes + threadIdx.x];
+    put(row, r, s);
+  }
+}
+
+// 16 rows' part of base or y, a wave's 64 columns, in whole lines: a lane has 8
+// neighbouring columns, `left` of them in the slice, of two rows.
+struct Tile {
+  size_t at[2];
+  Lines l;
+};
+__device__ __forceinline__ Tile load_base(const LoraArgs& a, const int* list, int t, int count,
+                                          int column, int left) {
+  Tile b;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    b.at[h] = (size_t)list[min(t + 8 * h + line_row(), count - 1)] * a.N + column;
+    const unsigned short* src = (const unsigned short*)a.base + b.at[h];
+    b.l.x[h] = u32x4{0, 0, 0, 0};
+    if (left >= 8) {
+      b.l.x[h] = *reinterpret_cast<const u32x4_any*>(src);
+    } else if (left > 0) {             // the last ones again behind them
+      unsigned v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = src[min(e, left - 1)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b.l.x[h][e] = v[2 * e] | v[2 * e + 1] << 16;
+    }
+  }
+  return b;
+}
+__device__ __forceinline__ void store_y(const LoraArgs& a, const Tile& b, int t, int count, int left) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (t + 8 * h + line_row() >= count) continue;
+    if (left >= 8) {
+      *reinterpret_cast<u32x4_any*>(a.y + b.at[h]) = b.l.x[h];
+    } else if (left > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left)
+          ((unsigned short*)a.y)[b.at[h] + e] = (unsigned short)(b.l.x[h][e / 2] >> (16 * (e % 2)));
+    }
+  }
+}
+
+// y of a group's rows in the wave's columns, 16 rows at a time; what the next 16
+// are added to comes while the products run.
+template <int KS, bool LINES, typename Low>
+__device__ __forceinline__ void expand(const LoraArgs& a, const Columns<KS>& b, int column, int left,
+                                       int count, const int* list, Tile next, Low low) {
+  u32x4 ahead[KS][2];
+  low(0, ahead);
+  for (int t = 0; t < count; t += 16) {
+    Tile here = next;
+    u32x4 v[KS][2];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      if constexpr (LINES) {           // line i of the rows: their first parts, then their second
+        const Lines l = Lines{{ahead[i][0], ahead[i][1]}}.turned();
+        const int k = KS == 1 ? 0 : 2 * i % KS, p = KS == 1 ? 0 : 2 * i / KS;
+        v[k][p] = l.x[0];
+        v[KS == 1 ? 0 : k + 1][KS == 1 ? 1 : p] = l.x[1];
+      } else {
+        v[i][0] = ahead[i][0];
+        v[i][1] = ahead[i][1];
       }
-      // The upper half of the fp32 number, and what that leaves of it, rounded.
-      const unsigned h = upper_halves(s0, s1);
-      hi[row * stride + r / 2] = h;
-      lo[row * stride + r / 2] = pack_bf16(rest_of(s0, bf16_lo(h)), rest_of(s1, bf16_hi(h)));
     }
-    __syncthreads();
-    const __bf16* w = a.b[slice] + (size_t)grp.adapter * n * a.rank;
-    if (lane_tile < n) {
-      if (count <= 16) expand<1>(a, w, rank, lane_tile, n, col, count, list, hi, lo, stride);
-      else if (count <= 32) expand<2>(a, w, rank, lane_tile, n, col, count, list, hi, lo, stride);
-      else expand<4>(a, w, rank, lane_tile, n, col, count, list, hi, lo, stride);
+    if (t + 16 < count) {
+      next = load_base(a, list, t + 16, count, column, left);
+      low(t + 16, ahead);
     }
+    f32x4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], v[k][p], acc[j]);
+    here.l = here.l.turned();
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned y = here.l.x[p][e];
+        here.l.x[p][e] = pack_bf16(bf16_lo(y) + acc[2 * p + e / 2][2 * (e % 2)],
+                                   bf16_hi(y) + acc[2 * p + e / 2][2 * (e % 2) + 1]);
+      }
+    here.l = here.l.turned();
+    store_y(a, here, t, count, left);
+  }
+}
+
+// Rows without an adapter, in the wave's columns.
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, int column, int left, int count,
+                                          const int* list) {
+#pragma unroll 4
+  for (int t = 0; t < count; t += 16)
+    store_y(a, load_base(a, list, t, count, column, left), t, count, left);
+}
+
+// The part of y that a workgroup writes: a wave's 64 columns of a slice from wave0 on,
+// of which a lane has 8 from `column` of y on, with `left` left in the slice.
+struct Part {
+  int slice, n, wave0, column, left;
+  __device__ __forceinline__ Part(const LoraArgs& a, int tile) {
+    slice = 0;
+    while (tile >= a.tile[slice + 1]) ++slice;
+    n = a.n[slice];
+    wave0 = ((tile - a.tile[slice]) * kWaves + uniform(threadIdx.x >> 6)) * kCols;
+    column = a.col[slice] + wave0 + 8 * line_part();
+    left = n - wave0 - 8 * line_part();
+  }
+};
+
+// STAGE: A x is summed over the splits here, by every workgroup for its rows; else it
+// was joined before.
+template <int KS, bool STAGE>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(KS <= 2 ? 4 : KS == 4 ? 2 : 1)))
+void skinny_lora_expand(const LoraArgs a) {
+  __shared__ int list[kRowBlock];
+  __shared__ __attribute__((aligned(16))) f32x4 sums[STAGE ? kThreads : 1];
+  extern __shared__ __attribute__((aligned(16))) unsigned staged[];    // A x in two parts
+  constexpr int padded = 32 * KS;
+  // Workgroups go to the eight XCDs in turn; each XCD takes a run of neighbouring
+  // parts of the same rows.
+  const int i = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+  const int tiles = a.tile[a.slices];
+  const int block = i / tiles;
+  if (block >= a.most_blocks) return;
+  const Block bl(a, block);
+  if (bl.count == 0) return;
+  const Part p(a, i - block * tiles);
+  bl.rows(a, list);
+  if (bl.rank == 0 || !a.a[p.slice]) {
     __syncthreads();
+    if (a.copy && p.wave0 < p.n) copy_rows(a, p.column, p.left, bl.count, list);
+    return;
+  }
+  Columns<KS> b;
+  b.load(a.b[p.slice] + (size_t)bl.adapter * p.n * a.rank, a.rank, bl.rank, p.wave0, p.n);
+  const float scale = STAGE && a.scale ? a.scale[bl.adapter] : 1.0f;
+  __syncthreads();
+  const Tile base = load_base(a, list, 0, bl.count, p.column, p.left);
+  if constexpr (STAGE) {
+    constexpr int stride = padded / 2 + 4;           // dwords of a row, kept off the same banks
+    unsigned* hi = staged;
+    unsigned* lo = staged + kRowBlock * stride;
+    stage(a, p.slice, bl.rank, padded, bl.count, list, scale, sums, hi, lo, stride);
+    b.cut(bl.rank);
+    __syncthreads();
+    if (p.wave0 >= p.n) return;
+    expand<KS, false>(a, b, p.column, p.left, bl.count, list, base, [&](int t, u32x4(&v)[KS][2]) {
+      const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int at = (t + c) * stride + 16 * k + 4 * g;
+        v[k][0] = *reinterpret_cast<const u32x4*>(hi + at);
+        v[k][1] = *reinterpret_cast<const u32x4*>(lo + at);
+      }
+    });
+  } else {
+    if (p.wave0 >= p.n) return;
+    b.cut(bl.rank);
+    expand<KS, true>(a, b, p.column, p.left, bl.count, list, base, [&](int t, u32x4(&v)[KS][2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const __bf16* src =
+            a.low + ((size_t)p.slice * a.rows + list[min(t + 8 * h + line_row(), bl.count - 1)]) * 2 *
+                        padded + 8 * line_part();
+#pragma unroll
+        for (int i = 0; i < KS; ++i) v[i][h] = *reinterpret_cast<const u32x4*>(src + 64 * i);
+      }
+    });
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 
-struct Cut {
-  int splits, pieces, rank_tiles, ordinals;
-};
-
 // How a call is cut: from the sizes alone, so that the workspace is known.
+struct Cut {
+  bool few;                            // one row block, no launch to group the rows
+  bool join;                           // A x is joined by a launch of its own
+  int tiles;                           // of 16 ranks in a workgroup (few) or a wave (many)
+  int groups;                          // of them
+  int splits, pieces, ordinals, most_blocks;
+};
+constexpr int kFewGroups = 256;        // workgroups to cut a call into, if it is long enough
+constexpr int kManyGroups = 512;
+constexpr int kJoinRows = 512;         // up to here every workgroup sums its rows' splits itself
 Cut cut_of(const skinny_lora& l, int rows) {
-  Cut c;
+  Cut c{};
   const int blocks = (rows + kRowBlock - 1) / kRowBlock;
-  const int rank_tiles = (l.rank + 15) / 16;
-  c.rank_tiles = rank_tiles >= 4 ? 4 : rank_tiles >= 2 ? 2 : 1;
-  const int most = rows < l.adapters ? rows : l.adapters;
-  c.ordinals = most < kRowBlock ? most : kRowBlock;
-  if (blocks > 4) c.ordinals = c.ordinals < 8 ? c.ordinals : 8;
-  if (blocks > 32) c.ordinals = c.ordinals < 2 ? c.ordinals : 2;
+  const int per = (l.rank + 15) / 16;                // rank tiles of a slice
   const int pieces = (l.K + kPiece - 1) / kPiece;
-  const long long items = (long long)blocks * (blocks > 4 ? 1 : c.ordinals) * l.slices *
-                          ((rank_tiles + c.rank_tiles - 1) / c.rank_tiles);
-  long long splits = (512 + items - 1) / items;
-  const int whole = (pieces + kWaves - 1) / kWaves;  // one piece per wave
-  if (splits > whole) splits = whole;
-  if (splits < 1) splits = 1;
+  const int most = rows < l.adapters ? rows : l.adapters;
+  c.few = blocks == 1;
+  long long splits;
+  if (c.few) {
+    c.ordinals = most < kRowBlock ? most : kRowBlock;
+    c.most_blocks = c.ordinals + 1;                  // the last one: rows without an adapter
+    splits = (pieces + kFewWaves - 1) / kFewWaves;   // one piece per wave
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    c.tiles = per >= 4 ? 4 : per >= 2 ? 2 : 1;
+    while (c.tiles > 1 && c.ordinals * l.slices * splits * ((per + c.tiles - 1) / c.tiles) < kFewGroups)
+      c.tiles /= 2;
+    c.groups = (per + c.tiles - 1) / c.tiles;
+  } else {
+    c.join = rows > kJoinRows;
+    // Each kind of rows, those without an adapter among them, may end in part of a block.
+    c.most_blocks = blocks + (rows < l.adapters + 1 ? rows : l.adapters + 1);
+    if (c.most_blocks > rows) c.most_blocks = rows;
+    int slices = 0;
+    for (int i = 0; i < l.slices; ++i) slices += l.a[i] != nullptr;
+    const int waves = (slices * per + kWaves - 1) / kWaves;        // tiles per wave
+    c.groups = (waves + 3) / 4;
+    c.tiles = (waves + c.groups - 1) / c.groups;
+    splits = kManyGroups / ((long long)blocks * c.groups);
+    const int whole = (pieces + 7) / 8;              // four stages
+    if (splits > whole) splits = whole;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits < 1) splits = 1;
+  }
   c.pieces = (int)((pieces + splits - 1) / splits);
+  if (!c.few) c.pieces = (c.pieces + 1) / 2 * 2;     // whole stages
   c.splits = (pieces + c.pieces - 1) / c.pieces;
   return c;
+}
+
+int padded_rank(const skinny_lora& l) {
+  return l.rank <= 32 ? 32 : l.rank <= 64 ? 64 : l.rank <= 128 ? 128 : 256;
 }
 
 skinny_status check_lora(const skinny_lora* l, int rows, long long* width) {
@@ -393,7 +870,7 @@ skinny_status check_lora(const skinny_lora* l, int rows, long long* width) {
     any = any || l->a[i];
   }
   if (!any) return SKINNY_ERR_INVALID_ARG;
-  if (rows > SKINNY_LORA_MAX_ROWS || l->adapters > 65536 || l->rank % 8 != 0 ||
+  if (rows > SKINNY_LORA_MAX_ROWS || l->adapters > SKINNY_LORA_MAX_ADAPTERS || l->rank % 8 != 0 ||
       l->rank > SKINNY_LORA_MAX_RANK || l->K % 8 != 0 || l->K > (1 << 28) || n > (1 << 28))
     return SKINNY_ERR_UNSUPPORTED;
   if (!aligned(l->ranks, 4) || !aligned(l->scale, 4)) return SKINNY_ERR_UNSUPPORTED;
@@ -401,10 +878,37 @@ skinny_status check_lora(const skinny_lora* l, int rows, long long* width) {
   return SKINNY_OK;
 }
 
-size_t workspace_of(const skinny_lora& l, int rows) {
-  const Cut c = cut_of(l, rows);
-  const size_t bytes = (size_t)c.splits * l.slices * rows * l.rank * sizeof(float);
-  return bytes > SKINNY_MIN_WORKSPACE_BYTES ? bytes : SKINNY_MIN_WORKSPACE_BYTES;
+// The workspace's parts, each 16-byte aligned.
+struct Space {
+  size_t low, blocks, order, bytes;
+  Space(const skinny_lora& l, const Cut& c, int rows) {
+    const size_t all = (size_t)l.slices * rows;
+    low = c.splits * all * l.rank * sizeof(float);
+    blocks = low + (c.join ? all * 2 * padded_rank(l) * sizeof(__bf16) : 0);
+    order = blocks + (size_t)c.most_blocks * sizeof(int4);
+    bytes = order + (c.few ? (size_t)c.most_blocks * kRowBlock : (size_t)rows) * sizeof(int);
+    if (bytes < SKINNY_MIN_WORKSPACE_BYTES) bytes = SKINNY_MIN_WORKSPACE_BYTES;
+  }
+};
+
+size_t workspace_of(const skinny_lora& l, int rows) { return Space(l, cut_of(l, rows), rows).bytes; }
+
+template <int KS, bool STAGE>
+skinny_status launch_expand(const LoraArgs& a, unsigned grid, hipStream_t stream) {
+  constexpr int lds = STAGE ? 2 * kRowBlock * (16 * KS + 4) * (int)sizeof(unsigned) : 0;
+  if (lds > 56 * 1024 &&               // beside the sums, more than a launch may have unasked
+      hipFuncSetAttribute((const void*)skinny_lora_expand<KS, STAGE>,
+                          hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+    return SKINNY_ERR_HIP;
+  hipLaunchKernelGGL((skinny_lora_expand<KS, STAGE>), dim3(grid), dim3(kThreads), lds, stream, a);
+  return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
+}
+template <bool STAGE>
+skinny_status launch_expand(const LoraArgs& a, int padded, unsigned grid, hipStream_t stream) {
+  if (padded == 32) return launch_expand<1, STAGE>(a, grid, stream);
+  if (padded == 64) return launch_expand<2, STAGE>(a, grid, stream);
+  if (padded == 128) return launch_expand<4, STAGE>(a, grid, stream);
+  return launch_expand<8, STAGE>(a, grid, stream);
 }
 
 }  // namespace
@@ -464,7 +968,12 @@ skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const i
   a.slices = l.slices;
   a.splits = c.splits;
   a.pieces = c.pieces;
-  a.rank_groups = (l.rank + 16 * c.rank_tiles - 1) / (16 * c.rank_tiles);
+  const Space space(l, c, rows);
+  a.low = (__bf16*)((char*)workspace + space.low);
+  a.order = (int*)((char*)workspace + space.order);
+  a.blocks = (int4*)((char*)workspace + space.blocks);
+  a.most_blocks = c.most_blocks;
+  a.rank_groups = c.groups;
   a.ordinals = c.ordinals;
   a.copy = base != y;
   int col = 0, tile = 0;
@@ -480,10 +989,13 @@ skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const i
   }
   a.tile[kMaxSlices] = tile;
   for (int i = l.slices; i < kMaxSlices; ++i) a.tile[i] = tile;
-  const long long blocks = (rows + kRowBlock - 1) / kRowBlock;
-  const long long first = blocks * a.ordinals * a.slices * a.rank_groups * a.splits;
-  const long long second = blocks * a.ordinals * tile;
-  if (first * kThreads > 0xffffffffLL || second * kThreads > 0xffffffffLL)   // threads of a launch
+  const long long first = c.few ? (long long)a.ordinals * a.slices * a.rank_groups * a.splits
+                                : ((long long)c.most_blocks * a.rank_groups * a.splits + 7) / 8 * 8;
+  const long long second = ((long long)c.most_blocks * tile + 7) / 8 * 8;
+  const int padded = padded_rank(l);
+  const long long join = ((long long)l.slices * rows * (padded / 4) + kThreads - 1) / kThreads;
+  if (first * (c.few ? 64 * kFewWaves : kThreads) > 0xffffffffLL ||      // threads of a launch
+      second * kThreads > 0xffffffffLL || join * kThreads > 0xffffffffLL)
     return SKINNY_ERR_UNSUPPORTED;
   DeviceInfo d;
   st = device_info(&d);
@@ -491,19 +1003,25 @@ skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const i
   if (!d.gfx950) return SKINNY_ERR_UNSUPPORTED;
 
   const hipStream_t hs = (hipStream_t)stream;
-  const dim3 grid((unsigned)first), threads(kThreads);
-  if (c.rank_tiles == 1) hipLaunchKernelGGL(skinny_lora_shrink<1>, grid, threads, 0, hs, a);
-  else if (c.rank_tiles == 2) hipLaunchKernelGGL(skinny_lora_shrink<2>, grid, threads, 0, hs, a);
-  else hipLaunchKernelGGL(skinny_lora_shrink<4>, grid, threads, 0, hs, a);
+  const dim3 grid((unsigned)first), few(64 * kFewWaves), many(kThreads);
+  if (c.few) {
+    if (c.tiles == 1) hipLaunchKernelGGL(skinny_lora_shrink_few<1>, grid, few, 0, hs, a);
+    else if (c.tiles == 2) hipLaunchKernelGGL(skinny_lora_shrink_few<2>, grid, few, 0, hs, a);
+    else hipLaunchKernelGGL(skinny_lora_shrink_few<4>, grid, few, 0, hs, a);
+  } else {
+    hipLaunchKernelGGL(skinny_lora_group, dim3(1), dim3(kGroupThreads),
+                       (size_t)(l.adapters + 1) * sizeof(int), hs, a);
+    if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
+    if (c.tiles == 1) hipLaunchKernelGGL(skinny_lora_shrink_many<1>, grid, many, 0, hs, a);
+    else if (c.tiles == 2) hipLaunchKernelGGL(skinny_lora_shrink_many<2>, grid, many, 0, hs, a);
+    else if (c.tiles == 3) hipLaunchKernelGGL(skinny_lora_shrink_many<3>, grid, many, 0, hs, a);
+    else hipLaunchKernelGGL(skinny_lora_shrink_many<4>, grid, many, 0, hs, a);
+    if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
+    if (c.join) hipLaunchKernelGGL(skinny_lora_join, dim3((unsigned)join), many, 0, hs, a, padded);
+  }
   if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
-  const int padded = (l.rank + 31) / 32 * 32;
-  const size_t lds = (size_t)2 * kRowBlock * (padded / 2 + 4) * sizeof(unsigned);
-  if (lds > 60 * 1024 &&               // beside the list, more than a launch may have unasked
-      hipFuncSetAttribute((const void*)skinny_lora_expand,
-                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
-    return SKINNY_ERR_HIP;
-  hipLaunchKernelGGL(skinny_lora_expand, dim3((unsigned)second), threads, lds, hs, a);
-  return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
+  return c.join ? launch_expand<false>(a, padded, (unsigned)second, hs)
+                : launch_expand<true>(a, padded, (unsigned)second, hs);
 }
 
 }  // extern "C"

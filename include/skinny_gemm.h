@@ -704,8 +704,8 @@ skinny_status skinny_block_norm(const skinny_norm* norm, void* stream);
  *             whatever they hold
  *   scale     [adapters] fp32, or NULL: 1
  *   ids       [rows] int32, device, read by the kernels; any values
- * Each adapter's weights are read once for all of its rows among 64 neighbouring
- * ones.  Sums are fp32; A x, as fp32, enters the product with B as two bf16 numbers, within
+ * Rows of one adapter share the reading of its weights, 64 at a time.  Sums are fp32;
+ * A x, as fp32, enters the product with B as two bf16 numbers, within
  * 2^-16; y is rounded once.  A row's result does not depend on the other rows'
  * values; results are bitwise reproducible for the same sizes.
  *   workspace >= skinny_lora_workspace_bytes(lora, rows) bytes (0 for invalid
@@ -714,9 +714,10 @@ skinny_status skinny_block_norm(const skinny_norm* norm, void* stream);
  * y and the workspace must not overlap anything else. */
 #define SKINNY_LORA_MAX_ROWS 1048576
 #define SKINNY_LORA_MAX_RANK 256
+#define SKINNY_LORA_MAX_ADAPTERS 8192
 #define SKINNY_LORA_MAX_SLICES 4
 typedef struct skinny_lora {
-  int adapters;         /* 1 .. 65536                     */
+  int adapters;         /* 1 .. SKINNY_LORA_MAX_ADAPTERS  */
   int rank;             /* 8 .. SKINNY_LORA_MAX_RANK      */
   int K;
   int slices;           /* 1 .. SKINNY_LORA_MAX_SLICES    */
