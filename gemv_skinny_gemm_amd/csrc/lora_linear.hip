@@ -19,6 +19,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));   // y's rows of an odd width
+typedef u32x4 u32x4_dword __attribute__((aligned(4)));
+typedef unsigned u32x3 __attribute__((ext_vector_type(3)));
+typedef u32x3 u32x3_dword __attribute__((aligned(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
@@ -42,6 +45,7 @@ struct LoraArgs {
                                        // none): adapter, first place in order, rows, its rank
   int* order;                          // row numbers
   int most_blocks;
+  int chunk_rows, chunk_blocks;        // many rows: those that are ordered together
   const __bf16* a[kMaxSlices];
   const __bf16* b[kMaxSlices];
   int n[kMaxSlices], col[kMaxSlices];  // columns of a slice, and the first one's number in y
@@ -70,27 +74,51 @@ __device__ __forceinline__ float bf16_hi(unsigned u) {
 
 // 128 bytes of each of 16 rows in two registers' worth of 16 bytes per lane: as the
 // products take them, lane (c, g) has parts g and g + 4 of row c; as they are loaded
-// and stored, in whole lines, parts g + 4 (c / 8) of rows c % 8 and c % 8 + 8.  A load
-// of half lines costs the L1 cache as much as one of whole lines (an instruction of
-// 16 half lines 66 cycles of a CU, one of 8 whole ones 23).
+// and stored, part l % 8 of rows l / 8 and l / 8 + 8, neighbouring lanes the parts of a
+// row.  A load's cost in the L1 cache goes by the lines that each 16 neighbouring lanes
+// touch: 16 rows apart an instruction of 1 KB takes some 66 cycles of a CU, 256 bytes in
+// a row some 23.  The wave turns one form into the other in a buffer of its own; its
+// accesses to shared memory are done in order.
+constexpr int kTurn = 128;             // 16-byte parts of the buffer
+__device__ __forceinline__ int line_row() { return (threadIdx.x & 63) >> 3; }
+__device__ __forceinline__ int line_part() { return threadIdx.x & 7; }
+__device__ __forceinline__ void in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 struct Lines {
   u32x4 x[2];
-  template <int BANKS>
-  static __device__ __forceinline__ u32x4 exchange(u32x4 own, u32x4 other) {
-    u32x4 r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)        // lane c ^ 8's, in lanes 8 .. 15 or 0 .. 7 of each 16
-      r[e] = __builtin_amdgcn_update_dpp((int)own[e], (int)other[e], 0x128, 0xf, BANKS, false);
-    return r;
+  // Two rows fill the banks once: parts are turned by the number of their pair.
+  static __device__ __forceinline__ int place(int row, int part) {
+    return row * 8 + (part ^ (row >> 1));
   }
-  // From one form to the other, either way.
-  __device__ __forceinline__ Lines turned() const {
-    return Lines{{exchange<0xc>(x[0], x[1]), exchange<0x3>(x[1], x[0])}};
+  __device__ __forceinline__ void to_products(u32x4* buf) {
+    const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    in_order();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) buf[place(line_row() + 8 * h, line_part())] = x[h];
+    in_order();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x[h] = buf[place(c, g + 4 * h)];
+  }
+  __device__ __forceinline__ void to_lines(u32x4* buf) {
+    const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    in_order();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) buf[place(c, g + 4 * h)] = x[h];
+    in_order();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x[h] = buf[place(line_row() + 8 * h, line_part())];
   }
 };
-__device__ __forceinline__ int line_row() { return threadIdx.x & 7; }
-__device__ __forceinline__ int line_part() {
-  return ((threadIdx.x & 63) >> 4) + ((threadIdx.x & 8) >> 1);
+// The same of 64 bytes of each of 16 rows, which a lane has one part of: l % 4 of row
+// l / 4, or g of row c.
+__device__ __forceinline__ void narrow_to_products(u32x4& x, u32x4* buf) {
+  const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
+  in_order();
+  buf[l / 4 * 4 + ((l % 4) ^ (l >> 4))] = x;
+  in_order();
+  x = buf[c * 4 + (g ^ (c >> 2))];
 }
 
 __device__ __forceinline__ unsigned upper_halves(float a, float b) {
@@ -119,7 +147,7 @@ constexpr int kSumTiles = 4;           // tiles that the waves add up at a time
 template <int MT, int RT>
 __device__ __forceinline__ void shrink(const LoraArgs& a, const __bf16* w, int rank, int r0,
                                        int count, int split, int slice, const int* list,
-                                       float* sums) {
+                                       u32x4* turn, float* sums) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   f32x4 acc[MT * RT];
@@ -140,19 +168,27 @@ __device__ __forceinline__ void shrink(const LoraArgs& a, const __bf16* w, int r
   for (int k = (split * a.pieces + wave) * kPiece; k < end; k += kFewWaves * kPiece) {
     Lines xf[RT], wf[MT];
     const bool in = k + lp < end;
+    const int at = in ? k : -lp;       // chunks behind K's end: the row's first, and zeros for it
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        wf[m].x[h] = in ? *reinterpret_cast<const u32x4*>(wp[m][h] + k) : u32x4{0, 0, 0, 0};
+      for (int m = 0; m < MT; ++m) wf[m].x[h] = *reinterpret_cast<const u32x4*>(wp[m][h] + at);
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-        xf[t].x[h] = in ? *reinterpret_cast<const u32x4*>(xp[t][h] + k) : u32x4{0, 0, 0, 0};
+      for (int t = 0; t < RT; ++t) xf[t].x[h] = *reinterpret_cast<const u32x4*>(xp[t][h] + at);
+    }
+    if (k + kPiece > end) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) wf[m].x[h] = in ? wf[m].x[h] : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < RT; ++t) xf[t].x[h] = in ? xf[t].x[h] : u32x4{0, 0, 0, 0};
+      }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) wf[m] = wf[m].turned();
+    for (int m = 0; m < MT; ++m) wf[m].to_products(turn);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) xf[t] = xf[t].turned();
+    for (int t = 0; t < RT; ++t) xf[t].to_products(turn);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -187,6 +223,8 @@ template <int MT>
 __global__ __launch_bounds__(64 * kFewWaves) void skinny_lora_shrink_few(const LoraArgs a) {
   __shared__ int list[kRowBlock];
   __shared__ __attribute__((aligned(16))) float sums[kFewWaves * kSumTiles * 256];
+  __shared__ __attribute__((aligned(16))) u32x4 turns[kFewWaves][kTurn];
+  u32x4* turn = turns[threadIdx.x >> 6];
   int i = blockIdx.x;
   const int split = i % a.splits;
   i /= a.splits;
@@ -228,13 +266,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void skinny_lora_shrink_few(const L
   __syncthreads();
   const __bf16* w = a.a[slice] + (size_t)adapter * a.rank * a.K;
   if (count <= 16) {
-    shrink<MT, 1>(a, w, rank, r0, count, split, slice, list, sums);
+    shrink<MT, 1>(a, w, rank, r0, count, split, slice, list, turn, sums);
   } else {
     constexpr int H = MT > 2 ? 2 : MT;               // registers for two tiles of ranks by 64 rows
 #pragma unroll
     for (int m = 0; m < MT; m += H)
       if (r0 + 16 * m < rank)
-        shrink<H, 4>(a, w, rank, r0 + 16 * m, count, split, slice, list, sums);
+        shrink<H, 4>(a, w, rank, r0 + 16 * m, count, split, slice, list, turn, sums);
   }
 }
 
@@ -246,12 +284,15 @@ constexpr int kStage = 128;            // values of K
 constexpr int kChunks = kStage / 8;    // 16-byte chunks of a row's stage
 template <int MT, int RT>
 __device__ __forceinline__ void shrink_rows(const LoraArgs& a, int adapter, int rank, int count,
-                                            int split, int pass, const int* list, u32x4* xs) {
+                                            int split, int pass, const int* list, u32x4* xs,
+                                            u32x4* turn) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int per = (a.rank + 15) / 16;                // tiles of a slice
-  // The wave's tiles: of which slice, and their first rank.
-  const __bf16* wp[MT][2];
+  // The wave's tiles: of which slice (-1: none), their first rank, and where a lane's
+  // part of their rows lies.
+  const unsigned char* wp[MT];
+  unsigned off[MT][2];
   int slice[MT], r0[MT];
   bool any = false;
 #pragma unroll
@@ -259,25 +300,22 @@ __device__ __forceinline__ void shrink_rows(const LoraArgs& a, int adapter, int 
     int tile = (pass * MT + m) * kWaves + wave;
     slice[m] = -1;
     r0[m] = 0;
-    for (int s = 0; s < a.slices; ++s) {
-      if (!a.a[s]) continue;
-      if (tile >= 0 && tile < per) {
+    wp[m] = (const unsigned char*)a.x;               // nothing to read: any row will do
+#pragma unroll
+    for (int s = 0; s < kMaxSlices; ++s) {
+      if (s >= a.slices || !a.a[s]) continue;
+      if (tile >= 0 && tile < per && 16 * tile < rank) {
         slice[m] = s;
         r0[m] = 16 * tile;
+        wp[m] = (const unsigned char*)(a.a[s] + (size_t)adapter * a.rank * a.K);
       }
       tile -= per;
     }
-    if (slice[m] >= 0 && r0[m] >= rank) slice[m] = -1;
     any = any || slice[m] >= 0;
-    const int s = max(slice[m], 0);
-    const __bf16* w = nullptr;
 #pragma unroll
-    for (int i = 0; i < kMaxSlices; ++i)
-      if (i == s) w = a.a[i];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      wp[m][h] = w + ((size_t)adapter * a.rank + min(r0[m] + 8 * h + line_row(), rank - 1)) * a.K +
-                 8 * line_part();
+    for (int h = 0; h < 2; ++h)        // below 2^31: an adapter's A has 2^30 values at most
+      off[m][h] = ((slice[m] < 0 ? 0u : (unsigned)min(r0[m] + 8 * h + line_row(), rank - 1) * (unsigned)a.K) +
+                   8 * line_part()) * 2;
   }
   f32x4 acc[MT][RT];
 #pragma unroll
@@ -293,20 +331,24 @@ __device__ __forceinline__ void shrink_rows(const LoraArgs& a, int adapter, int 
   const int begin = split * a.pieces * kPiece, end = min(begin + a.pieces * kPiece, a.K);
   u32x4 xr[RT];
   Lines wf[2][MT], wn[2][MT];
+  // K's last stage may go on behind K's end: loads there are of K's last chunk, and
+  // count as zeros when they are used.
   const auto load_x = [&](int k) {
+    const int d = min(k, a.K - 8 - 8 * chunk);
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-      xr[t] = k + 8 * chunk < end ? *reinterpret_cast<const u32x4*>(xp[t] + k) : u32x4{0, 0, 0, 0};
+    for (int t = 0; t < RT; ++t) xr[t] = *reinterpret_cast<const u32x4*>(xp[t] + d);
   };
   const auto load_w = [&](int k) {
+    unsigned d[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) d[u] = 2 * min(k + 64 * u, a.K - 8 - 8 * line_part());
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          wn[u][m].x[h] = slice[m] >= 0 && k + 64 * u + 8 * line_part() < end
-              ? *reinterpret_cast<const u32x4*>(wp[m][h] + k + 64 * u) : u32x4{0, 0, 0, 0};
+          wn[u][m].x[h] = *reinterpret_cast<const u32x4*>(wp[m] + (off[m][h] + d[u]));
   };
   load_x(begin);
   load_w(begin);
@@ -314,24 +356,49 @@ __device__ __forceinline__ void shrink_rows(const LoraArgs& a, int adapter, int 
   for (int k = begin; k < end; k += kStage) {
     u32x4* x = xs + buf * kRowBlock * kChunks;
     buf ^= 1;
+    if (k + kStage > end) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) xr[t] = k + 8 * chunk < end ? xr[t] : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            wn[u][m].x[h] = k + 64 * u + 8 * line_part() < end ? wn[u][m].x[h] : u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int t = 0; t < RT; ++t) x[(16 * t + row) * kChunks + (chunk ^ row)] = xr[t];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) wf[u][m] = wn[u][m].turned();
+      for (int m = 0; m < MT; ++m) {
+        wf[u][m] = wn[u][m];
+        wf[u][m].to_products(turn);
+      }
     __syncthreads();
-    load_x(k + kStage);
-    load_w(k + kStage);
+    if (k + kStage < end) {
+      load_x(k + kStage);
+      load_w(k + kStage);
+    }
     if (any) {
+      // The next 32 values' rows of x come while these are multiplied.
+      u32x4 xf[2][RT];
+      const auto read = [&](int u) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+        for (int t = 0; t < RT; ++t) xf[u % 2][t] = x[(16 * t + c) * kChunks + ((4 * u + g) ^ c)];
+      };
+      read(0);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const u32x4 xf = x[(16 * t + c) * kChunks + ((4 * u + g) ^ c)];
+      for (int u = 0; u < 4; ++u) {
+        if (u < 3) read(u + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[m][t] = mfma_bf16(wf[u / 2][m].x[u % 2], xf, acc[m][t]);
-        }
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            acc[m][t] = mfma_bf16(wf[u / 2][m].x[u % 2], xf[u % 2][t], acc[m][t]);
+      }
     }
   }
 #pragma unroll
@@ -368,33 +435,39 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void skinny_lora_shrink_many(const LoraArgs a) {
   __shared__ int list[kRowBlock];
   __shared__ __attribute__((aligned(16))) u32x4 xs[2 * kRowBlock * kChunks];
+  __shared__ __attribute__((aligned(16))) u32x4 turns[kWaves][kTurn];
+  u32x4* turn = turns[threadIdx.x >> 6];
   int i = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-  const int split = i % a.splits;
-  i /= a.splits;
-  const int pass = i % a.rank_groups;
-  i /= a.rank_groups;
-  if (i >= a.most_blocks) return;
-  const Block b(a, i);
+  if (i >= a.most_blocks * a.rank_groups * a.splits) return;
+  const int block = i % a.most_blocks;
+  i /= a.most_blocks;
+  const int pass = i % a.rank_groups, split = i / a.rank_groups;
+  const Block b(a, block);
   if (b.count == 0 || b.rank == 0) return;
   b.rows(a, list);
   __syncthreads();
-  if (b.count <= 16) shrink_rows<MT, 1>(a, b.adapter, b.rank, b.count, split, pass, list, xs);
-  else shrink_rows<MT, 4>(a, b.adapter, b.rank, b.count, split, pass, list, xs);
+  if (b.count <= 16) shrink_rows<MT, 1>(a, b.adapter, b.rank, b.count, split, pass, list, xs, turn);
+  else shrink_rows<MT, 4>(a, b.adapter, b.rank, b.count, split, pass, list, xs, turn);
 }
 
 // Many rows: their order by adapter, and the blocks of up to 64 that share one (the
-// blocks behind the last have no rows).  One workgroup counts in shared memory; in
-// what order the rows of one adapter come changes no result.
+// blocks behind the last have no rows).  A workgroup counts its chunk of the rows in
+// shared memory; in what order the rows of one adapter come changes no result.
 constexpr int kGroupThreads = 1024;
 __global__ __launch_bounds__(kGroupThreads) void skinny_lora_group(const LoraArgs a) {
   extern __shared__ int count[];                     // [adapters + 1], the last: without one
   __shared__ int2 waves[kGroupThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int kinds = a.adapters + 1;
+  const int row0 = blockIdx.x * a.chunk_rows, rows = min(a.rows - row0, a.chunk_rows);
+  const int block0 = blockIdx.x * a.chunk_blocks;
+  const int* ids = a.ids + row0;
+  int* order = a.order + row0;
+  int4* blocks = a.blocks + block0;
   for (int e = tid; e < kinds; e += kGroupThreads) count[e] = 0;
   __syncthreads();
   const auto kind_of = [&](int t) {
-    const int e = a.ids[t];
+    const int e = ids[t];
     return e >= 0 && e < a.adapters ? e : a.adapters;
   };
   // The place of the row among its kind's: one addition for a wave of one kind.
@@ -408,19 +481,29 @@ __global__ __launch_bounds__(kGroupThreads) void skinny_lora_group(const LoraArg
     }
     return live ? atomicAdd(&count[e], 1) : 0;
   };
-  // The first rows' kinds and places stay in registers, the others' are found twice.
-  constexpr int kKept = 8;
-  int kind[kKept], at[kKept];
+  // Rows go by kBatch times the threads, whose kinds are loaded at once.  The first
+  // batch's kinds and places stay in registers, the others' are found twice.
+  constexpr int kBatch = 8;
+  const auto load_kinds = [&](int t0, int (&kind)[kBatch]) {
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) kind[i] = kind_of(min(tid + i * kGroupThreads, a.rows - 1));
+    for (int i = 0; i < kBatch; ++i) kind[i] = kind_of(min(t0 + i * kGroupThreads, rows - 1));
+  };
+  const auto place_all = [&](int t0, const int (&kind)[kBatch], int (&at)[kBatch]) {
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const int t = tid + i * kGroupThreads;
-    at[i] = t - lane < a.rows ? place(kind[i], t < a.rows) : 0;
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = t0 + i * kGroupThreads;
+      at[i] = t - lane < rows ? place(kind[i], t < rows) : 0;
+    }
+  };
+  int kind[kBatch], at[kBatch];
+  load_kinds(tid, kind);
+  place_all(tid, kind, at);
+  __syncthreads();                     // the first batch's come first among their kind
+  for (int t0 = tid + kBatch * kGroupThreads; t0 - lane < rows; t0 += kBatch * kGroupThreads) {
+    int k[kBatch], p[kBatch];
+    load_kinds(t0, k);
+    place_all(t0, k, p);
   }
-  __syncthreads();                     // the kept rows come first among their kind
-  for (int t = tid + kKept * kGroupThreads; t - lane < a.rows; t += kGroupThreads)
-    place(kind_of(min(t, a.rows - 1)), t < a.rows);
   __syncthreads();
   // Rows and blocks of the kinds before each one's.
   const int per = (kinds + kGroupThreads - 1) / kGroupThreads;
@@ -457,26 +540,27 @@ __global__ __launch_bounds__(kGroupThreads) void skinny_lora_group(const LoraArg
     const bool one = e < a.adapters;
     const int rank = !one ? 0 : a.ranks ? min(max(a.ranks[e], 0), a.rank) : a.rank;
     for (int r = 0; r < n; r += kRowBlock)
-      a.blocks[before.y++] = int4{one ? e : -1, before.x + r, min(n - r, kRowBlock), rank};
+      blocks[before.y++] = int4{one ? e : -1, row0 + before.x + r, min(n - r, kRowBlock), rank};
     before.x += n;
   }
-  for (int b = used + tid; b < a.most_blocks; b += kGroupThreads) a.blocks[b] = int4{-1, 0, 0, 0};
+  for (int b = used + tid; b < a.chunk_blocks; b += kGroupThreads) blocks[b] = int4{-1, 0, 0, 0};
   __syncthreads();
+  const auto write_all = [&](int t0, const int (&place)[kBatch]) {
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const int t = tid + i * kGroupThreads;
-    if (t < a.rows) a.order[count[kind[i]] + at[i]] = t;
-  }
-  if (a.rows <= kKept * kGroupThreads) return;
-  __syncthreads();
-  // Places behind the kept rows': a kind's counter moves on from its first place by them.
+    for (int i = 0; i < kBatch; ++i)
+      if (t0 + i * kGroupThreads < rows) order[place[i]] = row0 + t0 + i * kGroupThreads;
+  };
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) place(kind[i], true);
+  for (int i = 0; i < kBatch; ++i) at[i] += count[kind[i]];
+  write_all(tid, at);
+  if (rows <= kBatch * kGroupThreads) return;
   __syncthreads();
-  for (int t = tid + kKept * kGroupThreads; t - lane < a.rows; t += kGroupThreads) {
-    const int e = kind_of(min(t, a.rows - 1));
-    const int p = place(e, t < a.rows);
-    if (t < a.rows) a.order[p] = t;
+  place_all(tid, kind, at);            // each kind's counter moves on by them
+  __syncthreads();
+  for (int t0 = tid + kBatch * kGroupThreads; t0 - lane < rows; t0 += kBatch * kGroupThreads) {
+    load_kinds(t0, kind);
+    place_all(t0, kind, at);
+    write_all(t0, at);
   }
 }
 
@@ -523,15 +607,17 @@ template <int KS>
 struct Columns {
   u32x4 w[KS][4];
   __device__ __forceinline__ void load(const __bf16* b, int pool, int rank, int n0, int n) {
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const auto column = [&](int j, int i) {
       return min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), n - 1);
     };
+    // Lanes past the adapter's rank read its first part again, for cut to drop: loads
+    // in branches of their own would wait for each other.
+    const auto at = [&](int r) { return r < rank ? r : 0; };
     if constexpr (KS == 1) {           // rows of up to 64 bytes, side by side
+      const int l = threadIdx.x & 63, r = at(8 * (l & 3));
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[0][j] = 8 * g < rank ? *reinterpret_cast<const u32x4*>(b + (size_t)column(j, c) * pool + 8 * g)
-                               : u32x4{0, 0, 0, 0};
+        w[0][j] = *reinterpret_cast<const u32x4*>(b + (size_t)column(j, l >> 2) * pool + r);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -539,28 +625,31 @@ struct Columns {
         for (int h = 0; h < 2; ++h) {
           const __bf16* row = b + (size_t)column(j, 8 * h + line_row()) * pool;
 #pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            const int r = 32 * k + 8 * line_part();
-            w[k + h][j] = r < rank ? *reinterpret_cast<const u32x4*>(row + r) : u32x4{0, 0, 0, 0};
-          }
+          for (int k = 0; k < KS; k += 2)
+            w[k + h][j] = *reinterpret_cast<const u32x4*>(row + at(32 * k + 8 * line_part()));
         }
     }
   }
   // As the products take them.
-  __device__ __forceinline__ void turn() {
-    if constexpr (KS > 1)
+  __device__ __forceinline__ void to_products(u32x4* buf) {
+    if constexpr (KS == 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) narrow_to_products(w[0][j], buf);
+    } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {
-          const Lines l = Lines{{w[k][j], w[k + 1][j]}}.turned();
+          Lines l = Lines{{w[k][j], w[k + 1][j]}};
+          l.to_products(buf);
           w[k][j] = l.x[0];
           w[k + 1][j] = l.x[1];
         }
+    }
   }
   // Columns past the adapter's own rank count as 0, whatever they hold.
   __device__ __forceinline__ void cut(int rank) {
-    turn();
+    if (rank == 32 * KS) return;
     const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
@@ -626,6 +715,19 @@ __device__ __forceinline__ void stage(const LoraArgs& a, int slice, int rank, in
   }
 }
 
+// The same of rows that were joined before.
+__device__ __forceinline__ void stage_joined(const LoraArgs& a, int slice, int padded, int count,
+                                             const int* list, unsigned* hi, unsigned* lo, int stride) {
+  const int parts = padded / 8;        // 16-byte parts of a row's hi, and of its lo
+  for (int i = threadIdx.x; i < count * 2 * parts; i += kThreads) {
+    const int row = i / (2 * parts), part = i - row * 2 * parts;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(
+        a.low + ((size_t)slice * a.rows + list[row]) * 2 * padded + 8 * part);
+    unsigned* dst = part < parts ? hi + row * stride + 4 * part : lo + row * stride + 4 * (part - parts);
+    *reinterpret_cast<u32x4*>(dst) = v;
+  }
+}
+
 // 16 rows' part of base or y, a wave's 64 columns, in whole lines: a lane has 8
 // neighbouring columns, `left` of them in the slice, of two rows.
 struct Tile {
@@ -641,6 +743,15 @@ __device__ __forceinline__ Tile load_base(const LoraArgs& a, const int* list, in
     const unsigned short* src = (const unsigned short*)a.base + b.at[h];
     b.l.x[h] = u32x4{0, 0, 0, 0};
     if (left >= 8) {
+      // Off a dword's border an access takes twice as long: dwords around it instead,
+      // where the neighbouring values are the tensor's own.
+      if ((reinterpret_cast<uintptr_t>(src) & 2) && b.at[h] > 0 && b.at[h] + 8 < (size_t)a.rows * a.N) {
+        const u32x4 lo = *reinterpret_cast<const u32x4_dword*>(src - 1);
+        const unsigned hi = *reinterpret_cast<const unsigned*>(src + 7);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          b.l.x[h][e] = __builtin_amdgcn_alignbyte(e < 3 ? lo[e + 1] : hi, lo[e], 2);
+      } else
       b.l.x[h] = *reinterpret_cast<const u32x4_any*>(src);
     } else if (left > 0) {             // the last ones again behind them
       unsigned v[8];
@@ -657,6 +768,16 @@ __device__ __forceinline__ void store_y(const LoraArgs& a, const Tile& b, int t,
   for (int h = 0; h < 2; ++h) {
     if (t + 8 * h + line_row() >= count) continue;
     if (left >= 8) {
+      unsigned short* dst = (unsigned short*)a.y + b.at[h];
+      if (reinterpret_cast<uintptr_t>(dst) & 2) {
+        const u32x4 v = b.l.x[h];
+        u32x3 m;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) m[e] = __builtin_amdgcn_alignbyte(v[e + 1], v[e], 2);
+        dst[0] = (unsigned short)v[0];
+        *reinterpret_cast<u32x3_dword*>(dst + 1) = m;
+        dst[7] = (unsigned short)(v[3] >> 16);
+      } else
       *reinterpret_cast<u32x4_any*>(a.y + b.at[h]) = b.l.x[h];
     } else if (left > 0) {
 #pragma unroll
@@ -667,42 +788,30 @@ __device__ __forceinline__ void store_y(const LoraArgs& a, const Tile& b, int t,
   }
 }
 
-// y of a group's rows in the wave's columns, 16 rows at a time; what the next 16
+// y of a block's rows in the wave's columns, 16 rows at a time; what the next 16
 // are added to comes while the products run.
-template <int KS, bool LINES, typename Low>
+template <int KS>
 __device__ __forceinline__ void expand(const LoraArgs& a, const Columns<KS>& b, int column, int left,
-                                       int count, const int* list, Tile next, Low low) {
-  u32x4 ahead[KS][2];
-  low(0, ahead);
+                                       int count, const int* list, Tile next, const unsigned* hi,
+                                       const unsigned* lo, int stride, u32x4* turn) {
+  const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
   for (int t = 0; t < count; t += 16) {
     Tile here = next;
-    u32x4 v[KS][2];
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      if constexpr (LINES) {           // line i of the rows: their first parts, then their second
-        const Lines l = Lines{{ahead[i][0], ahead[i][1]}}.turned();
-        const int k = KS == 1 ? 0 : 2 * i % KS, p = KS == 1 ? 0 : 2 * i / KS;
-        v[k][p] = l.x[0];
-        v[KS == 1 ? 0 : k + 1][KS == 1 ? 1 : p] = l.x[1];
-      } else {
-        v[i][0] = ahead[i][0];
-        v[i][1] = ahead[i][1];
-      }
-    }
-    if (t + 16 < count) {
-      next = load_base(a, list, t + 16, count, column, left);
-      low(t + 16, ahead);
-    }
+    if (t + 16 < count) next = load_base(a, list, t + 16, count, column, left);
     f32x4 acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int k = 0; k < KS; ++k) {
+      const int at = (t + c) * stride + 16 * k + 4 * g;
+      const u32x4 vh = *reinterpret_cast<const u32x4*>(hi + at);
+      const u32x4 vl = *reinterpret_cast<const u32x4*>(lo + at);
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], vh, acc[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], v[k][p], acc[j]);
-    here.l = here.l.turned();
+      for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], vl, acc[j]);
+    }
+    here.l.to_products(turn);
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -711,7 +820,7 @@ __device__ __forceinline__ void expand(const LoraArgs& a, const Columns<KS>& b, 
         here.l.x[p][e] = pack_bf16(bf16_lo(y) + acc[2 * p + e / 2][2 * (e % 2)],
                                    bf16_hi(y) + acc[2 * p + e / 2][2 * (e % 2) + 1]);
       }
-    here.l = here.l.turned();
+    here.l.to_lines(turn);
     store_y(a, here, t, count, left);
   }
 }
@@ -738,15 +847,19 @@ struct Part {
   }
 };
 
-// STAGE: A x is summed over the splits here, by every workgroup for its rows; else it
-// was joined before.
-template <int KS, bool STAGE>
+// JOINED: A x's two parts were made before; else every workgroup sums the splits of
+// its rows here.
+template <int KS, bool JOINED>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(KS <= 2 ? 4 : KS == 4 ? 2 : 1)))
 void skinny_lora_expand(const LoraArgs a) {
   __shared__ int list[kRowBlock];
-  __shared__ __attribute__((aligned(16))) f32x4 sums[STAGE ? kThreads : 1];
+  __shared__ __attribute__((aligned(16))) u32x4 turns[kWaves][kTurn];
   extern __shared__ __attribute__((aligned(16))) unsigned staged[];    // A x in two parts
   constexpr int padded = 32 * KS;
+  constexpr int stride = padded / 2 + 4;             // dwords of a row, kept off the same banks
+  unsigned* hi = staged;
+  unsigned* lo = staged + kRowBlock * stride;
+  u32x4* turn = turns[threadIdx.x >> 6];
   // Workgroups go to the eight XCDs in turn; each XCD takes a run of neighbouring
   // parts of the same rows.
   const int i = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
@@ -764,40 +877,16 @@ void skinny_lora_expand(const LoraArgs a) {
   }
   Columns<KS> b;
   b.load(a.b[p.slice] + (size_t)bl.adapter * p.n * a.rank, a.rank, bl.rank, p.wave0, p.n);
-  const float scale = STAGE && a.scale ? a.scale[bl.adapter] : 1.0f;
+  const float scale = !JOINED && a.scale ? a.scale[bl.adapter] : 1.0f;
   __syncthreads();
   const Tile base = load_base(a, list, 0, bl.count, p.column, p.left);
-  if constexpr (STAGE) {
-    constexpr int stride = padded / 2 + 4;           // dwords of a row, kept off the same banks
-    unsigned* hi = staged;
-    unsigned* lo = staged + kRowBlock * stride;
-    stage(a, p.slice, bl.rank, padded, bl.count, list, scale, sums, hi, lo, stride);
-    b.cut(bl.rank);
-    __syncthreads();
-    if (p.wave0 >= p.n) return;
-    expand<KS, false>(a, b, p.column, p.left, bl.count, list, base, [&](int t, u32x4(&v)[KS][2]) {
-      const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int at = (t + c) * stride + 16 * k + 4 * g;
-        v[k][0] = *reinterpret_cast<const u32x4*>(hi + at);
-        v[k][1] = *reinterpret_cast<const u32x4*>(lo + at);
-      }
-    });
-  } else {
-    if (p.wave0 >= p.n) return;
-    b.cut(bl.rank);
-    expand<KS, true>(a, b, p.column, p.left, bl.count, list, base, [&](int t, u32x4(&v)[KS][2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const __bf16* src =
-            a.low + ((size_t)p.slice * a.rows + list[min(t + 8 * h + line_row(), bl.count - 1)]) * 2 *
-                        padded + 8 * line_part();
-#pragma unroll
-        for (int i = 0; i < KS; ++i) v[i][h] = *reinterpret_cast<const u32x4*>(src + 64 * i);
-      }
-    });
-  }
+  if constexpr (JOINED) stage_joined(a, p.slice, padded, bl.count, list, hi, lo, stride);
+  else stage(a, p.slice, bl.rank, padded, bl.count, list, scale, (f32x4*)turns, hi, lo, stride);
+  __syncthreads();
+  if (p.wave0 >= p.n) return;
+  b.to_products(turn);
+  b.cut(bl.rank);
+  expand<KS>(a, b, p.column, p.left, bl.count, list, base, hi, lo, stride, turn);
 }
 
 // ---------------------------------------------------------------------------
@@ -810,9 +899,11 @@ struct Cut {
   int tiles;                           // of 16 ranks in a workgroup (few) or a wave (many)
   int groups;                          // of them
   int splits, pieces, ordinals, most_blocks;
+  int chunks, chunk_rows, chunk_blocks;
 };
 constexpr int kFewGroups = 256;        // workgroups to cut a call into, if it is long enough
 constexpr int kManyGroups = 512;
+constexpr int kChunkRows = 4096;
 constexpr int kJoinRows = 512;         // up to here every workgroup sums its rows' splits itself
 Cut cut_of(const skinny_lora& l, int rows) {
   Cut c{};
@@ -833,9 +924,18 @@ Cut cut_of(const skinny_lora& l, int rows) {
     c.groups = (per + c.tiles - 1) / c.tiles;
   } else {
     c.join = rows > kJoinRows;
-    // Each kind of rows, those without an adapter among them, may end in part of a block.
-    c.most_blocks = blocks + (rows < l.adapters + 1 ? rows : l.adapters + 1);
-    if (c.most_blocks > rows) c.most_blocks = rows;
+    // Rows are ordered in chunks of some kChunkRows (one for 4096 rows takes 7 us, for
+    // 16384 23), fewer where there are so many adapters that parts of blocks, of which
+    // every chunk may have one for each kind of rows, would outnumber full blocks.
+    c.chunks = (rows + kChunkRows - 1) / kChunkRows;
+    if (c.chunks > blocks / (l.adapters + 1)) c.chunks = blocks / (l.adapters + 1);
+    if (c.chunks < 1) c.chunks = 1;
+    c.chunk_rows = (rows + c.chunks - 1) / c.chunks;
+    c.chunks = (rows + c.chunk_rows - 1) / c.chunk_rows;
+    const int kinds = c.chunk_rows < l.adapters + 1 ? c.chunk_rows : l.adapters + 1;
+    c.chunk_blocks = (c.chunk_rows + kRowBlock - 1) / kRowBlock + kinds;
+    if (c.chunk_blocks > c.chunk_rows) c.chunk_blocks = c.chunk_rows;
+    c.most_blocks = c.chunks * c.chunk_blocks;
     int slices = 0;
     for (int i = 0; i < l.slices; ++i) slices += l.a[i] != nullptr;
     const int waves = (slices * per + kWaves - 1) / kWaves;        // tiles per wave
@@ -871,7 +971,7 @@ skinny_status check_lora(const skinny_lora* l, int rows, long long* width) {
   }
   if (!any) return SKINNY_ERR_INVALID_ARG;
   if (rows > SKINNY_LORA_MAX_ROWS || l->adapters > SKINNY_LORA_MAX_ADAPTERS || l->rank % 8 != 0 ||
-      l->rank > SKINNY_LORA_MAX_RANK || l->K % 8 != 0 || l->K > (1 << 28) || n > (1 << 28))
+      l->rank > SKINNY_LORA_MAX_RANK || l->K % 8 != 0 || (long long)l->K * l->rank > (1 << 30) || n > (1 << 28))
     return SKINNY_ERR_UNSUPPORTED;
   if (!aligned(l->ranks, 4) || !aligned(l->scale, 4)) return SKINNY_ERR_UNSUPPORTED;
   *width = n;
@@ -893,22 +993,22 @@ struct Space {
 
 size_t workspace_of(const skinny_lora& l, int rows) { return Space(l, cut_of(l, rows), rows).bytes; }
 
-template <int KS, bool STAGE>
+template <int KS, bool JOINED>
 skinny_status launch_expand(const LoraArgs& a, unsigned grid, hipStream_t stream) {
-  constexpr int lds = STAGE ? 2 * kRowBlock * (16 * KS + 4) * (int)sizeof(unsigned) : 0;
-  if (lds > 56 * 1024 &&               // beside the sums, more than a launch may have unasked
-      hipFuncSetAttribute((const void*)skinny_lora_expand<KS, STAGE>,
+  constexpr int lds = 2 * kRowBlock * (16 * KS + 4) * (int)sizeof(unsigned);
+  if (lds > 48 * 1024 &&               // beside the rest, more than a launch may have unasked
+      hipFuncSetAttribute((const void*)skinny_lora_expand<KS, JOINED>,
                           hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return SKINNY_ERR_HIP;
-  hipLaunchKernelGGL((skinny_lora_expand<KS, STAGE>), dim3(grid), dim3(kThreads), lds, stream, a);
+  hipLaunchKernelGGL((skinny_lora_expand<KS, JOINED>), dim3(grid), dim3(kThreads), lds, stream, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
-template <bool STAGE>
+template <bool JOINED>
 skinny_status launch_expand(const LoraArgs& a, int padded, unsigned grid, hipStream_t stream) {
-  if (padded == 32) return launch_expand<1, STAGE>(a, grid, stream);
-  if (padded == 64) return launch_expand<2, STAGE>(a, grid, stream);
-  if (padded == 128) return launch_expand<4, STAGE>(a, grid, stream);
-  return launch_expand<8, STAGE>(a, grid, stream);
+  if (padded == 32) return launch_expand<1, JOINED>(a, grid, stream);
+  if (padded == 64) return launch_expand<2, JOINED>(a, grid, stream);
+  if (padded == 128) return launch_expand<4, JOINED>(a, grid, stream);
+  return launch_expand<8, JOINED>(a, grid, stream);
 }
 
 }  // namespace
@@ -973,6 +1073,8 @@ skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const i
   a.order = (int*)((char*)workspace + space.order);
   a.blocks = (int4*)((char*)workspace + space.blocks);
   a.most_blocks = c.most_blocks;
+  a.chunk_rows = c.chunk_rows;
+  a.chunk_blocks = c.chunk_blocks;
   a.rank_groups = c.groups;
   a.ordinals = c.ordinals;
   a.copy = base != y;
@@ -1009,7 +1111,7 @@ skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const i
     else if (c.tiles == 2) hipLaunchKernelGGL(skinny_lora_shrink_few<2>, grid, few, 0, hs, a);
     else hipLaunchKernelGGL(skinny_lora_shrink_few<4>, grid, few, 0, hs, a);
   } else {
-    hipLaunchKernelGGL(skinny_lora_group, dim3(1), dim3(kGroupThreads),
+    hipLaunchKernelGGL(skinny_lora_group, dim3(c.chunks), dim3(kGroupThreads),
                        (size_t)(l.adapters + 1) * sizeof(int), hs, a);
     if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
     if (c.tiles == 1) hipLaunchKernelGGL(skinny_lora_shrink_many<1>, grid, many, 0, hs, a);
@@ -1020,8 +1122,8 @@ skinny_status skinny_lora_linear(const skinny_lora* lora, const void* x, const i
     if (c.join) hipLaunchKernelGGL(skinny_lora_join, dim3((unsigned)join), many, 0, hs, a, padded);
   }
   if (hipGetLastError() != hipSuccess) return SKINNY_ERR_HIP;
-  return c.join ? launch_expand<false>(a, padded, (unsigned)second, hs)
-                : launch_expand<true>(a, padded, (unsigned)second, hs);
+  return c.join ? launch_expand<true>(a, padded, (unsigned)second, hs)
+                : launch_expand<false>(a, padded, (unsigned)second, hs);
 }
 
 }  // extern "C"
