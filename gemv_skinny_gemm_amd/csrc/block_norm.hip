@@ -7,6 +7,7 @@
 
 #include "host_util.h"
 #include "skinny_gemm.h"
+#include "wave_util.h"
 
 namespace {
 
@@ -16,6 +17,8 @@ using skinny_host::aligned;
 using skinny_host::device_info;
 using skinny_host::overlap;
 using skinny_host::range_of;
+using skinny_wave::lanes_sum;
+using skinny_wave::wave_sum;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // 16 bytes at any address: rows of an odd width begin anywhere, and the hardware
@@ -118,42 +121,6 @@ __device__ __forceinline__ void store(void* p, size_t at, const float (&v)[kUnit
     if constexpr (F32) ((float*)p)[at + e] = v[e];
     else ((__bf16*)p)[at + e] = (__bf16)v[e];
   }
-}
-
-// The value of the lane that CTRL names within a row of 16 lanes.
-template <int CTRL>
-__device__ __forceinline__ double from_lane(double x) {
-  const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
-  const int lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, 0xf, 0xf, true);
-  const int hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xf, 0xf, true);
-  return __builtin_bit_cast(double, (unsigned long long)(unsigned)lo |
-                                        (unsigned long long)(unsigned)hi << 32);
-}
-// The sums over runs of 2, 4, 8 and 16 neighbouring lanes, in all of them.
-template <int N>
-__device__ __forceinline__ double lanes_sum(double x) {
-  if constexpr (N > 1) x += from_lane<0xb1>(x);      // quad_perm 1 0 3 2
-  if constexpr (N > 2) x += from_lane<0x4e>(x);      // quad_perm 2 3 0 1
-  if constexpr (N > 4) x += from_lane<0x141>(x);     // row_half_mirror: quads agree by now
-  if constexpr (N > 8) x += from_lane<0x140>(x);     // row_mirror
-  return x;
-}
-__device__ __forceinline__ double wave_sum(double x) {
-  x = lanes_sum<16>(x);
-#pragma unroll
-  for (int off = 16; off < 64; off *= 2) {
-    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
-    const auto lo = off == 16
-        ? __builtin_amdgcn_permlane16_swap((unsigned)u, (unsigned)u, false, false)
-        : __builtin_amdgcn_permlane32_swap((unsigned)u, (unsigned)u, false, false);
-    const auto hi = off == 16
-        ? __builtin_amdgcn_permlane16_swap((unsigned)(u >> 32), (unsigned)(u >> 32), false, false)
-        : __builtin_amdgcn_permlane32_swap((unsigned)(u >> 32), (unsigned)(u >> 32), false, false);
-    const unsigned l0 = lo[0], l1 = lo[1], h0 = hi[0], h1 = hi[1];
-    x = __builtin_bit_cast(double, (unsigned long long)l0 | (unsigned long long)h0 << 32) +
-        __builtin_bit_cast(double, (unsigned long long)l1 | (unsigned long long)h1 << 32);
-  }
-  return x;
 }
 
 // The sum over a row's threads, in every one of them; `part` is used once only.

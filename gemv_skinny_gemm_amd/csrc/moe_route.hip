@@ -7,6 +7,7 @@
 
 #include "host_util.h"
 #include "skinny_gemm.h"
+#include "wave_util.h"
 
 namespace {
 
@@ -16,8 +17,9 @@ using skinny_host::aligned;
 using skinny_host::device_info;
 using skinny_host::overlap;
 using skinny_host::range_of;
-
-typedef unsigned long long u64;
+using skinny_wave::u64;
+using skinny_wave::wave_max;
+using skinny_wave::wave_sum;
 
 constexpr int kWaves = 4;              // rows of a workgroup, one per wave
 constexpr double kNegInf = -__builtin_inf();
@@ -32,112 +34,142 @@ struct RouteArgs {
   double scale;
 };
 
-// Unsigned numbers that order as x does; every one is above 0, which stands
-// for what is not to be chosen.
+// Unsigned numbers that order as x does; every one is above 0, which stands for
+// what is not to be chosen.
 __device__ __forceinline__ u64 key_of(double x) {
   const u64 u = __builtin_bit_cast(u64, x + 0.0);    // -0 counts as 0
   return u >> 63 ? ~u : u | 1ull << 63;
 }
-
-__device__ __forceinline__ u64 wave_max(u64 x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const u64 y = __shfl_xor(x, off);
-    x = x > y ? x : y;
-  }
-  return x;
-}
-__device__ __forceinline__ int wave_min(int x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x = min(x, __shfl_xor(x, off));
-  return x;
-}
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
-  return x;
+__device__ __forceinline__ unsigned key_of(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x + 0.0f);
+  return u >> 31 ? ~u : u | 1u << 31;
 }
 
-// A wave takes a row; lane holds experts lane, lane + 64, ..
-template <int V>
+__device__ __forceinline__ double sigmoid(double l) {
+  const double t = exp(-fabs(l));
+  return (l >= 0.0 ? 1.0 : t) / (1.0 + t);
+}
+
+__device__ __forceinline__ float of_lane(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ double of_lane(double x, int lane) {
+  const u64 u = __builtin_bit_cast(u64, x);
+  const unsigned lo = __builtin_amdgcn_readlane((unsigned)u, lane);
+  const unsigned hi = __builtin_amdgcn_readlane((unsigned)(u >> 32), lane);
+  return __builtin_bit_cast(double, (u64)lo | (u64)hi << 32);
+}
+
+// The lanes that hold the wave's largest key.
+__device__ __forceinline__ u64 lanes_of_max(unsigned key) { return __ballot(key == wave_max(key)); }
+__device__ __forceinline__ u64 lanes_of_max(u64 key) {
+  // By their upper halves, and by the lower ones where those do not tell.
+  const unsigned hi = (unsigned)(key >> 32), top = wave_max(hi);
+  const u64 equal = __ballot(hi == top);
+  if ((equal & (equal - 1)) == 0) return equal;
+  const unsigned lo = hi == top ? (unsigned)key : 0, most = wave_max(lo);
+  return __ballot(hi == top && lo == most);
+}
+
+// What the wave wrote to its own shared memory, for its other lanes.
+__device__ __forceinline__ void in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A wave takes a row; lane l holds experts l, l + 64, ..  Without a bias (Key
+// unsigned) the choice goes by the logits, in 32 bits, and only chosen ones are
+// exponentiated, unless the weights are shares of all; with one (Key u64) all scores
+// are needed, in 64 bits.
+//
+// What bounds it: the wave's instructions, of few rows their chain (1 row of 8 experts
+// 2.1 us, which is a launch; 16 rows of 256 biased experts in groups 7.5: 12 times the
+// largest of the wave's 64-bit keys), of many their number: 16384 rows, 6 of
+// 161 experts each, in 11 us, 8 of 256 biased ones in 32, 16 of 1024 in 60, where reading the
+// logits would take 1.2, 3.4 and 7.  With exponentials of all experts, 64-bit keys
+// throughout and maxima by way of the shared memory the first two took 10.7 and 30 us.
+// Each lane's own largest key is found again in every turn: ballots over every place
+// instead, to find the first of equals, took 84 us where this takes 60.
+template <int V, typename Key>
 __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArgs a) {
-  __shared__ double shared[kWaves][64 * V];
+  constexpr bool kBiased = sizeof(Key) == 8;
+  // Groups' members side by side, one place between groups to spread them over the banks.
+  __shared__ double members[kBiased ? kWaves : 1][kBiased ? 64 * V + SKINNY_ROUTE_MAX_GROUPS : 1];
+  __shared__ unsigned best_of[kWaves][SKINNY_ROUTE_MAX_GROUPS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int row = blockIdx.x * kWaves + wave;
   if (row >= a.rows) return;           // whole waves; the kernel has no barrier
-  double l[V], s[V];
-  double top = kNegInf;
+  float l[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = 64 * v + lane;
-    float x = -__builtin_inff();
-    if (e < a.experts) {
-      const size_t at = (size_t)row * a.experts + e;
-      x = a.f32 ? ((const float*)a.logits)[at] : (float)((const __bf16*)a.logits)[at];
-      if (x != x) x = -__builtin_inff();
-      x = fminf(x, __FLT_MAX__);
-    }
-    l[v] = x;
-    top = fmax(top, l[v]);
+    const int e = min(64 * v + lane, a.experts - 1);
+    const size_t at = (size_t)row * a.experts + e;
+    l[v] = a.f32 ? ((const float*)a.logits)[at] : (float)((const __bf16*)a.logits)[at];
   }
-  double total = 0.0;
-  if (a.sigmoid) {
+  Key key[V];
+  double s[kBiased ? V : 1];
+  double total = 0.0;                  // of the exponentials, over all experts
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (l[v] != l[v] || 64 * v + lane >= a.experts) l[v] = -__builtin_inff();
+    l[v] = fminf(l[v], __FLT_MAX__);
+    top = fmaxf(top, l[v]);
+  }
+  if (!a.sigmoid && (kBiased || !a.renormalize)) {
+    const unsigned k = wave_max(key_of(top));
+    top = __builtin_bit_cast(float, k >> 31 ? k & 0x7fffffffu : ~k);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const double t = exp(-fabs(l[v]));
-      s[v] = (l[v] >= 0.0 ? 1.0 : t) / (1.0 + t);
+      const double x = top == -__builtin_inff() ? 0.0 : exp((double)l[v] - (double)top);
+      if constexpr (kBiased) s[v] = x;
+      total += x;
+    }
+    total = wave_sum(total);
+  }
+  if constexpr (kBiased) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = 64 * v + lane;
+      s[v] = a.sigmoid ? sigmoid((double)l[v]) : total > 0.0 ? s[v] / total : 0.0;
+      double c = s[v] + (double)a.bias[min(e, a.experts - 1)];
+      if (c != c) c = kNegInf;
+      key[v] = e < a.experts ? key_of(c) : 0;
+      if (a.groups > 1 && e < a.experts) members[wave][e + e / a.each] = c;
     }
   } else {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = fmax(top, __shfl_xor(top, off));
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[v] = top == kNegInf ? 0.0 : exp(l[v] - top);
-      total += s[v];
-    }
-    total = wave_sum(total);
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = total > 0.0 ? s[v] / total : 0.0;
-  }
-  u64 key[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = 64 * v + lane;
-    double c = l[v];
-    if (a.bias && e < a.experts) {
-      c = s[v] + (double)a.bias[e];
-      if (c != c) c = kNegInf;
-    }
-    l[v] = c;
-    key[v] = e < a.experts ? key_of(c) : 0;
+    for (int v = 0; v < V; ++v) key[v] = 64 * v + lane < a.experts ? key_of(l[v]) : 0;
   }
   if (a.groups > 1) {
-    // Lane g ranks group g from the wave's own part of the shared memory.
-    double* c = shared[wave];
-#pragma unroll
-    for (int v = 0; v < V; ++v) c[64 * v + lane] = l[v];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    u64 worth = 0;
-    if (lane < a.groups) {
-      double first = kNegInf, second = kNegInf;
-      for (int i = 0; i < a.each; ++i) {
-        const double x = c[lane * a.each + i];
-        second = fmax(second, fmin(first, x));
-        first = fmax(first, x);
-      }
-      double w = first;
-      if (a.bias && a.each > 1) {
-        w += second;
+    Key worth = 0;                     // of group `lane`
+    if constexpr (kBiased) {
+      in_order();
+      if (lane < a.groups) {
+        const double* c = members[wave] + lane * (a.each + 1);
+        double first = kNegInf, second = kNegInf;
+#pragma unroll 8
+        for (int i = 0; i < a.each; ++i) {
+          const double x = c[i];
+          second = fmax(second, fmin(first, x));
+          first = fmax(first, x);
+        }
+        double w = a.each > 1 ? first + second : first;
         if (w != w) w = kNegInf;
+        worth = key_of(w);
       }
-      worth = key_of(w);
+    } else {
+      if (lane < a.groups) best_of[wave][lane] = 0;
+      in_order();
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (key[v]) atomicMax(&best_of[wave][(64 * v + lane) / a.each], key[v]);
+      in_order();
+      if (lane < a.groups) worth = best_of[wave][lane];
     }
     u64 kept = 0;
     for (int j = 0; j < a.top_groups; ++j) {
-      const u64 best = wave_max(worth);
-      const int g = __builtin_ctzll(__ballot(worth == best));
+      const int g = __builtin_ctzll(lanes_of_max(worth));
       kept |= 1ull << g;
       if (lane == g) worth = 0;
     }
@@ -145,29 +177,50 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
     for (int v = 0; v < V; ++v)
       if (!(kept >> ((64 * v + lane) / a.each & 63) & 1)) key[v] = 0;
   }
-  double mine = 0.0;                   // lane j: the score of choice j
+  // Lane j gets choice j: its number, and its logit or score.
   int id = 0;
+  double mine = kBiased ? 0.0 : kNegInf;
   for (int j = 0; j < a.topk; ++j) {
-    u64 best = 0;
+    Key best = key[0];                 // the lane's own largest, and the first place of it
+    int at = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) best = best > key[v] ? best : key[v];
-    best = wave_max(best);
-    int e = 64 * V;
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) e = 64 * v + lane;
-    e = wave_min(e);
+    for (int v = 1; v < V; ++v) {
+      const bool more = key[v] > best;
+      best = more ? key[v] : best;
+      at = more ? v : at;
+    }
+    u64 equal = lanes_of_max(best);
+    int lane0 = __builtin_ctzll(equal), v0 = __builtin_amdgcn_readlane(at, lane0);
+    while (equal &= equal - 1) {       // the first of equals
+      const int other = __builtin_ctzll(equal), v1 = __builtin_amdgcn_readlane(at, other);
+      if (v1 < v0) {
+        v0 = v1;
+        lane0 = other;
+      }
+    }
     double got = 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == 64 * v + lane) {
-        got = s[v];
-        key[v] = 0;
+    for (int v = 0; v < V; ++v) {
+      if (v0 == v) {
+        if constexpr (kBiased) got = of_lane(s[v], lane0);
+        else got = (double)of_lane(l[v], lane0);
       }
-    got = __shfl(got, e & 63);
+      key[v] = lane == lane0 && v0 == v ? 0 : key[v];
+    }
     if (lane == j) {
       mine = got;
-      id = e;
+      id = 64 * v0 + lane0;
+    }
+  }
+  if constexpr (!kBiased) {
+    if (a.sigmoid) {
+      mine = lane < a.topk ? sigmoid(mine) : 0.0;
+    } else {
+      // Without a bias the first choice has the largest logit of all.
+      const float first = __builtin_bit_cast(
+          float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, (float)mine)));
+      mine = lane >= a.topk || first == -__builtin_inff() ? 0.0 : exp(mine - (double)first);
+      if (!a.renormalize) mine = total > 0.0 ? mine / total : 0.0;
     }
   }
   if (a.renormalize) {
@@ -183,8 +236,9 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
 
 template <int V>
 skinny_status launch(const RouteArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((skinny_moe_route_k<V>), dim3((a.rows + kWaves - 1) / kWaves),
-                     dim3(64 * kWaves), 0, stream, a);
+  const dim3 grid((a.rows + kWaves - 1) / kWaves), threads(64 * kWaves);
+  if (a.bias) hipLaunchKernelGGL((skinny_moe_route_k<V, u64>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((skinny_moe_route_k<V, unsigned>), grid, threads, 0, stream, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 
@@ -240,6 +294,7 @@ skinny_status skinny_moe_route(const skinny_route* route, void* stream) {
   const hipStream_t hs = (hipStream_t)stream;
   if (r.experts <= 64) return launch<1>(a, hs);
   if (r.experts <= 128) return launch<2>(a, hs);
+  if (r.experts <= 192) return launch<3>(a, hs);
   if (r.experts <= 256) return launch<4>(a, hs);
   if (r.experts <= 512) return launch<8>(a, hs);
   return launch<16>(a, hs);

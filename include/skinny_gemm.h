@@ -692,7 +692,8 @@ skinny_status skinny_block_norm(const skinny_norm* norm, void* stream);
  * and y[t] = base[t] for every t whose e is outside [0, adapters).  A projection
  * of several parts (q, k and v; gate and up) has an A and a B for each: slice i
  * covers the n[i] columns of y behind those of the slices before it.
- *   x         [rows][K] bf16, the projection's x; K % 8 == 0, 16-byte aligned
+ *   x         [rows][K] bf16, the projection's x; K % 8 == 0, 16-byte aligned;
+ *             rank * K at most 2^30
  *   base, y   [rows][N] bf16, N = n[0] + .. + n[slices - 1]: the projection's y and
  *             the result; base NULL: y itself (added in place; rows without an
  *             adapter are then left as they were); base overlaps y in no other way
@@ -711,7 +712,9 @@ skinny_status skinny_block_norm(const skinny_norm* norm, void* stream);
  *   workspace >= skinny_lora_workspace_bytes(lora, rows) bytes (0 for invalid
  *             arguments), 16-byte aligned, contents undefined before and after, so
  *             calls that may overlap need their own
- * y and the workspace must not overlap anything else. */
+ * Up to 64 rows take two launches, more three, more than 512 four.  A call of more
+ * workgroups than a launch may have threads for (2^32) is refused
+ * (SKINNY_ERR_UNSUPPORTED).  y and the workspace must not overlap anything else. */
 #define SKINNY_LORA_MAX_ROWS 1048576
 #define SKINNY_LORA_MAX_RANK 256
 #define SKINNY_LORA_MAX_ADAPTERS 8192

@@ -66,7 +66,7 @@ def lora(call=None, rows=5, ws=P[11], n=None, x=P[8], ids=P[9], base=P[7], y=P[1
     (dict(a0=None, b0=None, a1=None, b1=None), INVALID), (dict(x=None), INVALID),
     (dict(ids=None), INVALID), (dict(y=None), INVALID), (dict(slices=5), UNSUPPORTED),
     (dict(rows=(1 << 20) + 1), UNSUPPORTED), (dict(adapters=8193), UNSUPPORTED),
-    (dict(rank=12), UNSUPPORTED), (dict(rank=264), UNSUPPORTED), (dict(K=60), UNSUPPORTED),
+    (dict(rank=12), UNSUPPORTED), (dict(rank=256, K=1 << 23), UNSUPPORTED), (dict(rank=264), UNSUPPORTED), (dict(K=60), UNSUPPORTED),
     (dict(a1=P[1] + 8), UNSUPPORTED), (dict(b0=P[2] + 2), UNSUPPORTED), (dict(x=P[8] + 8), UNSUPPORTED),
     (dict(ids=P[9] + 2), UNSUPPORTED), (dict(ranks=P[4] + 1), UNSUPPORTED),
     (dict(scale=P[5] + 2), UNSUPPORTED), (dict(y=P[10] + 1), UNSUPPORTED),

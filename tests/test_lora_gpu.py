@@ -77,6 +77,7 @@ SIZES = [
     (16, 1000, [256, 100, 31], 5, 32), (17, 520, [257], 1, 64), (33, 128, [300], 40, 40),
     (64, 256, [70], 64, 16), (65, 256, [70, 3], 3, 72), (200, 328, [513], 9, 128),
     (300, 64, [40], 2, 256), (1000, 136, [96, 17], 70, 8), (2500, 72, [130], 4, 48),
+    (600, 200, [64, 33], 3, 256), (9000, 24, [19], 200, 8), (9001, 16, [8], 3, 16),
 ]
 
 
@@ -157,6 +158,33 @@ def test_largest_numbers():
     got = c.run()
     want = torch.full_like(c.base, v * 2.0 ** -100)
     assert torch.equal(got, want)
+
+
+def test_many_adapters():
+    need_gpu()
+    ids = torch.arange(700) * 37 % 8192
+    Call(700, 64, [33], 8192, 8, ids=ids, whole=True).check(whole=True)
+
+
+@pytest.mark.parametrize("rows,rank", [(5, 256), (70, 16), (600, 256)])
+def test_as_a_graph(rows, rank):
+    """Replays take the ids and values that are in the buffers then."""
+    need_gpu()
+    c = Call(rows, 136, [65, 40], 6, rank, whole=True)
+    y = torch.empty_like(c.base)
+    go = lambda: sg.lora_linear(c.lora, c.x, c.ids, y, c.ws, base=c.base)
+    go()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for step in range(3):
+        c.ids.copy_(torch.randint(-1, 6, (rows,), device="cuda"))
+        c.x.copy_(torch.randint(-2, 3, c.x.shape, device="cuda"))
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), torch.from_numpy(c.want()[0]).to(torch.float32).to(BF))
 
 
 def test_long_offsets():
