@@ -24,6 +24,35 @@ typedef unsigned u32x3 __attribute__((ext_vector_type(3)));
 typedef u32x3 u32x3_dword __attribute__((aligned(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// y[t] = base[t] + scale B (A x[t]) on the matrix cores, v_mfma_f32_16x16x32_bf16,
+// fp32 sums: A x with A = 16 ranks and B = 16 rows, so that lane (c, g) ends with four
+// neighbouring ranks of row c; then, B's columns for A and the rows' A x for B, with
+// neighbouring columns of one row of y.  Between the two products A x is the sum of two
+// bf16 numbers, the upper half of the fp32 one (its largest numbers too) and the rest:
+// within 2^-16, where one alone, within 2^-9, would be the largest error of the delta.
+//
+// Launches: the first product (K split over workgroups, partial sums in the workspace)
+// and the second one.  Up to 64 rows every workgroup of the first finds the rows of its
+// adapter itself, one of them tells the second.  Beyond, a launch before them orders
+// the rows by adapter into blocks of up to 64; with more than 512 a launch between them
+// joins the splits, which otherwise every workgroup of the second sums for its rows.
+// Ordering the whole call counts: blocks of 64 neighbouring rows each with its own
+// adapters read A two and a half times on requests of 40 rows (246 us where 91 are now).
+//
+// What bounds it, measured (in a graph, beside 10240 x 8192 in three slices unless
+// said): one token of rank 16 7.9 us, two launches of 4.1 and 4.9, each a chain of
+// three round trips to memory; 16 requests of ranks to 64 beside 59136 x 8192 35 us, of
+// which 28 the second launch, 83 MB (B's rows are lines of 128 bytes, however much of
+// them an adapter's rank uses) by waves that wait for their one tile; 4099 rows of rank
+// 64, three adapters, 91 us = 6 + 35 + 6 + 46: the last adds to y at 3.7 TB/s, the first
+// product waits for A (2.2 MB for every 64 rows, from the L2 cache).
+//   Whole lines: see Lines; 114 to 92 us on the 4099 rows.  Odd rows of y by dwords:
+// 26 to 21.5 us (251 rows of 2561 columns).  Loads in branches of their own wait for
+// each other; clamped addresses instead: 38 to 31 us (32 adapters of rank 128).  Tried
+// and no faster: blocks of 128 rows (92 us; 30 for 24 on 1024 rows), two tiles of
+// columns per wave (37.4 for 34.3 on the 16 requests), workgroups of 16 waves for few
+// rows (9.1 for 8.5 on one token), K's stages in another order for every block.
+
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRowBlock = 64;          // rows whose adapters a wave looks over at once
