@@ -235,7 +235,8 @@ __device__ __forceinline__ void normalise(const NormArgs& a, float (&v)[CH][kUni
 // 16384 rows of 8192 with two LAYER norms in fp32 took 481 us instead of 422.
 // Loading weights before the sums, to have them at hand behind, costs those
 // registers and gained nothing at one row.  Several one-wave rows per workgroup gain
-// nothing either (16384 rows of 512: 12.4 us alone, 12.9 by fours).
+// nothing either (16384 rows of 512: 12.4 us alone, 12.9 by fours), nor do dwords
+// around bf16 units of odd rows (16384 x 5001: 201 us, 208 with them).
 template <int CH, bool RF, bool WF>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(CH == 1 ? 8 : 4)))
 void skinny_block_norm_k(const NormArgs a) {

@@ -55,7 +55,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kRowBlock = 64;          // rows whose adapters a wave looks over at once
+constexpr int kRowBlock = 64;          // rows of a block, all of one adapter
 constexpr int kPiece = 64;             // values of K per row and wave at a time: a cache line
 constexpr int kCols = 64;              // columns of y of a wave
 constexpr int kMaxSlices = SKINNY_LORA_MAX_SLICES;
@@ -780,8 +780,9 @@ __device__ __forceinline__ Tile load_base(const LoraArgs& a, const int* list, in
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           b.l.x[h][e] = __builtin_amdgcn_alignbyte(e < 3 ? lo[e + 1] : hi, lo[e], 2);
-      } else
-      b.l.x[h] = *reinterpret_cast<const u32x4_any*>(src);
+      } else {
+        b.l.x[h] = *reinterpret_cast<const u32x4_any*>(src);
+      }
     } else if (left > 0) {             // the last ones again behind them
       unsigned v[8];
 #pragma unroll
@@ -806,8 +807,9 @@ __device__ __forceinline__ void store_y(const LoraArgs& a, const Tile& b, int t,
         dst[0] = (unsigned short)v[0];
         *reinterpret_cast<u32x3_dword*>(dst + 1) = m;
         dst[7] = (unsigned short)(v[3] >> 16);
-      } else
-      *reinterpret_cast<u32x4_any*>(a.y + b.at[h]) = b.l.x[h];
+      } else {
+        *reinterpret_cast<u32x4_any*>(dst) = b.l.x[h];
+      }
     } else if (left > 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)

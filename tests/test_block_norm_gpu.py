@@ -161,3 +161,19 @@ def test_reproducible_on_another_stream():
         torch.cuda.synchronize()
         outs.append(out)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[1], outs[2])
+
+
+def test_long_offsets():
+    """The most rows, and more than 2^31 values: a row gives what it gives alone."""
+    need_gpu()
+    rows, width = 1 << 20, 2056
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF)
+    residual, block, gate, weight = rnd(rows, width), rnd(rows, width), rnd(rows, width), rnd(width)
+    out, kept = torch.empty_like(residual), torch.empty_like(residual)
+    sg.block_norm(out, weight, residual=residual, block=block, gate=gate, residual_out=kept)
+    one, one_kept = torch.empty_like(out[:1]), torch.empty_like(kept[:1])
+    for t in (0, 1, (1 << 31) // width, (1 << 31) // width + 1, rows - 1):
+        sg.block_norm(one, weight, residual=residual[t:t + 1], block=block[t:t + 1],
+                      gate=gate[t:t + 1], residual_out=one_kept)
+        assert torch.equal(out[t:t + 1], one) and torch.equal(kept[t:t + 1], one_kept)

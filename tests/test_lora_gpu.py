@@ -205,3 +205,23 @@ def test_long_offsets():
         if e >= 0:
             want = want + b[e].float() @ (a[e].float() @ x[t].float())
         assert torch.equal(y[t], want.to(BF))
+
+
+def test_long_x():
+    """The most rows, and more than 2^31 values of x."""
+    need_gpu()
+    rows, K, N = 1 << 20, 2056, 17
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda", dtype=torch.int8).to(BF)
+    x, a, b = ints(rows, K), ints(3, 8, K), ints(3, N, 8)
+    ids = torch.randint(-1, 3, (rows,), generator=g, device="cuda").to(torch.int32)
+    y = torch.ones(rows, N, dtype=BF, device="cuda")
+    lora = sg.make_lora(a, b)
+    ws = torch.empty(sg.lora_workspace_bytes(lora, rows), dtype=torch.uint8, device="cuda")
+    sg.lora_linear(lora, x, ids, y, ws)
+    for t in (0, 1, (1 << 31) // K, (1 << 31) // K + 1, rows - 2, rows - 1):
+        e = int(ids[t])
+        want = torch.ones(N, device="cuda")
+        if e >= 0:                     # whole numbers below 2^24, exact in fp32
+            want = want + b[e].float() @ (a[e].float() @ x[t].float())
+        assert torch.equal(y[t], want.to(BF))

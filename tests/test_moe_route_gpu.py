@@ -91,3 +91,19 @@ def test_values_that_are_no_numbers():
             for kw in (dict(), dict(groups=7, top_groups=2), dict(groups=35, top_groups=3)):
                 run_and_check(l, 6, scoring=scoring, renormalize=renormalize, **kw)
                 run_and_check(l, 6, bias=bias, scoring=scoring, renormalize=renormalize, **kw)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+def test_long_offsets(biased):
+    """The most rows and experts, logits of 2^32 bytes: a row gives what it gives alone."""
+    need_gpu()
+    rows, experts, topk = 1 << 20, 1024, 16
+    logits = rand(rows, experts, torch.float32, 8)
+    bias = rand(1, experts, torch.float32, 5, 0.2)[0] if biased else None
+    ids = torch.full((rows, topk), -7, dtype=torch.int32, device="cuda")
+    weights = torch.full((rows, topk), NAN, device="cuda")
+    sg.moe_route(logits, ids, weights, bias=bias, groups=64, top_groups=8)
+    one, one_w = torch.empty_like(ids[:1]), torch.empty_like(weights[:1])
+    for t in (0, 1, rows // 2 - 1, rows // 2, rows - 1):
+        sg.moe_route(logits[t:t + 1], one, one_w, bias=bias, groups=64, top_groups=8)
+        assert torch.equal(ids[t:t + 1], one) and torch.equal(weights[t:t + 1], one_w)
