@@ -80,17 +80,19 @@ __device__ __forceinline__ void in_order() {
 // A wave takes a row; lane l holds experts l, l + 64, ..  Without a bias (Key
 // unsigned) the choice goes by the logits, in 32 bits, and only chosen ones are
 // exponentiated, unless the weights are shares of all; with one (Key u64) all scores
-// are needed, in 64 bits.
+// are needed, in 64 bits.  A bf16 logit leaves 16 bits of its key for the expert's
+// number (PACKED), lower ones the larger, so that no two keys are equal and the
+// largest says which it is.
 //
 // What bounds it: the wave's instructions, of few rows their chain (1 row of 8 experts
 // 2.1 us, which is a launch; 16 rows of 256 biased experts in groups 7.5: 12 times the
-// largest of the wave's 64-bit keys), of many their number: 16384 rows, 6 of
-// 161 experts each, in 11 us, 8 of 256 biased ones in 32, 16 of 1024 in 60, where reading the
-// logits would take 1.2, 3.4 and 7.  With exponentials of all experts, 64-bit keys
-// throughout and maxima by way of the shared memory the first two took 10.7 and 30 us.
-// Each lane's own largest key is found again in every turn: ballots over every place
-// instead, to find the first of equals, took 84 us where this takes 60.
-template <int V, typename Key>
+// largest of the wave's 64-bit keys), of many their number: 16384 rows of bf16, 6 of
+// 161 experts each, in 8.5 us, 16 of 1024 in 32, 8 of 256 biased ones in 32, where
+// reading the logits would take 1.2, 7 and 1.9.  With the number apart from the key, as
+// fp32 logits need it (11.2 and 54 us), the first two took 11.1 and 60.
+// There each lane's own largest key is found again in every turn: ballots over every
+// place instead, to find the first of equals, took 84 us for the 60.
+template <int V, typename Key, bool PACKED>
 __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArgs a) {
   constexpr bool kBiased = sizeof(Key) == 8;
   // Groups' members side by side, one place between groups to spread them over the banks.
@@ -104,7 +106,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
   for (int v = 0; v < V; ++v) {
     const int e = min(64 * v + lane, a.experts - 1);
     const size_t at = (size_t)row * a.experts + e;
-    l[v] = a.f32 ? ((const float*)a.logits)[at] : (float)((const __bf16*)a.logits)[at];
+    l[v] = !PACKED && a.f32 ? ((const float*)a.logits)[at] : (float)((const __bf16*)a.logits)[at];
   }
   Key key[V];
   double s[kBiased ? V : 1];
@@ -113,6 +115,10 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (l[v] != l[v] || 64 * v + lane >= a.experts) l[v] = -__builtin_inff();
+    if constexpr (PACKED) {            // before the cut: bf16's largest is not infinity
+      const int e = 64 * v + lane;
+      key[v] = e < a.experts ? (key_of(l[v]) & 0xffff0000u) | (unsigned)(0xffff - e) : 0;
+    }
     l[v] = fminf(l[v], __FLT_MAX__);
     top = fmaxf(top, l[v]);
   }
@@ -137,7 +143,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
       key[v] = e < a.experts ? key_of(c) : 0;
       if (a.groups > 1 && e < a.experts) members[wave][e + e / a.each] = c;
     }
-  } else {
+  } else if constexpr (!PACKED) {
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = 64 * v + lane < a.experts ? key_of(l[v]) : 0;
   }
@@ -180,36 +186,52 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
   // Lane j gets choice j: its number, and its logit or score.
   int id = 0;
   double mine = kBiased ? 0.0 : kNegInf;
-  for (int j = 0; j < a.topk; ++j) {
-    Key best = key[0];                 // the lane's own largest, and the first place of it
-    int at = 0;
+  if constexpr (PACKED) {
+    unsigned choice = 0;
+    for (int j = 0; j < a.topk; ++j) {
+      unsigned best = key[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) {
-      const bool more = key[v] > best;
-      best = more ? key[v] : best;
-      at = more ? v : at;
-    }
-    u64 equal = lanes_of_max(best);
-    int lane0 = __builtin_ctzll(equal), v0 = __builtin_amdgcn_readlane(at, lane0);
-    while (equal &= equal - 1) {       // the first of equals
-      const int other = __builtin_ctzll(equal), v1 = __builtin_amdgcn_readlane(at, other);
-      if (v1 < v0) {
-        v0 = v1;
-        lane0 = other;
-      }
-    }
-    double got = 0.0;
+      for (int v = 1; v < V; ++v) best = max(best, key[v]);
+      best = wave_max(best);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (v0 == v) {
-        if constexpr (kBiased) got = of_lane(s[v], lane0);
-        else got = (double)of_lane(l[v], lane0);
-      }
-      key[v] = lane == lane0 && v0 == v ? 0 : key[v];
+      for (int v = 0; v < V; ++v) key[v] = key[v] == best ? 0 : key[v];
+      choice = lane == j ? best : choice;
     }
-    if (lane == j) {
-      mine = got;
-      id = 64 * v0 + lane0;
+    id = 0xffff - (int)(choice & 0xffffu);
+    const unsigned u = (choice >> 31 ? choice & 0x7fffffffu : ~choice) & 0xffff0000u;
+    if (lane < a.topk) mine = (double)fminf(__builtin_bit_cast(float, u), __FLT_MAX__);
+  } else {
+    for (int j = 0; j < a.topk; ++j) {
+      Key best = key[0];               // the lane's own largest, and the first place of it
+      int at = 0;
+#pragma unroll
+      for (int v = 1; v < V; ++v) {
+        const bool more = key[v] > best;
+        best = more ? key[v] : best;
+        at = more ? v : at;
+      }
+      u64 equal = lanes_of_max(best);
+      int lane0 = __builtin_ctzll(equal), v0 = __builtin_amdgcn_readlane(at, lane0);
+      while (equal &= equal - 1) {     // the first of equals
+        const int other = __builtin_ctzll(equal), v1 = __builtin_amdgcn_readlane(at, other);
+        if (v1 < v0) {
+          v0 = v1;
+          lane0 = other;
+        }
+      }
+      double got = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (v0 == v) {
+          if constexpr (kBiased) got = of_lane(s[v], lane0);
+          else got = (double)of_lane(l[v], lane0);
+        }
+        key[v] = lane == lane0 && v0 == v ? 0 : key[v];
+      }
+      if (lane == j) {
+        mine = got;
+        id = 64 * v0 + lane0;
+      }
     }
   }
   if constexpr (!kBiased) {
@@ -237,8 +259,9 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_moe_route_k(const RouteArg
 template <int V>
 skinny_status launch(const RouteArgs& a, hipStream_t stream) {
   const dim3 grid((a.rows + kWaves - 1) / kWaves), threads(64 * kWaves);
-  if (a.bias) hipLaunchKernelGGL((skinny_moe_route_k<V, u64>), grid, threads, 0, stream, a);
-  else hipLaunchKernelGGL((skinny_moe_route_k<V, unsigned>), grid, threads, 0, stream, a);
+  if (a.bias) hipLaunchKernelGGL((skinny_moe_route_k<V, u64, false>), grid, threads, 0, stream, a);
+  else if (a.f32) hipLaunchKernelGGL((skinny_moe_route_k<V, unsigned, false>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((skinny_moe_route_k<V, unsigned, true>), grid, threads, 0, stream, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
 

@@ -107,3 +107,32 @@ def test_long_offsets(biased):
     for t in (0, 1, rows // 2 - 1, rows // 2, rows - 1):
         sg.moe_route(logits[t:t + 1], one, one_w, bias=bias, groups=64, top_groups=8)
         assert torch.equal(ids[t:t + 1], one) and torch.equal(weights[t:t + 1], one_w)
+
+
+@pytest.mark.parametrize("experts,groups,top", [(64, 1, 1), (161, 1, 1), (256, 8, 4), (1000, 4, 1),
+                                                (1024, 64, 16)])
+def test_bf16_values_that_are_no_numbers(experts, groups, top):
+    """And bf16 neighbours: equal ones by index, its largest behind infinity, its smallest."""
+    need_gpu()
+    l = rand(12, experts, torch.bfloat16, experts)
+    l[0, :] = -INF
+    l[1, :] = NAN
+    l[2, 3:] = -INF                    # fewer experts than choices
+    l[3, 40] = INF
+    l[3, 2] = l[3, 50] = torch.finfo(torch.bfloat16).max
+    l[4, 10] = l[4, 60] = INF
+    l[5, ::2] = NAN
+    l[6, :] = torch.finfo(torch.bfloat16).min
+    l[6, 7] = -INF
+    l[7, :] = -1.0                     # equal but for the sign of zeros and the smallest numbers
+    l[7, 30:] = -0.0
+    l[7, 45:] = 0.0
+    l[7, 62] = 2.0 ** -133
+    l[7, 63] = -2.0 ** -133
+    l[8] *= 100.0
+    l[9] = l[9].round()                # many equal ones
+    l[10, :] = 0.5
+    for scoring in (sg.ROUTE_SOFTMAX, sg.ROUTE_SIGMOID):
+        for renormalize in (True, False):
+            run_and_check(l, 8, scoring=scoring, renormalize=renormalize, groups=groups,
+                          top_groups=top)
