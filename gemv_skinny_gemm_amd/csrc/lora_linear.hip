@@ -27,9 +27,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // y[t] = base[t] + scale B (A x[t]) on the matrix cores, v_mfma_f32_16x16x32_bf16,
 // fp32 sums: A x with A = 16 ranks and B = 16 rows, so that lane (c, g) ends with four
 // neighbouring ranks of row c; then, B's columns for A and the rows' A x for B, with
-// neighbouring columns of one row of y.  Between the two products A x is the sum of two
-// bf16 numbers, the upper half of the fp32 one (its largest numbers too) and the rest:
-// within 2^-16, where one alone, within 2^-9, would be the largest error of the delta.
+// neighbouring columns of one row of y.  Between the two products A x, an fp32 number of
+// 24 bits, is the sum of three bf16 numbers of 8 each: the upper half (the largest numbers
+// too), the upper half of what is left, and the rest.  Two parts, 16 bits, turned up to
+// 0.3% of bf16 results into their neighbours, three 0.02%, for 94.5 us instead of 92.0 on
+// the 4099 rows below; of rank 128 (4096 rows beside 59136 x 8192) 416 instead of 387.
 //
 // Launches: the first product (K split over workgroups, partial sums in the workspace)
 // and the second one.  Up to 64 rows every workgroup of the first finds the rows of its
@@ -69,7 +71,7 @@ struct LoraArgs {
   const float* scale;
   // In the workspace:
   float* part;                         // [splits][slices][rows][rank]: A x over a split's K
-  __bf16* low;                         // joined: [slices][rows][2][padded], A x in two parts
+  __bf16* low;                         // joined: [slices][rows][kParts][padded], A x in parts
   int4* blocks;                        // [most_blocks]: up to 64 rows of one adapter (-1: of
                                        // none): adapter, first place in order, rows, its rank
   int* order;                          // row numbers
@@ -159,6 +161,19 @@ __device__ __forceinline__ float rest_of(float x, float part) {
   const float r = x - part;
   return r - r == 0.0f ? r : 0.0f;
 }
+// Two fp32 numbers as the sums of kParts bf16 numbers each, largest first.
+constexpr int kParts = 3;
+struct Parts {
+  unsigned p[kParts];
+  __device__ __forceinline__ Parts(float x, float y) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      p[i] = upper_halves(x, y);
+      x = rest_of(x, bf16_lo(p[i]));
+      y = rest_of(y, bf16_hi(p[i]));
+    }
+  }
+};
 
 // The numbers of `rows`, side by side, the last one again behind them (one wave).
 __device__ __forceinline__ void list_rows(unsigned long long rows, int* list) {
@@ -593,8 +608,8 @@ __global__ __launch_bounds__(kGroupThreads) void skinny_lora_group(const LoraArg
   }
 }
 
-// Many rows: the splits' sums, times the scale, in the two bf16 numbers that the
-// products with B take; zeros behind the adapter's rank.
+// Many rows: the splits' sums, times the scale, in the bf16 numbers that the products
+// with B take; zeros behind the adapter's rank.
 __global__ __launch_bounds__(kThreads) void skinny_lora_join(const LoraArgs a, int padded) {
   const int quads = padded / 4;
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -616,17 +631,13 @@ __global__ __launch_bounds__(kThreads) void skinny_lora_join(const LoraArgs a, i
   if (r < rank)
 #pragma unroll 8
     for (int k = 0; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(src + k * step);
-  unsigned h[2], l[2];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const float x = r + 2 * p < rank ? s[2 * p] * scale : 0.0f;
-    const float y = r + 2 * p + 1 < rank ? s[2 * p + 1] * scale : 0.0f;
-    h[p] = upper_halves(x, y);
-    l[p] = pack_bf16(rest_of(x, bf16_lo(h[p])), rest_of(y, bf16_hi(h[p])));
-  }
-  __bf16* dst = a.low + (size_t)at * 2 * padded + r;
-  *reinterpret_cast<u32x2*>(dst) = u32x2{h[0], h[1]};
-  *reinterpret_cast<u32x2*>(dst + padded) = u32x2{l[0], l[1]};
+  for (int e = 0; e < 4; ++e) s[e] = r + e < rank ? s[e] * scale : 0.0f;
+  const Parts v(s[0], s[1]), w(s[2], s[3]);
+  __bf16* dst = a.low + (size_t)at * kParts * padded + r;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i)
+    *reinterpret_cast<u32x2*>(dst + i * padded) = u32x2{v.p[i], w.p[i]};
 }
 
 // The columns of B that one wave multiplies: product j's row i is column 32 (j / 2) +
@@ -693,23 +704,25 @@ struct Columns {
   }
 };
 
-// A x of a group's rows, summed over the splits in order, times the scale, as two
-// bf16 numbers each: row t's at dwords t * stride of hi and lo, zeros behind the rank.
+// A x of some of a block's rows, summed over the splits in order, times the scale, in its
+// bf16 parts: row t's at dwords t * stride of each part's `most` rows, zeros behind the rank.
 constexpr int kMaxSplits = 8;
+// Rows that are staged at a time.  All 64 of ranks above 64 leave room for a workgroup less
+// on a CU: of rank 128, 16 rows beside 59136 x 8192 62.2 us for 57.6, 4096 rows 484 for 416;
+// of rank 256, 4096 rows beside 10240 x 8192, 374 for 298.
+constexpr int staged_rows(int ks) { return ks <= 2 ? kRowBlock : kRowBlock / 2; }
 __device__ __forceinline__ void stage(const LoraArgs& a, int slice, int rank, int padded, int count,
-                                      const int* list, float scale, f32x4* sums, unsigned* hi,
-                                      unsigned* lo, int stride) {
+                                      const int* list, float scale, f32x4* sums, unsigned* staged,
+                                      int most, int stride) {
   const int quads = padded / 4, items = count * quads;
   const size_t step = (size_t)a.slices * a.rows * a.rank;
   const auto put = [&](int row, int r, f32x4 s) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const float x = r + 2 * p < rank ? s[2 * p] * scale : 0.0f;
-      const float y = r + 2 * p + 1 < rank ? s[2 * p + 1] * scale : 0.0f;
-      const unsigned h = upper_halves(x, y);
-      hi[row * stride + r / 2 + p] = h;
-      lo[row * stride + r / 2 + p] = pack_bf16(rest_of(x, bf16_lo(h)), rest_of(y, bf16_hi(h)));
-    }
+    for (int e = 0; e < 4; ++e) s[e] = r + e < rank ? s[e] * scale : 0.0f;
+    const Parts v(s[0], s[1]), w(s[2], s[3]);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      *reinterpret_cast<u32x2*>(staged + (i * most + row) * stride + r / 2) = u32x2{v.p[i], w.p[i]};
   };
   const auto source = [&](int item, int& row, int& r) {
     row = item / quads;
@@ -746,14 +759,14 @@ __device__ __forceinline__ void stage(const LoraArgs& a, int slice, int rank, in
 
 // The same of rows that were joined before.
 __device__ __forceinline__ void stage_joined(const LoraArgs& a, int slice, int padded, int count,
-                                             const int* list, unsigned* hi, unsigned* lo, int stride) {
-  const int parts = padded / 8;        // 16-byte parts of a row's hi, and of its lo
-  for (int i = threadIdx.x; i < count * 2 * parts; i += kThreads) {
-    const int row = i / (2 * parts), part = i - row * 2 * parts;
+                                             const int* list, unsigned* staged, int most,
+                                             int stride) {
+  const int chunks = padded / 8;       // of 16 bytes, of a row's part
+  for (int i = threadIdx.x; i < count * kParts * chunks; i += kThreads) {
+    const int row = i / (kParts * chunks), at = i - row * kParts * chunks;
     const u32x4 v = *reinterpret_cast<const u32x4*>(
-        a.low + ((size_t)slice * a.rows + list[row]) * 2 * padded + 8 * part);
-    unsigned* dst = part < parts ? hi + row * stride + 4 * part : lo + row * stride + 4 * (part - parts);
-    *reinterpret_cast<u32x4*>(dst) = v;
+        a.low + ((size_t)slice * a.rows + list[row]) * kParts * padded + 8 * at);
+    *reinterpret_cast<u32x4*>(staged + (at / chunks * most + row) * stride + at % chunks * 4) = v;
   }
 }
 
@@ -819,29 +832,28 @@ __device__ __forceinline__ void store_y(const LoraArgs& a, const Tile& b, int t,
   }
 }
 
-// y of a block's rows in the wave's columns, 16 rows at a time; what the next 16
-// are added to comes while the products run.
+// y of a block's rows from t0 up to t1 in the wave's columns, 16 rows at a time; what
+// the next 16 are added to comes while the products run.
 template <int KS>
 __device__ __forceinline__ void expand(const LoraArgs& a, const Columns<KS>& b, int column, int left,
-                                       int count, const int* list, Tile next, const unsigned* hi,
-                                       const unsigned* lo, int stride, u32x4* turn) {
+                                       int t0, int t1, int count, const int* list, Tile& next,
+                                       const unsigned* staged, int stride, u32x4* turn) {
   const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  for (int t = 0; t < count; t += 16) {
+  for (int t = t0; t < t1; t += 16) {
     Tile here = next;
     if (t + 16 < count) next = load_base(a, list, t + 16, count, column, left);
     f32x4 acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int at = (t + c) * stride + 16 * k + 4 * g;
-      const u32x4 vh = *reinterpret_cast<const u32x4*>(hi + at);
-      const u32x4 vl = *reinterpret_cast<const u32x4*>(lo + at);
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], vh, acc[j]);
+      for (int i = 0; i < kParts; ++i) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(staged + (i * staged_rows(KS) + t - t0 + c) * stride +
+                                                        16 * k + 4 * g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], vl, acc[j]);
-    }
+        for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], v, acc[j]);
+      }
     here.l.to_products(turn);
 #pragma unroll
     for (int p = 0; p < 2; ++p)
@@ -878,18 +890,16 @@ struct Part {
   }
 };
 
-// JOINED: A x's two parts were made before; else every workgroup sums the splits of
+// JOINED: A x's parts were made before; else every workgroup sums the splits of
 // its rows here.
 template <int KS, bool JOINED>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(KS <= 2 ? 4 : KS == 4 ? 2 : 1)))
 void skinny_lora_expand(const LoraArgs a) {
   __shared__ int list[kRowBlock];
   __shared__ __attribute__((aligned(16))) u32x4 turns[kWaves][kTurn];
-  extern __shared__ __attribute__((aligned(16))) unsigned staged[];    // A x in two parts
+  extern __shared__ __attribute__((aligned(16))) unsigned staged[];    // A x in its parts
   constexpr int padded = 32 * KS;
   constexpr int stride = padded / 2 + 4;             // dwords of a row, kept off the same banks
-  unsigned* hi = staged;
-  unsigned* lo = staged + kRowBlock * stride;
   u32x4* turn = turns[threadIdx.x >> 6];
   // Workgroups go to the eight XCDs in turn; each XCD takes a run of neighbouring
   // parts of the same rows.
@@ -910,14 +920,21 @@ void skinny_lora_expand(const LoraArgs a) {
   b.load(a.b[p.slice] + (size_t)bl.adapter * p.n * a.rank, a.rank, bl.rank, p.wave0, p.n);
   const float scale = !JOINED && a.scale ? a.scale[bl.adapter] : 1.0f;
   __syncthreads();
-  const Tile base = load_base(a, list, 0, bl.count, p.column, p.left);
-  if constexpr (JOINED) stage_joined(a, p.slice, padded, bl.count, list, hi, lo, stride);
-  else stage(a, p.slice, bl.rank, padded, bl.count, list, scale, (f32x4*)turns, hi, lo, stride);
-  __syncthreads();
-  if (p.wave0 >= p.n) return;
-  b.to_products(turn);
-  b.cut(bl.rank);
-  expand<KS>(a, b, p.column, p.left, bl.count, list, base, hi, lo, stride, turn);
+  Tile next = load_base(a, list, 0, bl.count, p.column, p.left);
+  constexpr int most = staged_rows(KS);
+  for (int t0 = 0; t0 == 0 || (most < kRowBlock && t0 < bl.count); t0 += most) {
+    const int t1 = min(t0 + most, bl.count);
+    if (t0) __syncthreads();           // the rows before these are done
+    if constexpr (JOINED) stage_joined(a, p.slice, padded, t1 - t0, list + t0, staged, most, stride);
+    else stage(a, p.slice, bl.rank, padded, t1 - t0, list + t0, scale, (f32x4*)turns, staged, most, stride);
+    __syncthreads();
+    if (p.wave0 >= p.n) continue;
+    if (t0 == 0) {
+      b.to_products(turn);
+      b.cut(bl.rank);
+    }
+    expand<KS>(a, b, p.column, p.left, t0, t1, bl.count, list, next, staged, stride, turn);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1015,7 +1032,7 @@ struct Space {
   Space(const skinny_lora& l, const Cut& c, int rows) {
     const size_t all = (size_t)l.slices * rows;
     low = c.splits * all * l.rank * sizeof(float);
-    blocks = low + (c.join ? all * 2 * padded_rank(l) * sizeof(__bf16) : 0);
+    blocks = low + (c.join ? all * kParts * padded_rank(l) * sizeof(__bf16) : 0);
     order = blocks + (size_t)c.most_blocks * sizeof(int4);
     bytes = order + (c.few ? (size_t)c.most_blocks * kRowBlock : (size_t)rows) * sizeof(int);
     if (bytes < SKINNY_MIN_WORKSPACE_BYTES) bytes = SKINNY_MIN_WORKSPACE_BYTES;
@@ -1026,8 +1043,9 @@ size_t workspace_of(const skinny_lora& l, int rows) { return Space(l, cut_of(l, 
 
 template <int KS, bool JOINED>
 skinny_status launch_expand(const LoraArgs& a, unsigned grid, hipStream_t stream) {
-  constexpr int lds = 2 * kRowBlock * (16 * KS + 4) * (int)sizeof(unsigned);
-  if (lds > 48 * 1024 &&               // beside the rest, more than a launch may have unasked
+  constexpr int lds = kParts * staged_rows(KS) * (16 * KS + 4) * (int)sizeof(unsigned);
+  constexpr int rest = kRowBlock * (int)sizeof(int) + kWaves * kTurn * (int)sizeof(u32x4);
+  if (lds + rest > 64 * 1024 &&        // more than a launch may have unasked
       hipFuncSetAttribute((const void*)skinny_lora_expand<KS, JOINED>,
                           hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return SKINNY_ERR_HIP;

@@ -225,3 +225,28 @@ def test_long_x():
         if e >= 0:                     # whole numbers below 2^24, exact in fp32
             want = want + b[e].float() @ (a[e].float() @ x[t].float())
         assert torch.equal(y[t], want.to(BF))
+
+
+@pytest.mark.parametrize("rows,rank", [(1, 8), (5, 40), (30, 128), (64, 256), (70, 16), (200, 64),
+                                       (300, 256), (600, 8), (700, 72), (1100, 200)])
+def test_sums_of_24_bits_stay_whole(rows, rank):
+    """A x of up to 23 bits, whose differences y shows: pairs of A's rows differ where x counts
+    once only.  Every partial sum is a whole number below 2^24, exact in fp32 in any order."""
+    need_gpu()
+    adapters, K, N = 3, 24, 70
+    c = Call(rows, K, [N], adapters, rank, ids=[t % 4 for t in range(rows)], whole=True, scaled=False)
+    g = torch.Generator(device="cuda").manual_seed(rank)
+    ints = lambda most, *s: torch.randint(-most, most + 1, s, generator=g, device="cuda")
+    step = 2 ** (torch.arange(K, device="cuda") % 12)
+    a = ints(255, adapters, rank // 2, 1, K) * step
+    a = a.repeat(1, 1, 2, 1)
+    a[..., ::12] = ints(255, adapters, rank // 2, 2, K // 12)
+    c.a[0].copy_(a.reshape(adapters, rank, K))
+    pair = torch.randint(0, rank // 2, (adapters, N, 1), generator=g, device="cuda")
+    b = torch.zeros(adapters, N, rank, device="cuda")
+    b.scatter_(2, 2 * pair, 1.0).scatter_(2, 2 * pair + 1, -1.0)
+    c.b[0].copy_(b)
+    c.check(whole=True)
+    x, A = lu.host(c.x), lu.host(c.a[0])
+    size = max(float((np.abs(A[i]) @ np.abs(x[t])).max()) for t, i in enumerate(c.ids.tolist()) if i < adapters)
+    assert 2 * size + 100 < 2 ** 24
