@@ -646,10 +646,10 @@ __global__ __launch_bounds__(kThreads) void skinny_lora_join(const LoraArgs a, i
 template <int KS>
 struct Columns {
   u32x4 w[KS][4];
+  static __device__ __forceinline__ int column(int j, int i, int n0, int n) {
+    return min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), n - 1);
+  }
   __device__ __forceinline__ void load(const __bf16* b, int pool, int rank, int n0, int n) {
-    const auto column = [&](int j, int i) {
-      return min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), n - 1);
-    };
     // Lanes past the adapter's rank read its first part again, for cut to drop: loads
     // in branches of their own would wait for each other.
     const auto at = [&](int r) { return r < rank ? r : 0; };
@@ -657,13 +657,13 @@ struct Columns {
       const int l = threadIdx.x & 63, r = at(8 * (l & 3));
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[0][j] = *reinterpret_cast<const u32x4*>(b + (size_t)column(j, l >> 2) * pool + r);
+        w[0][j] = *reinterpret_cast<const u32x4*>(b + (size_t)column(j, l >> 2, n0, n) * pool + r);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const __bf16* row = b + (size_t)column(j, 8 * h + line_row()) * pool;
+          const __bf16* row = b + (size_t)column(j, 8 * h + line_row(), n0, n) * pool;
 #pragma unroll
           for (int k = 0; k < KS; k += 2)
             w[k + h][j] = *reinterpret_cast<const u32x4*>(row + at(32 * k + 8 * line_part()));
@@ -832,50 +832,6 @@ __device__ __forceinline__ void store_y(const LoraArgs& a, const Tile& b, int t,
   }
 }
 
-// y of a block's rows from t0 up to t1 in the wave's columns, 16 rows at a time; what
-// the next 16 are added to comes while the products run.
-template <int KS>
-__device__ __forceinline__ void expand(const LoraArgs& a, const Columns<KS>& b, int column, int left,
-                                       int t0, int t1, int count, const int* list, Tile& next,
-                                       const unsigned* staged, int stride, u32x4* turn) {
-  const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  for (int t = t0; t < t1; t += 16) {
-    Tile here = next;
-    if (t + 16 < count) next = load_base(a, list, t + 16, count, column, left);
-    f32x4 acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(staged + (i * staged_rows(KS) + t - t0 + c) * stride +
-                                                        16 * k + 4 * g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], v, acc[j]);
-      }
-    here.l.to_products(turn);
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const unsigned y = here.l.x[p][e];
-        here.l.x[p][e] = pack_bf16(bf16_lo(y) + acc[2 * p + e / 2][2 * (e % 2)],
-                                   bf16_hi(y) + acc[2 * p + e / 2][2 * (e % 2) + 1]);
-      }
-    here.l.to_lines(turn);
-    store_y(a, here, t, count, left);
-  }
-}
-
-// Rows without an adapter, in the wave's columns.
-__device__ __forceinline__ void copy_rows(const LoraArgs& a, int column, int left, int count,
-                                          const int* list) {
-#pragma unroll 4
-  for (int t = 0; t < count; t += 16)
-    store_y(a, load_base(a, list, t, count, column, left), t, count, left);
-}
-
 // The part of y that a workgroup writes: a wave's 64 columns of a slice from wave0 on,
 // of which a lane has 8 from `column` of y on, with `left` left in the slice.
 struct Part {
@@ -889,6 +845,83 @@ struct Part {
     left = n - wave0 - 8 * line_part();
   }
 };
+
+// Sums of a lane's row that came out as no numbers, once more, by all of A x: an infinity
+// in B times a part of A x that is 0, because A x has few bits, is NaN, where A x times it
+// is infinite.
+template <int KS>
+__device__ __forceinline__ void sum_again(const LoraArgs& a, f32x4 (&acc)[4], const __bf16* w, int rank,
+                                          int n0, int n, const unsigned* staged, int row, int stride) {
+  int g = (threadIdx.x & 63) >> 4;
+  asm volatile("" : "+v"(g), "+v"(row));             // or addresses take registers in every turn
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float s = acc[j][i];
+      if (s == s) continue;
+      const __bf16* b = w + (size_t)Columns<KS>::column(j, 4 * g + i, n0, n) * a.rank;
+      s = 0.0f;
+      for (int r = 0; r < rank && s == s; ++r) {
+        float v = 0.0f;
+#pragma unroll
+        for (int p = kParts - 1; p >= 0; --p)        // smallest first: every sum is exact
+          v += (float)((const __bf16*)(staged + (p * staged_rows(KS) + row) * stride))[r];
+        s = fmaf((float)b[r], v, s);
+      }
+      acc[j][i] = s;
+    }
+}
+
+// y of a block's rows from t0 up to t1 in the wave's columns, 16 rows at a time; what
+// the next 16 are added to comes while the products run.
+template <int KS>
+__device__ __forceinline__ void expand(const LoraArgs& a, const Columns<KS>& b, const __bf16* w,
+                                       int rank, const Part& p, int t0, int t1, int count,
+                                       const int* list, Tile& next, const unsigned* staged, int stride,
+                                       u32x4* turn) {
+  const int c = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  for (int t = t0; t < t1; t += 16) {
+    Tile here = next;
+    if (t + 16 < count) next = load_base(a, list, t + 16, count, p.column, p.left);
+    f32x4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(staged + (i * staged_rows(KS) + t - t0 + c) * stride +
+                                                        16 * k + 4 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(b.w[k][j], v, acc[j]);
+      }
+    float all = 0.0f;                  // NaN if one of them is
+#pragma unroll
+    for (int j = 0; j < 4; ++j) all += (acc[j][0] + acc[j][1]) + (acc[j][2] + acc[j][3]);
+    if (__builtin_expect(all != all && t + c < t1, 0))
+      sum_again<KS>(a, acc, w, rank, p.wave0, p.n, staged, t - t0 + c, stride);
+    here.l.to_products(turn);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned y = here.l.x[h][e];
+        here.l.x[h][e] = pack_bf16(bf16_lo(y) + acc[2 * h + e / 2][2 * (e % 2)],
+                                   bf16_hi(y) + acc[2 * h + e / 2][2 * (e % 2) + 1]);
+      }
+    here.l.to_lines(turn);
+    store_y(a, here, t, count, p.left);
+  }
+}
+
+// Rows without an adapter, in the wave's columns.
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, int column, int left, int count,
+                                          const int* list) {
+#pragma unroll 4
+  for (int t = 0; t < count; t += 16)
+    store_y(a, load_base(a, list, t, count, column, left), t, count, left);
+}
 
 // JOINED: A x's parts were made before; else every workgroup sums the splits of
 // its rows here.
@@ -917,7 +950,8 @@ void skinny_lora_expand(const LoraArgs a) {
     return;
   }
   Columns<KS> b;
-  b.load(a.b[p.slice] + (size_t)bl.adapter * p.n * a.rank, a.rank, bl.rank, p.wave0, p.n);
+  const __bf16* w = a.b[p.slice] + (size_t)bl.adapter * p.n * a.rank;
+  b.load(w, a.rank, bl.rank, p.wave0, p.n);
   const float scale = !JOINED && a.scale ? a.scale[bl.adapter] : 1.0f;
   __syncthreads();
   Tile next = load_base(a, list, 0, bl.count, p.column, p.left);
@@ -933,7 +967,7 @@ void skinny_lora_expand(const LoraArgs a) {
       b.to_products(turn);
       b.cut(bl.rank);
     }
-    expand<KS>(a, b, p.column, p.left, t0, t1, bl.count, list, next, staged, stride, turn);
+    expand<KS>(a, b, w, bl.rank, p, t0, t1, bl.count, list, next, staged, stride, turn);
   }
 }
 

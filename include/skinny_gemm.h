@@ -707,8 +707,9 @@ skinny_status skinny_block_norm(const skinny_norm* norm, void* stream);
  *   ids       [rows] int32, device, read by the kernels; any values
  * Rows of one adapter share the reading of its weights, 64 at a time.  Sums are fp32;
  * scale * (A x), as fp32, enters the product with B without another rounding (numbers
- * below 2^-110 within 2^-133); y is rounded once.  A row's result does not depend on the
- * other rows' values; results are bitwise reproducible for the same sizes.
+ * below 2^-110 within 2^-133); y is rounded once.  Infinities and NaN come out as fp32
+ * sums of those products have them.  A row's result does not depend on the other rows'
+ * values; results are bitwise reproducible for the same sizes.
  *   workspace >= skinny_lora_workspace_bytes(lora, rows) bytes (0 for invalid
  *             arguments), 16-byte aligned, contents undefined before and after, so
  *             calls that may overlap need their own

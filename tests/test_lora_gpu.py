@@ -10,7 +10,7 @@ from tests.gpu_util import need_gpu
 
 pytestmark = pytest.mark.gpu
 
-BF, NAN = torch.bfloat16, float("nan")
+BF, NAN, INF = torch.bfloat16, float("nan"), float("inf")
 
 
 class Call:
@@ -250,3 +250,39 @@ def test_sums_of_24_bits_stay_whole(rows, rank):
     x, A = lu.host(c.x), lu.host(c.a[0])
     size = max(float((np.abs(A[i]) @ np.abs(x[t])).max()) for t, i in enumerate(c.ids.tolist()) if i < adapters)
     assert 2 * size + 100 < 2 ** 24
+
+
+@pytest.mark.parametrize("rows,rank", [(1, 8), (20, 64), (40, 128), (64, 256), (90, 16), (200, 40),
+                                       (600, 64), (700, 200)])
+@pytest.mark.parametrize("most", [2, 255])
+def test_infinities_in_b(rows, rank, most):
+    """B's infinities and NaN within the rank: y is infinite where A x is not 0 there, whether
+    A x is a bf16 number (most 2) or needs more bits, and other columns and rows are whole."""
+    need_gpu()
+    adapters, K, N = 3, 64, 150
+    c = Call(rows, K, [N], adapters, rank, ids=[t % 4 for t in range(rows)], whole=True, scaled=False)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    c.a[0].copy_(torch.randint(-most, most + 1, c.a[0].shape, generator=g, device="cuda"))
+    b = c.b[0]
+    b[:, 3, rank - 1], b[0, 70, 0], b[1, 71, 1], b[2, 72, 2] = INF, -INF, NAN, INF
+    b[0, 149, 5], b[0, 149, 6] = INF, -INF
+    want = torch.from_numpy(c.want()[0]).to(torch.float32).to(BF)
+    assert want[:, 3].isinf().any() and torch.isfinite(want[:, 4:70]).all()
+    for in_place in (False, True):
+        got = c.run(in_place).cpu()
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.nan_to_num(nan=0.5, posinf=INF, neginf=-INF),
+                           want.nan_to_num(nan=0.5, posinf=INF, neginf=-INF))
+
+
+def test_smallest_numbers():
+    """A x of 2^-115 + 2^-132 and 2^-115: parts below bf16's normal numbers count, too."""
+    need_gpu()
+    for rows in (2, 70, 600):
+        c = Call(rows, 64, [16], 1, 8, ids=[0] * rows, scaled=False, whole=True)
+        for t in (c.x, c.a[0], c.b[0], c.base):
+            t.zero_()
+        c.x[:, 0], c.x[:, 1] = 2.0 ** -60, 2.0 ** -66
+        c.a[0][0, :2, 0], c.a[0][0, 0, 1] = 2.0 ** -55, 2.0 ** -66
+        c.b[0][0, :, 0], c.b[0][0, :, 1] = 2.0 ** 120, -2.0 ** 120
+        assert (c.run() == 2.0 ** -12).all()
