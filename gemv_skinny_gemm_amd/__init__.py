@@ -139,6 +139,7 @@ class Lora(ctypes.Structure):
                 ("a", ctypes.c_void_p * MAX_LORA_SLICES), ("b", ctypes.c_void_p * MAX_LORA_SLICES),
                 ("ranks", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
     gpu = None                 # of the tensors that make_lora was given
+    width = None               # of y, as make_lora summed it
 
 
 class Route(ctypes.Structure):
@@ -998,7 +999,7 @@ def lora_linear(lora: Lora, x, ids, y, workspace, base=None, stream=None):
     rows = x.shape[0]
     xp = _operand(x, (rows, lora.K), tt.bf16, "x", dev)
     ip = _operand(ids, (rows,), tt.i32, "ids", dev)
-    shape = (rows, lora.width)
+    shape = (rows, lora.width or sum(lora.n[:max(lora.slices, 0)]))
     yp = _operand(y, shape, tt.bf16, "y", dev)
     bp = None if base is None else _operand(base, shape, tt.bf16, "base", dev)
     wp, wb = _space(workspace, dev)

@@ -174,3 +174,15 @@ def test_route_binding():
     refuses(sg.moe_route, "weights: shape", l, ids, z(4, 3))
     refuses(sg.moe_route, "bias: shape", l, ids, w, bias=z(9))
     refuses(sg.moe_route, "must be on the GPU", l, ids, w)
+
+
+def test_lora_filled_by_hand():
+    """A Lora without make_lora: y's width is the sum of its slices'."""
+    z = lambda *s, t=BF: torch.zeros(s, dtype=t)
+    lora = sg.Lora(3, 16, 64, 2)
+    for i in range(2):
+        lora.n[i], lora.a[i], lora.b[i] = 40 + i, P[i], P[2 + i]
+    x, ids, ws = z(5, 64), z(5, t=torch.int32), z(4096, t=torch.uint8)
+    refuses(sg.lora_linear, "y: shape", lora, x, ids, z(5, 80), ws)
+    refuses(sg.lora_linear, "base: shape", lora, x, ids, z(5, 81), ws, base=z(5, 40))
+    refuses(sg.lora_linear, "must be on the GPU", lora, x, ids, z(5, 81), ws)

@@ -286,3 +286,14 @@ def test_smallest_numbers():
         c.a[0][0, :2, 0], c.a[0][0, 0, 1] = 2.0 ** -55, 2.0 ** -66
         c.b[0][0, :, 0], c.b[0][0, :, 1] = 2.0 ** 120, -2.0 ** 120
         assert (c.run() == 2.0 ** -12).all()
+
+
+def test_filled_by_hand():
+    """A descriptor that a program fills itself is make_lora's."""
+    need_gpu()
+    c = Call(20, 64, [33, 40], 3, 16, whole=True, scaled=False)
+    made, c.lora = c.lora, sg.Lora(3, 16, 64, 2)
+    for i in range(2):
+        c.lora.n[i], c.lora.a[i], c.lora.b[i] = made.n[i], made.a[i], made.b[i]
+    assert sg.lora_workspace_bytes(c.lora, 20) == sg.lora_workspace_bytes(made, 20)
+    c.check(whole=True)
