@@ -294,6 +294,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void skinny_lora_shrink_few(const L
   const bool tells = split == 0 && slice == 0 && r0 == 0;
   if (threadIdx.x < 64) {
     list_rows(rows, list);
+    in_order();
     if (tells) {
       if (lane < count) a.order[ordinal * kRowBlock + lane] = list[lane];
       if (lane == 0) a.blocks[ordinal] = int4{adapter, ordinal * kRowBlock, count, rank};

@@ -297,3 +297,11 @@ def test_filled_by_hand():
         c.lora.n[i], c.lora.a[i], c.lora.b[i] = made.n[i], made.a[i], made.b[i]
     assert sg.lora_workspace_bytes(c.lora, 20) == sg.lora_workspace_bytes(made, 20)
     c.check(whole=True)
+
+
+@pytest.mark.parametrize("rows", [2, 17, 63, 64])
+@pytest.mark.parametrize("step", [1, 7, 13])
+def test_rows_of_an_adapter_anywhere(rows, step):
+    """The rows of an adapter, spread over the call, as the first launch lists them for the second."""
+    need_gpu()
+    Call(rows, 72, [100], 4, 24, ids=[t * step % 5 for t in range(rows)], whole=True).check(whole=True)
