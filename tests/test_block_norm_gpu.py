@@ -177,3 +177,67 @@ def test_long_offsets():
         sg.block_norm(one, weight, residual=residual[t:t + 1], block=block[t:t + 1],
                       gate=gate[t:t + 1], residual_out=one_kept)
         assert torch.equal(out[t:t + 1], one) and torch.equal(kept[t:t + 1], one_kept)
+
+
+WIDE = [("residual", "block", "weight"),
+        ("residual", "block", "post_weight", "post_bias", "gate", "weight", "bias"),
+        ("block", "post_weight", "gate_rows")]
+
+
+@pytest.mark.parametrize("width", [8200, 12001, 16385, 20000, 32767])
+@pytest.mark.parametrize("res_type,w_type", [(F32, F32), (F32, BF), (BF, F32)])
+@pytest.mark.parametrize("form", WIDE, ids="+".join)
+def test_wide_rows_of_32_bits(width, res_type, w_type, form):
+    """Several units per thread with fp32 operands."""
+    need_gpu()
+    for kind in (sg.NORM_RMS, sg.NORM_LAYER):
+        t = make(4, width, residual=res_type, weight=w_type, seed=width)
+        run_and_check(4, width, {("gate" if k == "gate_rows" else k): t[k] for k in form}, kind=kind,
+                      res_type=res_type if "residual" in form else BF, residual_scale=0.75,
+                      block_scale=-1.25, weight_offset=1.0)
+
+
+@pytest.mark.parametrize("width", [8191, 8192, 9000, 16384, 16391, 32768])
+@pytest.mark.parametrize("res_type", [BF, F32])
+def test_routes_of_wide_rows(width, res_type):
+    need_gpu()
+    for routes, weighted in ((2, True), (3, False), (8, True)):
+        t = make(5, width, routes, residual=res_type, seed=width)
+        names = ["residual", "block", "weight"] + (["route_weights"] if weighted else [])
+        run_and_check(5, width, {k: t[k] for k in names}, routes=routes, res_type=res_type)
+
+
+@pytest.mark.parametrize("width", [5, 64, 777, 8200, 16400])
+@pytest.mark.parametrize("res_type,w_type", [(BF, BF), (F32, F32)])
+def test_addresses_of_a_value(width, res_type, w_type):
+    """Every operand at a multiple of its type's bytes; values beside them do not count or change."""
+    need_gpu()
+    rows = 3
+    t = make(rows, width, residual=res_type, weight=w_type, seed=width)
+    del t["gate_rows"], t["route_weights"]
+    aligned, apart, guards = [torch.empty(rows, width, dtype=BF, device="cuda"),
+                              torch.empty(rows, width, dtype=res_type, device="cuda")], {}, []
+
+    def placed(v, offset, fill):
+        buf = torch.full((v.numel() + 64,), fill, dtype=v.dtype, device="cuda")
+        guards.append((buf, 16 + offset, 16 + offset + v.numel()))
+        inner = buf[16 + offset:16 + offset + v.numel()].view(v.shape)
+        return inner.copy_(v)
+
+    for i, (k, v) in enumerate(sorted(t.items())):
+        apart[k] = placed(v, 1 + i % 3 * 2, float("nan"))
+    guards.clear()
+    out, res = placed(aligned[0], 1, 7.0), placed(aligned[1], 3, 7.0)
+    for kind in (sg.NORM_RMS, sg.NORM_LAYER):
+        for operands, o, r in ((t, *aligned), (apart, out, res)):
+            kw = {k: v for k, v in operands.items() if k != "weight"}
+            sg.block_norm(o, operands["weight"], residual_out=r, kind=kind, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(out, aligned[0]) and torch.equal(res, aligned[1])
+        for buf, lo, hi in guards:
+            assert (buf[:lo] == 7).all() and (buf[hi:] == 7).all()
+    apart["residual"].copy_(t["residual"])
+    kw = {k: v for k, v in apart.items() if k != "weight"}
+    sg.block_norm(out, apart["weight"], residual_out=apart["residual"], kind=sg.NORM_LAYER, **kw)
+    torch.cuda.synchronize()           # in place, as the last pass of the loop
+    assert torch.equal(out, aligned[0]) and torch.equal(apart["residual"], aligned[1])

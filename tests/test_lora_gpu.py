@@ -305,3 +305,33 @@ def test_rows_of_an_adapter_anywhere(rows, step):
     """The rows of an adapter, spread over the call, as the first launch lists them for the second."""
     need_gpu()
     Call(rows, 72, [100], 4, 24, ids=[t * step % 5 for t in range(rows)], whole=True).check(whole=True)
+
+
+def placed(values, offset, fill):
+    """A copy of a 2-D tensor, `offset` values behind an aligned address, and the whole buffer."""
+    n = values.numel()
+    buf = torch.full((n + 48,), fill, dtype=values.dtype, device="cuda")
+    inner = buf[16 + offset:16 + offset + n].view(values.shape)
+    inner.copy_(values)
+    return inner, buf
+
+
+@pytest.mark.parametrize("rows,n,rank", [(1, [8], 8), (5, [64], 40), (5, [65], 16), (40, [7, 70], 136),
+                                         (70, [64], 16), (300, [129], 72), (600, [130], 16),
+                                         (600, [3, 129], 136)])
+def test_addresses_of_a_value(rows, n, rank):
+    """base and y at any multiple of 2 bytes, each at its own; nothing beside them counts or
+    changes, nor what lies behind a workspace of just the bytes that it has to have."""
+    need_gpu()
+    c = Call(rows, 64, n, 3, rank, ids=[t % 4 for t in range(rows)], whole=True)
+    want = torch.from_numpy(c.want()[0]).to(torch.float32).to(BF)
+    need = sg.lora_workspace_bytes(c.lora, rows)
+    ws = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+    for base_at, y_at in ((0, 1), (1, 0), (1, 1), (3, 2), (2, 3), (7, 5), (None, 1), (None, 3)):
+        y, buf = placed(torch.full_like(c.base, NAN) if base_at is not None else c.base, y_at, 7.0)
+        base = None if base_at is None else placed(c.base, base_at, NAN)[0]
+        sg.lora_linear(c.lora, c.x, c.ids, y, ws[:need], base=base)
+        torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), want)
+        assert (buf[:16 + y_at] == 7).all() and (buf[16 + y_at + y.numel():] == 7).all()
+        assert (ws[need:] == 0xAB).all()
