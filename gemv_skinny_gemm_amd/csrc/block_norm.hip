@@ -134,8 +134,8 @@ __device__ __forceinline__ double row_sum(double x, double* part) {
   return lanes_sum<16>(w < waves ? part[w] : 0.0);
 }
 
-// 1 / sqrt(x) within 2^-44: the instruction's number (within 2^-22) after one step
-// of Newton's method; 0 and infinity as it has them.
+// 1 / sqrt(x) within 2^-43: the instruction's number, off by e < 2^-22, after one step of
+// Newton's method, which leaves 1.5 e^2; 0 and infinity as it has them.
 __device__ __forceinline__ double inverse_root(double x) {
   const double r = __builtin_amdgcn_rsq(x);
   const double y = fma(r * 0.5, fma(-x * r, r, 1.0), r);
@@ -229,10 +229,13 @@ __device__ __forceinline__ void normalise(const NormArgs& a, float (&v)[CH][kUni
 //   One unit per thread, against rows of 8192 in 512 threads of two units and 256 of
 // four: 180 / 190 / 194 us (16384 rows), 3.2 / 3.5 / 5.0 (one); rows of 4096 in
 // 512, 1024 (half of them idle) and 256 threads: 91 / 108 / 93.  Two units from 8193
-// values on, four from 16385, whose registers spill (fp32 residual and weights, two
-// LAYER norms, 16384 rows of 32768: 2.7 ms, 3.2 TB/s; bf16 RMS 850 us, 5.0).
+// values on, four from 16385, whose registers spill whatever the types (17 of bf16, 88 of
+// fp32 operands).  2^27 values, bf16 RMS without a norm of the block, in rows of 8192,
+// 16384 and 32768: 180 / 191 / 199 us; fp32 residual and weights, two LAYER norms: 355 /
+// 418 / 529 (1.6 GB, 3.0 TB/s).
 //   A kernel of 64 registers has two workgroups of 16 waves on a CU; 65 had one, and
-// 16384 rows of 8192 with two LAYER norms in fp32 took 481 us instead of 422.
+// 16384 rows of 8192 with two LAYER norms in fp32 took 481 us instead of 422 (two
+// registers spill there).
 // Loading weights before the sums, to have them at hand behind, costs those
 // registers and gained nothing at one row.  Several one-wave rows per workgroup gain
 // nothing either (16384 rows of 512: 12.4 us alone, 12.9 by fours), nor do dwords

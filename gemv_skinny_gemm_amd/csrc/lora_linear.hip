@@ -39,17 +39,22 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // the rows by adapter into blocks of up to 64; with more than 512 a launch between them
 // joins the splits, which otherwise every workgroup of the second sums for its rows.
 // Ordering the whole call counts: blocks of 64 neighbouring rows each with its own
-// adapters read A two and a half times on requests of 40 rows (246 us where 91 are now).
+// adapters read A two and a half times on requests of 40 rows (246 us where 91 were then).
 //
 // What bounds it, measured (in a graph, beside 10240 x 8192 in three slices unless
-// said): one token of rank 16 7.9 us, two launches of 4.1 and 4.9, each a chain of
-// three round trips to memory; 16 requests of ranks to 64 beside 59136 x 8192 35 us, of
+// said): one token of rank 16 8.0 us, two launches of 4.2 and 4.9, each a chain of
+// three round trips to memory; 16 requests of ranks to 64 beside 59136 x 8192 34.7 us, of
 // which 28 the second launch, 83 MB (B's rows are lines of 128 bytes, however much of
-// them an adapter's rank uses) by waves that wait for their one tile; 4099 rows of rank
-// 64, three adapters, 91 us = 6 + 35 + 6 + 46: the last adds to y at 3.7 TB/s, the first
-// product waits for A (2.2 MB for every 64 rows, from the L2 cache).
-//   Whole lines: see Lines; 114 to 92 us on the 4099 rows.  Odd rows of y by dwords:
-// 26 to 21.5 us (251 rows of 2561 columns).  Loads in branches of their own wait for
+// them an adapter's rank uses) by waves that wait for their one tile; 251 rows of which
+// 166 have five of 64 adapters, 1032 -> 2561, 22 us, of which 13 the second launch, whose
+// 88 workgroups are all on one XCD (see skinny_lora_expand); 4099 rows of rank
+// 64, three adapters, 93.5 us = 6 + 35 + 6.5 + 49: the last adds to y at 3.4 TB/s, the
+// first product waits for A (2.2 MB for every 64 rows, from the L2 cache).  4096 rows of
+// rank 128 beside 59136 x 8192 426 us, of which some 355 the second launch, y at 2.7 TB/s
+// beside three parts' matrix instructions; four tiles of ranks per wave of
+// skinny_lora_shrink_many, which gate and up have there, spill 19 registers.
+//   Tried with two parts of A x.  Whole lines: see Lines; 114 to 92 us on the 4099 rows.
+// Odd rows of y by dwords: 26 to 21.5 us (251 rows).  Loads in branches of their own wait for
 // each other; clamped addresses instead: 38 to 31 us (32 adapters of rank 128).  Tried
 // and no faster: blocks of 128 rows (92 us; 30 for 24 on 1024 rows), two tiles of
 // columns per wave (37.4 for 34.3 on the 16 requests), workgroups of 16 waves for few
@@ -936,7 +941,9 @@ void skinny_lora_expand(const LoraArgs a) {
   constexpr int stride = padded / 2 + 4;             // dwords of a row, kept off the same banks
   u32x4* turn = turns[threadIdx.x >> 6];
   // Workgroups go to the eight XCDs in turn; each XCD takes a run of neighbouring
-  // parts of the same rows.
+  // parts of the same rows.  The blocks that have rows come first, before those that the
+  // pool's adapters might have had: a call of few of a large pool's adapters works on few
+  // of the XCDs.
   const int i = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
   const int tiles = a.tile[a.slices];
   const int block = i / tiles;
@@ -984,10 +991,18 @@ struct Cut {
   int splits, pieces, ordinals, most_blocks;
   int chunks, chunk_rows, chunk_blocks;
 };
-constexpr int kFewGroups = 256;        // workgroups to cut a call into, if it is long enough
+// Workgroups of the first product to cut a call into, if it is long enough.  128 to 512 of
+// few rows are within 4% of each other, 1024 takes 19.6 us for 18.2 (16 rows of rank 64) and
+// 34.2 for 31.7 (beside 59136 x 8192); 256 of many rows take 103 us for 92 (4096 of rank 64)
+// and 454 for 425 (rank 128, 59136 x 8192), 1024 what 512 do.
+constexpr int kFewGroups = 256;
 constexpr int kManyGroups = 512;
 constexpr int kChunkRows = 4096;
-constexpr int kJoinRows = 512;         // up to here every workgroup sums its rows' splits itself
+// Up to here every workgroup of the second launch sums its rows' splits itself.  A launch
+// that joins them takes 24.4 us for 21.8 on 251 odd rows of rank 32 and 26.1 for 25.9 on 300
+// of rank 16, 37.4 for 39.9 on 512 of rank 64, 63.5 for 70.9 on 2000.  Where y is wide and
+// ranks are large it gains below, too: 126 for 177 on 512 rows of rank 128 beside 59136 x 8192.
+constexpr int kJoinRows = 512;
 Cut cut_of(const skinny_lora& l, int rows) {
   Cut c{};
   const int blocks = (rows + kRowBlock - 1) / kRowBlock;
