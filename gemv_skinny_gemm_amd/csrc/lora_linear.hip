@@ -1095,10 +1095,7 @@ template <int KS, bool JOINED>
 skinny_status launch_expand(const LoraArgs& a, unsigned grid, hipStream_t stream) {
   constexpr int lds = kParts * staged_rows(KS) * (16 * KS + 4) * (int)sizeof(unsigned);
   constexpr int rest = kRowBlock * (int)sizeof(int) + kWaves * kTurn * (int)sizeof(u32x4);
-  if (lds + rest > 64 * 1024 &&        // more than a launch may have unasked
-      hipFuncSetAttribute((const void*)skinny_lora_expand<KS, JOINED>,
-                          hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
-    return SKINNY_ERR_HIP;
+  static_assert(lds + rest <= 64 * 1024, "more shared memory than a launch may have unasked");
   hipLaunchKernelGGL((skinny_lora_expand<KS, JOINED>), dim3(grid), dim3(kThreads), lds, stream, a);
   return hipGetLastError() == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP;
 }
